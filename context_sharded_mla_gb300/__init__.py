@@ -11,7 +11,9 @@ Functions (same names as the C ABI):
   dcp_count, dcp_slot_map, dcp_kv_append, dcp_mla_decode_partial,
   dcp_mla_decode_workspace_size, dcp_lse_merge, dcp_kv_relayout, dcp_absorb_q,
   dcp_absorb_o, dcp_lse_merge_absorb_o, dcp_a2a_chunk_bytes, dcp_pack_partials,
-  dcp_lse_merge_packed, dcp_lse_rescale
+  dcp_lse_merge_packed, dcp_lse_rescale, dcp_kv_append_q4, dcp_kv_relayout_q4,
+  dcp_kv_read_q4, dcp_mla_decode_partial_q4, dcp_mla_decode_workspace_size_q4,
+  dcp_block_tables
 """
 
 from __future__ import annotations
@@ -29,6 +31,8 @@ __all__ = [
     "dcp_mla_decode_workspace_size", "dcp_lse_merge", "dcp_launch_count", "dcp_kv_relayout",
     "dcp_mla_decode_partial_static", "dcp_mla_decode_static_scratch_bytes", "dcp_absorb_q", "dcp_absorb_o",
     "dcp_a2a_chunk_bytes", "dcp_pack_partials", "dcp_lse_merge_packed", "dcp_lse_rescale", "dcp_lse_merge_absorb_o",
+    "dcp_kv_append_q4", "dcp_kv_relayout_q4", "dcp_kv_read_q4", "dcp_mla_decode_partial_q4",
+    "dcp_mla_decode_workspace_size_q4", "dcp_block_tables", "Q4_ROW_BYTES",
     "DCP_LSE_BASE_E", "DCP_LSE_BASE_2", "DCP_F32", "DCP_BF16", "STATUS_BITS",
 ]
 
@@ -37,7 +41,8 @@ DCP_ERR_TOO_LARGE = -5
 DCP_LSE_BASE_E, DCP_LSE_BASE_2 = 0, 1
 DCP_F32, DCP_BF16 = 0, 1
 STATUS_BITS = {1: "BAD_POSITION", 2: "BAD_PAGE_INDEX", 4: "BAD_PAGE_ID", 8: "BAD_REQUEST", 16: "BAD_LENGTH",
-               32: "TIMEOUT", 64: "INTERNAL"}
+               32: "TIMEOUT", 64: "INTERNAL", 128: "NO_PAGES", 256: "TOO_MANY_TOKENS", 512: "BAD_POOL"}
+Q4_ROW_BYTES = 416   # one latent row of a 4-bit cache
 
 
 class DcpError(RuntimeError):
@@ -83,6 +88,14 @@ _SIGNATURES = {
     "dcp_pack_partials": (_I32, [_I32, _I32, _I32, _I32, _P, _I32, _P, _P, _I32, _P]),
     "dcp_lse_merge_packed": (_I32, [_I32, _I32, _I64, _P, _I32, _I32, _P, _I32, _P, _P]),
     "dcp_lse_rescale": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _I32, _P, _P, _P]),
+    "dcp_kv_append_q4": (_I32, [_LP, _I32, _I32, _P, _P, _P, _I64, _P, _I32, _I64, _I64, _P, _I64, _P, _P]),
+    "dcp_kv_relayout_q4": (_I32, [_LP, _I32, _I32, _P, _I64, _I32, _P, _I64, _I64, _P, _P, _I64, _I32, _P, _I64, _I64,
+                                  _P, _I64, _P, _P]),
+    "dcp_kv_read_q4": (_I32, [_LP, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I64, _I64, _P, _P, _P]),
+    "dcp_mla_decode_partial_q4": (_I32, [_LP, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _P, _I64, _I64,
+                                         _P, _F, _I32, _P, _I32, _P, _P, _SZ, _P, _P]),
+    "dcp_mla_decode_workspace_size_q4": (_SZ, [_LP, _I32, _I32, _I32, _I32, _I32]),
+    "dcp_block_tables": (_I32, [_LP, _I32, _P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -444,3 +457,136 @@ def dcp_lse_rescale(lse_all, o_part, shard_begin, world, lse_base, o_sum, lse=No
     _check("dcp_lse_rescale", load_library().dcp_lse_rescale(
         n_shards, shard_begin, n_held, T, H, world, _ptr(lse_all), _ptr(o_part), _dtype_code(o_part), lse_base,
         _ptr(o_sum), _ptr(lse), _stream(stream)))
+
+
+def _here(*tensors):
+    """The tensors lie on the current device (the one the library launches on)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor lies on {t.device}, but the current device is cuda:{dev}")
+
+
+def _tokens(pos, req, block_table):
+    T = pos.numel()
+    _dev(pos, "pos", torch.int64, (T,))
+    _dev(req, "req", torch.int32, (T,))
+    _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max pages]")
+    return T
+
+
+def _arena_q4(layout, shard_begin, shard_end, arena, pool_pages):
+    _dev(arena, "arena", torch.uint8, (shard_end - shard_begin, pool_pages * layout.page_size, Q4_ROW_BYTES))
+
+
+def dcp_kv_append_q4(layout, shard_begin, shard_end, kv_new, pos, req, block_table, max_pages, arena, pool_pages,
+                     status, stream=None):
+    """Owner-filtered write of kv_new [T, 576] bf16 into a 4-bit arena [shards, pool_pages*P, 416] uint8;
+    entries with pos = req = -1 are padding."""
+    T = _tokens(pos, req, block_table)
+    _dev(kv_new, "kv_new", torch.bfloat16, (T, 576))
+    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
+    _dev(status, "status", torch.int32, (1,))
+    _here(kv_new, pos, req, block_table, arena, status)
+    B, stride = block_table.shape
+    _check("dcp_kv_append_q4", load_library().dcp_kv_append_q4(
+        ctypes.byref(layout), shard_begin, shard_end, _ptr(kv_new), _ptr(pos), _ptr(req), T, _ptr(block_table),
+        B, stride, max_pages, _ptr(arena), pool_pages, _ptr(status), _stream(stream)))
+
+
+def dcp_kv_relayout_q4(layout, shard_begin, shard_end, src_pool, src_page_size, src_block_table, src_max_pages,
+                       pos, req, block_table, max_pages, arena, pool_pages, status, stream=None):
+    """Owner-filtered copy of tokens (pos, req) from a paged bf16 prefill pool [rows, 576] into a 4-bit arena."""
+    T = _tokens(pos, req, block_table)
+    _dev(src_pool, "src_pool", torch.bfloat16)
+    if src_pool.dim() != 2 or src_pool.shape[1] != 576:
+        raise ValueError("src_pool must be [rows, 576]")
+    _dev(src_block_table, "src_block_table", torch.int32)
+    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
+    _dev(status, "status", torch.int32, (1,))
+    B, stride = block_table.shape
+    if src_block_table.dim() != 2 or src_block_table.shape[0] != B:
+        raise ValueError("src_block_table and block_table must have one row per request")
+    _here(src_pool, src_block_table, pos, req, block_table, arena, status)
+    _check("dcp_kv_relayout_q4", load_library().dcp_kv_relayout_q4(
+        ctypes.byref(layout), shard_begin, shard_end, _ptr(src_pool), src_pool.shape[0], src_page_size,
+        _ptr(src_block_table), src_block_table.shape[1], src_max_pages, _ptr(pos), _ptr(req), T, B,
+        _ptr(block_table), stride, max_pages, _ptr(arena), pool_pages, _ptr(status), _stream(stream)))
+
+
+def dcp_kv_read_q4(layout, shard_begin, shard_end, arena, pool_pages, pos, req, block_table, max_pages, kv, status,
+                   stream=None):
+    """kv [T, 576] bf16: the values a 4-bit arena holds for tokens (pos, req); rows of tokens that are not held
+    (other shards', padding) are left as they were."""
+    T = _tokens(pos, req, block_table)
+    _dev(kv, "kv", torch.bfloat16, (T, 576))
+    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
+    _dev(status, "status", torch.int32, (1,))
+    _here(arena, pos, req, block_table, kv, status)
+    B, stride = block_table.shape
+    _check("dcp_kv_read_q4", load_library().dcp_kv_read_q4(
+        ctypes.byref(layout), shard_begin, shard_end, _ptr(arena), pool_pages, _ptr(pos), _ptr(req), T,
+        _ptr(block_table), B, stride, max_pages, _ptr(kv), _ptr(status), _stream(stream)))
+
+
+def dcp_mla_decode_workspace_size_q4(layout, shard_begin, shard_end, B, q_len, H) -> int:
+    return int(load_library().dcp_mla_decode_workspace_size_q4(
+        ctypes.byref(layout), shard_begin, shard_end, B, q_len, H))
+
+
+def dcp_mla_decode_partial_q4(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages,
+                              seq_lens, scale, lse_base, o_part, lse_part, workspace, status, stream=None):
+    """dcp_mla_decode_partial over a 4-bit arena [shards, pool_pages*P, 416] uint8."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, q_len, H, 576]")
+    B, q_len, H, _ = q.shape
+    n = shard_end - shard_begin
+    _dev(q, "q", torch.bfloat16, (B, q_len, H, 576))
+    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int64, (B,))
+    _dev(o_part, "o_part", o_part.dtype, (n, B, q_len, H, 512))
+    _dev(lse_part, "lse_part", torch.float32, (n, B, q_len, H))
+    _dev(status, "status", torch.int32, (1,))
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+        ws_ptr, ws_bytes = _ptr(workspace), workspace.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per request")
+    _here(q, arena, block_table, seq_lens, o_part, lse_part, workspace, status)
+    _check("dcp_mla_decode_partial_q4", load_library().dcp_mla_decode_partial_q4(
+        ctypes.byref(layout), shard_begin, shard_end, _ptr(q), B, q_len, H, _ptr(arena), pool_pages,
+        _ptr(block_table), block_table.shape[1], max_pages, _ptr(seq_lens), float(scale), lse_base,
+        _ptr(o_part), _dtype_code(o_part), _ptr(lse_part), ws_ptr, ws_bytes, _ptr(status), _stream(stream)))
+
+
+def dcp_block_tables(layout, seq_lens, new_lens, block_table, max_pages, free_pages, free_state, cu_tokens, status,
+                     pos=None, req=None, owner=None, row=None, slot=None, stream=None):
+    """Moves the requests from seq_lens to new_lens (int64 [B], seq_lens updated): takes pages from and gives them
+    back to the ring free_pages (int32 [pool pages], free_state int64 {head, count}), updates block_table, and lists
+    the new tokens in pos / req (and owner / row / slot), cu_tokens int64 [B + 1]."""
+    _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max pages]")
+    B, stride = block_table.shape
+    _dev(seq_lens, "seq_lens", torch.int64, (B,))
+    _dev(new_lens, "new_lens", torch.int64, (B,))
+    _dev(free_pages, "free_pages", torch.int32)
+    _dev(free_state, "free_state", torch.int64, (2,))
+    _dev(cu_tokens, "cu_tokens", torch.int64, (B + 1,))
+    _dev(status, "status", torch.int32, (1,))
+    T = 0 if pos is None else pos.numel()
+    for t, name, dtype in ((pos, "pos", torch.int64), (req, "req", torch.int32), (owner, "owner", torch.int32),
+                           (row, "row", torch.int64), (slot, "slot", torch.int64)):
+        if t is not None:
+            _dev(t, name, dtype, (T,))
+    if T == 0 and pos is not None:
+        raise ValueError("pos is empty: leave the token arrays out to list no tokens")
+    _here(seq_lens, new_lens, block_table, free_pages, free_state, cu_tokens, status, pos, req, owner, row, slot)
+    _check("dcp_block_tables", load_library().dcp_block_tables(
+        ctypes.byref(layout), B, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), stride, max_pages,
+        _ptr(free_pages), _ptr(free_state), free_pages.numel(), T, _ptr(pos), _ptr(req), _ptr(owner), _ptr(row),
+        _ptr(slot), _ptr(cu_tokens), _ptr(status), _stream(stream)))

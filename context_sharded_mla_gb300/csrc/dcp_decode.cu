@@ -52,6 +52,19 @@
 // range boundaries leaves normalised pieces (o, lse in base 2) in the workspace
 // which a second kernel merges with the same LSE rule.  A tiny kernel run first
 // writes the tile prefix sums.
+//
+// The same kernel reads a cache held in 4 bits (kQ4; the row format is in
+// dcp_internal.cuh).  Its TMA producer then loads only the rope dims, and four
+// more warps, 12-15, turn the codes of the value chunks into the bf16 tiles the
+// products read:
+//   value of dim d = code * scale of its 16-dim group: 3 bits times an e4m3's 4
+//   significant bits, exact in bf16, so the products see the cached value itself.
+//   A code arrives as n = code + 8 in 4 bits.  (n | 0x4300) is the bf16 128 + n,
+//   and one fma with the scale s and -136 s gives (n - 8) s in a single rounding
+//   that has nothing to round: two dims per instruction.
+// Warp 12 + w takes rows [16 w, 16 w + 16) of each tile: its loads of tile j + 1
+// are in flight while it writes tile j.  The producer prefetches whole 416-byte
+// rows into L2, so those loads find them there.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -85,6 +98,10 @@ constexpr int kHalfRows = 16;                 // rows served by one softmax warp
 constexpr int kProducerWarp = 10;
 constexpr int kMmaWarp = 11;                  // QK issuer and TMEM owner
 constexpr int kPvWarp = 9;                    // PV issuer
+constexpr int kDequantWarp0 = 12;             // 4-bit cache: warps 12-15 write the tiles' value chunks
+constexpr int kDequantWarps = 4;
+constexpr int kDequantRows = kTile / kDequantWarps;
+constexpr int threads_of(bool q4) { return kThreads + (q4 ? 32 * kDequantWarps : 0); }
 constexpr int kMaxGroupRows = 128;
 constexpr int64_t kMaxQueryRows = 65536;      // q_len * H per request (512 row groups)
 constexpr uint32_t kOCol = 0;                 // TMEM columns [0, 256): O, rows on lanes
@@ -105,6 +122,7 @@ struct TcArgs {
   int32_t nts;                   // tile slots in the ring
   int32_t box_rows;              // KV TMA box height = min(P, 64)
   int64_t pool_rows, pool_pages;
+  const unsigned char* arena_q4;  // 4-bit cache rows (null for a bf16 cache)
   const int32_t* bt;
   int64_t bt_stride, max_pages;
   const int64_t* seq_lens;
@@ -421,7 +439,8 @@ __device__ __noinline__ void store_o_rows(const TcArgs& a, uint32_t o_addr, int 
 // sequence; the score exchange is double-buffered and S tiles are released as
 // soon as they have been read, so QK products run up to two tiles ahead of the
 // softmax while the exchange is in flight.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool kQ4>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kQ4), 1)
     partial_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
                       const __grid_constant__ CUtensorMap tmap_q64, const __grid_constant__ CUtensorMap tmap_kv64,
                       const __grid_constant__ CUtensorMap tmap_kv4, TcArgs a) {
@@ -476,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // The score exchange runs as one channel per softmax warp (its 16 rows), with
     // one single-arrival "landed" barrier per buffer and channel.
     for (int i = 0; i < nts; ++i) {
-      mbar_init(&tfull[i], 1);
+      mbar_init(&tfull[i], kQ4 ? 1 + kDequantWarps : 1);
       mbar_init(&tempty[i], 1);
     }
     fence_barrier_init();
@@ -487,9 +506,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&bars[kXFull + 8 * ((j & 1) ^ 1) + w], kHalfRows * kXRowBytes);
   }
   // rows of a page past a request's length are read with zero weight: start from finite zeros
-  for (int i = tid; i < nts * kSlotBytes / 16; i += kThreads) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < nts * kSlotBytes / 16; i += threads_of(kQ4)) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
   // query rows past the group are read by the M = 128 products: zeros
-  for (int i = tid; i < (int)(sl.x / 16); i += kThreads) reinterpret_cast<uint4*>(qc_s)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (int)(sl.x / 16); i += threads_of(kQ4)) reinterpret_cast<uint4*>(qc_s)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_base_s, 512);
@@ -509,10 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lo < hi) {
       if (lane == 0) {
         prefetch_tmap(&tmap_q);
-        prefetch_tmap(&tmap_kv);
         prefetch_tmap(&tmap_q64);
         prefetch_tmap(&tmap_kv64);
-        prefetch_tmap(&tmap_kv4);
+        if constexpr (!kQ4) {
+          prefetch_tmap(&tmap_kv);
+          prefetch_tmap(&tmap_kv4);
+        }
       }
       SegIter it;
       it.init(a.tile_start, U, lo, hi);
@@ -544,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int32_t rho = rho0 + q * a.box_rows;
           if (tile < tile_end && q < nbox && rho < nvis) {
             const int32_t pidx = rho / a.L.P;
-            pg[q] = pidx < a.max_pages ? __ldg(a.bt + (int64_t)b * a.bt_stride + pidx) : -1;
+            pg[q] = pidx >= 0 && pidx < a.max_pages ? __ldg(a.bt + (int64_t)b * a.bt_stride + pidx) : -1;
           }
         }
       };
@@ -603,7 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // this CTA's 32 rope dims of the tile: rows of 64 bytes, 64-byte swizzle
       auto issue_rope = [&](const Boxes& bx, unsigned char* dst, uint64_t* bar) {
-        const int32_t x = 2 * kOwnChunks * kChunkDims + kRopeHalf * (int)rank;
+        // (a 4-bit cache's rope map starts at the rope dims)
+        const int32_t x = (kQ4 ? 0 : 2 * kOwnChunks * kChunkDims) + kRopeHalf * (int)rank;
         if (nbox == 1) {
           if (bx.y[0] >= 0) tma_load_2d(dst, &tmap_kv64, bar, x, bx.y[0]);
         } else {
@@ -617,9 +639,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto load_tile = [&](const Boxes& bx) -> bool {
         if (!warp_wait(&tempty[ts], tphase ^ 1, abort_s, lane)) return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&tfull[ts], bx.bytes * kOwnChunks + bx.bytes / 2);
+          mbar_arrive_expect_tx(&tfull[ts], (kQ4 ? 0 : bx.bytes * kOwnChunks) + bx.bytes / 2);
           unsigned char* dst = ring + ts * kSlotBytes;
-          if (nbox == 1) {
+          if (kQ4) {
+            // the value chunks come from the dequantising warps
+          } else if (nbox == 1) {
             // all four value chunks of the tile with one 3-D box: [4 chunks][64 rows][128 B]
             if (bx.y[0] >= 0) tma_load_3d(dst, &tmap_kv4, &tfull[ts], 0, bx.y[0], kOwnChunks * (int)rank);
           } else {
@@ -634,6 +658,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tphase ^= 1;
         }
         return true;
+      };
+      // this CTA's share of the tile whose rows start at pool row y, into L2
+      auto prefetch_tile = [&](int32_t y) {
+        if constexpr (kQ4) {  // half of its rows, whole
+          bulk_prefetch_l2(a.arena_q4 + (int64_t)(y + kTile / 2 * (int)rank) * kQ4RowBytes, kTile / 2 * kQ4RowBytes);
+        } else {
+          tma_prefetch_3d(&tmap_kv4, 0, y, kOwnChunks * (int)rank);
+          tma_prefetch_2d(&tmap_kv64, 2 * kOwnChunks * kChunkDims + kRopeHalf * (int)rank, y);
+        }
       };
       // A segment's length and the page ids of its first 32 tiles are loaded
       // during the segment before it, so that a segment start waits on no
@@ -694,10 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // tile jj + kL2Ahead into L2, so that its ring load finds it there
             const int32_t ja = jj + kL2Ahead;
             const int32_t ya = __shfl_sync(0xffffffffu, (ja & 31) > (jj & 31) ? yc[0] : yn, ja & 31);
-            if (lane == 0 && ja < nt && ya >= 0) {
-              tma_prefetch_3d(&tmap_kv4, 0, ya, kOwnChunks * (int)rank);
-              tma_prefetch_2d(&tmap_kv64, 2 * kOwnChunks * kChunkDims + kRopeHalf * (int)rank, ya);
-            }
+            if (lane == 0 && ja < nt && ya >= 0) prefetch_tile(ya);
             // past this segment's end: the next segment's first tiles
             if (ja >= nt && has_next && ja - nt < nt2 && ja - nt < 32) {
               if (!next_rows) {
@@ -707,10 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 next_rows = true;
               }
               const int32_t yb = __shfl_sync(0xffffffffu, y_next, ja - nt);
-              if (lane == 0 && yb >= 0) {
-                tma_prefetch_3d(&tmap_kv4, 0, yb, kOwnChunks * (int)rank);
-                tma_prefetch_2d(&tmap_kv64, 2 * kOwnChunks * kChunkDims + kRopeHalf * (int)rank, yb);
-              }
+              if (lane == 0 && yb >= 0) prefetch_tile(yb);
             }
           }
           Boxes cur;
@@ -743,6 +770,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (uint32_t s = 0; s < (uint32_t)nts && s < ntiles_cta; ++s) {
           const uint32_t last = s + ((ntiles_cta - 1 - s) / nts) * nts;  // last tile in slot s
           if (!warp_wait(&tempty[s], (last / nts) & 1, abort_s, lane)) break;
+        }
+      }
+    }
+  } else if (kQ4 && warp >= kDequantWarp0) {
+    // ------------------------------------------------------------------ 4-bit rows -> bf16 tiles
+    // Lane l serves row l % 8 of each of the warp's two 8-row groups (a group
+    // never crosses a page) and the 32-dim pieces l / 8 and l / 8 + 4 of this
+    // CTA's 256 dims: a load instruction reads 64 contiguous bytes of 8 rows,
+    // and the 8 lanes of a store phase write the 8 swizzled 16-byte slots.
+    if (lo < hi) {
+      const int w = warp - kDequantWarp0;
+      const int r8 = lane & 7, pc = lane >> 3;
+      const int32_t ntile = (int32_t)ntiles_cta;
+      struct Rows {
+        uint4 code[2][2];
+        uint32_t scale[2][2];
+      };
+      SegIter it;
+      it.init(a.tile_start, U, lo, hi);
+      int32_t u = 0, t0 = 0, nt = 0, kslot = 0;
+      bool whole = false;
+      int32_t jj = 0;               // next tile of the segment to load
+      int rs = 0, b = 0;
+      int64_t nvis = 0;
+      int32_t y8[2] = {-1, -1};     // lane l: first pool rows of the groups of tile (batch + l), -1: none
+      // loads the next tile of the range (a row past the length or on a bad page
+      // gets scale 0, so it is written as zeros)
+      auto load = [&](Rows& x) {
+        if (jj == nt) {
+          it.next(&u, &t0, &nt, &whole, &kslot);
+          jj = 0;
+          b = u / a.n_held;
+          rs = u % a.n_held;
+          bool bad = false;
+          nvis = unit_nvis_max(a, b, rs, &bad);
+        }
+        if ((jj & 31) == 0) {
+#pragma unroll
+          for (int g8 = 0; g8 < 2; ++g8) {
+            const int32_t rho = (t0 + jj + lane) * kTile + kDequantRows * w + 8 * g8;
+            y8[g8] = -1;
+            if (jj + lane < nt && rho < nvis) {
+              const int32_t pidx = rho / a.L.P;
+              const int32_t page =
+                  pidx >= 0 && pidx < a.max_pages ? __ldg(a.bt + (int64_t)b * a.bt_stride + pidx) : -1;
+              if (page >= 0 && page < a.pool_pages)
+                y8[g8] = rs * (int32_t)a.pool_rows + page * (int32_t)a.L.P + rho % (int32_t)a.L.P;
+            }
+          }
+        }
+#pragma unroll
+        for (int g8 = 0; g8 < 2; ++g8) {
+          const int32_t y = __shfl_sync(0xffffffffu, y8[g8], jj & 31);
+          const int64_t rho = (int64_t)(t0 + jj) * kTile + kDequantRows * w + 8 * g8 + r8;
+          const bool ok = y >= 0 && rho < nvis;
+          const unsigned char* row = a.arena_q4 + (int64_t)(ok ? y + r8 : 0) * kQ4RowBytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int piece = 8 * (int)rank + pc + 4 * i;
+            x.code[g8][i] = ok ? __ldg(reinterpret_cast<const uint4*>(row) + piece) : make_uint4(0, 0, 0, 0);
+            x.scale[g8][i] = ok ? __ldg(reinterpret_cast<const uint16_t*>(row + kQ4ScaleOff) + piece) : 0u;
+          }
+        }
+        ++jj;
+      };
+      auto write = [&](const Rows& x, uint32_t slot) {
+#pragma unroll
+        for (int g8 = 0; g8 < 2; ++g8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int piece = pc + 4 * i;  // of this CTA's 8
+            const uint32_t dst =
+                slot + (uint32_t)(piece >> 1) * kChunkBytes + (uint32_t)(kDequantRows * w + 8 * g8 + r8) * 128;
+            uint32_t s2[2];
+            q4_scales(x.scale[g8][i], s2);
+            const uint32_t wd[4] = {x.code[g8][i].x, x.code[g8][i].y, x.code[g8][i].z, x.code[g8][i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t v[4];
+              q4_values(wd[k], s2[k >> 1], v);
+              st_shared_v4(dst + (uint32_t)((4 * (piece & 1) + k) ^ r8) * 16, v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+      };
+      Rows cur, nxt;
+      load(cur);
+      uint32_t ts = 0, tphase = 0;
+      for (int32_t j = 0; j < ntile; ++j) {
+        if (j + 1 < ntile) load(nxt);
+        if (!warp_wait(&tempty[ts], tphase ^ 1, abort_s, lane)) break;
+        write(cur, smem_u32(ring) + ts * kSlotBytes);
+        fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tfull[ts]);
+        cur = nxt;
+        if (++ts == (uint32_t)nts) {
+          ts = 0;
+          tphase ^= 1;
         }
       }
     }
@@ -1247,33 +1373,44 @@ int sm_count_current() {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-SmemLimit g_partial_smem;  // partial_tc_kernel's dynamic shared-memory limit, per device
+// partial_tc_kernel's dynamic shared-memory limit, per cache format and device
+SmemLimit g_partial_smem[2];
+
+using PartialKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                               const CUtensorMap, TcArgs);
+PartialKernel partial_kernel(bool q4) { return q4 ? partial_tc_kernel<true> : partial_tc_kernel<false>; }
+
+bool ensure_partial_smem(bool q4, size_t smem) {
+  return g_partial_smem[q4].ensure(reinterpret_cast<const void*>(partial_kernel(q4)), smem);
+}
 
 // Resident 2-CTA clusters of partial_tc_kernel at `smem` bytes on the current
-// device.  Cached per device and shared-memory size (a workload uses one or two
-// sizes); guarded by a mutex, since one host thread per GPU may plan at once.
-int max_active_clusters(size_t smem) {
+// device.  Cached per device, cache format and shared-memory size (a workload
+// uses one or two sizes); guarded by a mutex, since one host thread per GPU may
+// plan at once.
+int max_active_clusters(size_t smem, bool q4) {
   constexpr int kEntries = 8;
   struct Entry {
     size_t smem;
     int clusters;
   };
   static std::mutex m;
-  static Entry cache[kMaxDevices][kEntries] = {};
+  static Entry caches[2][kMaxDevices][kEntries] = {};
   const int dev = current_device();
   if (dev < 0) return 0;
+  auto& cache = caches[q4];
   {
     std::lock_guard<std::mutex> lock(m);
     for (const Entry& e : cache[dev])
       if (e.smem == smem && e.clusters > 0) return e.clusters;
   }
-  if (!g_partial_smem.ensure(reinterpret_cast<const void*>(&partial_tc_kernel), smem)) return 0;
+  if (!ensure_partial_smem(q4, smem)) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 512, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads_of(q4), 1, 1);
   cfg.dynamicSmemBytes = smem;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, partial_tc_kernel, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, partial_kernel(q4), &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1290,7 +1427,7 @@ int max_active_clusters(size_t smem) {
   return n;
 }
 
-bool make_plan(const dcp_layout_t* layout, int n_held, int B, int q_len, int H, Plan* p) {
+bool make_plan(const dcp_layout_t* layout, int n_held, int B, int q_len, int H, bool q4, Plan* p) {
   const int R_total = q_len * H;
   p->ngroups = (R_total + kMaxGroupRows - 1) / kMaxGroupRows;
   const int per = (R_total + p->ngroups - 1) / p->ngroups;
@@ -1306,7 +1443,7 @@ bool make_plan(const dcp_layout_t* layout, int n_held, int B, int q_len, int H, 
   p->nts = nts;
   p->smem = smem_layout(p->Rg, nts).total;
   // clusters that can be resident at once (both CTAs of a cluster share a GPC)
-  const int clusters = max_active_clusters(p->smem);
+  const int clusters = max_active_clusters(p->smem, q4);
   if (clusters > 0) {
     // V ranges per row group.  One wave of V0 = clusters / ngroups ranges is the
     // default; when that leaves many clusters idle (ngroups not much below the
@@ -1362,21 +1499,35 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_row
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the bf16 rope dims of 4-bit rows: boxes of [box_rows, 32] with 64-byte swizzle
+bool make_tmap_q4_rope(CUtensorMap* m, const void* arena, uint64_t rows, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)(kDk - kDv), (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kQ4RowBytes};
+  cuuint32_t box[2] = {(cuuint32_t)kRopeHalf, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  void* base = const_cast<unsigned char*>(static_cast<const unsigned char*>(arena)) + kQ4RopeOff;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 bool page_size_ok(int P) { return P >= 8 && P % 8 == 0 && (P % kTile == 0 || kTile % P == 0); }
 
 }  // namespace
 
-extern "C" size_t dcp_mla_decode_workspace_size(const dcp_layout_t* layout, int32_t shard_begin,
-                                                int32_t shard_end, int32_t B, int32_t q_len, int32_t H) {
+namespace {
+
+size_t workspace_size(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, int32_t B, int32_t q_len,
+                      int32_t H, bool q4) {
   if (!layout_ok(layout) || shard_begin < 0 || shard_end > layout->n_shards || shard_begin >= shard_end ||
       B < 1 || q_len < 1 || H < 1 || (int64_t)q_len * H > kMaxQueryRows)
     return 0;
   Plan p;
-  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, &p)) return 0;
+  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, q4, &p)) return 0;
   return p.ws_total;
 }
-
-namespace {
 
 // Host checks of dcp_mla_decode_partial's arguments (all but the workspace).
 int32_t check_decode_args(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
@@ -1409,16 +1560,21 @@ int32_t launch_decode(const Plan& p, const dcp_layout_t* layout, int32_t shard_b
                       const void* q, int32_t B, int32_t q_len, int32_t H, const void* arena, int64_t pool_pages,
                       const int32_t* block_table, int64_t bt_stride, int64_t max_pages, const int64_t* seq_lens,
                       float scale, int32_t lse_base, void* o_part, int32_t o_part_dtype, float* lse_part,
-                      void* workspace, int32_t* status, void* stream) {
+                      void* workspace, int32_t* status, void* stream, bool q4) {
   const int n_held = shard_end - shard_begin;
   const int64_t pool_rows = pool_pages * layout->page_size;
-  CUtensorMap tq, tkv, tq64, tkv64, tkv4;
+  CUtensorMap tq, tkv = {}, tq64, tkv64, tkv4 = {};
   if (!make_tmap(&tq, q, (uint64_t)B * q_len * H, (uint32_t)p.Rg)) return DCP_ERR_CUDA;
-  if (!make_tmap(&tkv, arena, (uint64_t)n_held * pool_rows, (uint32_t)p.box_rows)) return DCP_ERR_CUDA;
   if (!make_tmap(&tq64, q, (uint64_t)B * q_len * H, (uint32_t)p.Rg, true)) return DCP_ERR_CUDA;
-  if (!make_tmap(&tkv64, arena, (uint64_t)n_held * pool_rows, (uint32_t)p.box_rows, true)) return DCP_ERR_CUDA;
-  if (!make_tmap_chunks(&tkv4, arena, (uint64_t)n_held * pool_rows, (uint32_t)p.box_rows)) return DCP_ERR_CUDA;
-  if (!g_partial_smem.ensure(reinterpret_cast<const void*>(&partial_tc_kernel), p.smem)) return DCP_ERR_CUDA;
+  const uint64_t arena_rows = (uint64_t)n_held * pool_rows;
+  if (q4) {
+    if (!make_tmap_q4_rope(&tkv64, arena, arena_rows, (uint32_t)p.box_rows)) return DCP_ERR_CUDA;
+  } else {
+    if (!make_tmap(&tkv, arena, arena_rows, (uint32_t)p.box_rows)) return DCP_ERR_CUDA;
+    if (!make_tmap(&tkv64, arena, arena_rows, (uint32_t)p.box_rows, true)) return DCP_ERR_CUDA;
+    if (!make_tmap_chunks(&tkv4, arena, arena_rows, (uint32_t)p.box_rows)) return DCP_ERR_CUDA;
+  }
+  if (!ensure_partial_smem(q4, p.smem)) return DCP_ERR_CUDA;
 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   TcArgs a;
@@ -1429,6 +1585,7 @@ int32_t launch_decode(const Plan& p, const dcp_layout_t* layout, int32_t shard_b
   a.Rg = p.Rg; a.ngroups = p.ngroups; a.V = p.V; a.nts = p.nts; a.box_rows = p.box_rows;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.pool_rows = pool_rows; a.pool_pages = pool_pages;
+  a.arena_q4 = q4 ? static_cast<const unsigned char*>(arena) : nullptr;
   a.bt = block_table; a.bt_stride = bt_stride; a.max_pages = max_pages;
   a.seq_lens = seq_lens;
   a.scale_log2 = scale * kLog2e;
@@ -1450,12 +1607,12 @@ int32_t launch_decode(const Plan& p, const dcp_layout_t* layout, int32_t shard_b
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(2 * p.V * p.ngroups));
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(threads_of(q4));
   lc.dynamicSmemBytes = p.smem;
   lc.stream = st;
   lc.attrs = pdl;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, partial_tc_kernel, tq, tkv, tq64, tkv64, tkv4, a) != cudaSuccess) return DCP_ERR_CUDA;
+  if (cudaLaunchKernelEx(&lc, partial_kernel(q4), tq, tkv, tq64, tkv64, tkv4, a) != cudaSuccess) return DCP_ERR_CUDA;
   // Cut units need their pieces merged: one block column per range boundary,
   // one warp per row up to 96 rows, blocks looping over further row chunks.
   // With one range per row group nothing is cut and no fixup runs.
@@ -1473,7 +1630,35 @@ int32_t launch_decode(const Plan& p, const dcp_layout_t* layout, int32_t shard_b
   return launch_status(2);
 }
 
+int32_t decode_partial(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q, int32_t B,
+                       int32_t q_len, int32_t H, const void* arena, int64_t pool_pages, const int32_t* block_table,
+                       int64_t bt_stride, int64_t max_pages, const int64_t* seq_lens, float scale, int32_t lse_base,
+                       void* o_part, int32_t o_part_dtype, float* lse_part, void* workspace, size_t workspace_bytes,
+                       int32_t* status, void* stream, bool q4) {
+  const int32_t rc = check_decode_args(layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages,
+                                       block_table, bt_stride, max_pages, seq_lens, scale, lse_base, o_part,
+                                       o_part_dtype, lse_part);
+  if (rc != DCP_OK) return rc;
+  Plan p;
+  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, q4, &p)) return DCP_ERR_CUDA;
+  if (!workspace || workspace_bytes < p.ws_total) return DCP_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return DCP_ERR_INVALID;
+  return launch_decode(p, layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
+                       max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, workspace, status,
+                       stream, q4);
+}
+
 }  // namespace
+
+extern "C" size_t dcp_mla_decode_workspace_size(const dcp_layout_t* layout, int32_t shard_begin,
+                                                int32_t shard_end, int32_t B, int32_t q_len, int32_t H) {
+  return workspace_size(layout, shard_begin, shard_end, B, q_len, H, false);
+}
+
+extern "C" size_t dcp_mla_decode_workspace_size_q4(const dcp_layout_t* layout, int32_t shard_begin,
+                                                   int32_t shard_end, int32_t B, int32_t q_len, int32_t H) {
+  return workspace_size(layout, shard_begin, shard_end, B, q_len, H, true);
+}
 
 extern "C" int32_t dcp_mla_decode_partial(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                           const void* q, int32_t B, int32_t q_len, int32_t H,
@@ -1483,17 +1668,22 @@ extern "C" int32_t dcp_mla_decode_partial(const dcp_layout_t* layout, int32_t sh
                                           void* o_part, int32_t o_part_dtype, float* lse_part,
                                           void* workspace, size_t workspace_bytes,
                                           int32_t* status, void* stream) {
-  const int32_t rc = check_decode_args(layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages,
-                                       block_table, bt_stride, max_pages, seq_lens, scale, lse_base, o_part,
-                                       o_part_dtype, lse_part);
-  if (rc != DCP_OK) return rc;
-  Plan p;
-  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, &p)) return DCP_ERR_CUDA;
-  if (!workspace || workspace_bytes < p.ws_total) return DCP_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) & 255) return DCP_ERR_INVALID;
-  return launch_decode(p, layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
-                       max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, workspace, status,
-                       stream);
+  return decode_partial(layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
+                        max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, workspace,
+                        workspace_bytes, status, stream, false);
+}
+
+extern "C" int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                                             const void* q, int32_t B, int32_t q_len, int32_t H,
+                                             const void* arena, int64_t pool_pages,
+                                             const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                                             const int64_t* seq_lens, float scale, int32_t lse_base,
+                                             void* o_part, int32_t o_part_dtype, float* lse_part,
+                                             void* workspace, size_t workspace_bytes,
+                                             int32_t* status, void* stream) {
+  return decode_partial(layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
+                        max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, workspace,
+                        workspace_bytes, status, stream, true);
 }
 
 // ---------------------------------------------------------------------------- allocation-free variant
@@ -1541,10 +1731,10 @@ extern "C" int32_t dcp_mla_decode_partial_static(const dcp_layout_t* layout, int
                                        o_part_dtype, lse_part);
   if (rc != DCP_OK) return rc;
   Plan p;
-  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, &p)) return DCP_ERR_CUDA;
+  if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, false, &p)) return DCP_ERR_CUDA;
   if (p.ws_total > kStaticScratchBytes) return DCP_ERR_TOO_LARGE;
   void* ws = scratch_address();
   if (!ws) return DCP_ERR_CUDA;
   return launch_decode(p, layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
-                       max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, ws, status, stream);
+                       max_pages, seq_lens, scale, lse_base, o_part, o_part_dtype, lse_part, ws, status, stream, false);
 }

@@ -10,6 +10,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -124,6 +126,46 @@ __device__ inline void store16(void* row, int lane, const float (&v)[16]) {
       p[2 * lane + 64 * j] = make_float4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
       p[2 * lane + 64 * j + 1] = make_float4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
     }
+  }
+}
+
+// ---------------------------------------------------------------- 4-bit cache rows
+// A latent row in 4 bits, 416 bytes (include/dcp.h, "4-bit latent cache"):
+// 64 32-bit words of codes, 32 e4m3 scales (one per 16 dims), 64 bf16 dims.
+// Word k holds dims 8k .. 8k + 7, each as n = code + 8: dim 8k + 2i in bits
+// [4i, 4i + 4), dim 8k + 2i + 1 in bits [16 + 4i, 20 + 4i), so that one shift
+// and mask leaves an adjacent pair of dims in the two halves of a register.
+constexpr int kQ4Group = 16;
+constexpr int kQ4ScaleOff = kDv / 2;                        // 256
+constexpr int kQ4RopeOff = kQ4ScaleOff + kDv / kQ4Group;    // 288
+constexpr int kQ4RowBytes = kQ4RopeOff + (kDk - kDv) * 2;   // 416
+
+// Two e4m3 scales (low byte first) as floats; a NaN stays one.
+__device__ __forceinline__ float2 q4_scales_f32(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The same two scales, each as a bf16 pair (an e4m3's 4 significant bits fit).
+__device__ __forceinline__ void q4_scales(uint32_t two, uint32_t (&s2)[2]) {
+  const float2 f = q4_scales_f32(two);
+  const __nv_bfloat162 a = __float2bfloat162_rn(f.x), b = __float2bfloat162_rn(f.y);
+  s2[0] = *reinterpret_cast<const uint32_t*>(&a);
+  s2[1] = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The 8 values of one word of codes, as bf16 pairs in dim order.  With n in the
+// low mantissa bits of a bf16 of exponent 7, (n | 0x4300) = 128 + n, and
+// (128 + n) s - 136 s = (n - 8) s.  136 s = 17 * 8 s has at most 4 + 4
+// significant bits and (n - 8) s at most 7, so neither product is rounded.
+__device__ __forceinline__ void q4_values(uint32_t word, uint32_t s2, uint32_t (&v)[4]) {
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+  const __nv_bfloat162 off = __hmul2(s, __float2bfloat162_rn(-136.f));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&n), s, off);
+    v[i] = *reinterpret_cast<const uint32_t*>(&r);
   }
 }
 

@@ -142,11 +142,11 @@ class DcpGroupDecoder:
     def __init__(self, layout: Layout, B: int, q_len: int, H: int, pool_pages: int, max_pages: int, scale: float,
                  rank: int, world: int, lse_base: int = DCP_LSE_BASE_E, strategy: str = "a2a",
                  wire_dtype=torch.bfloat16, out_dtype=torch.bfloat16, part_dtype=torch.float32, group=None,
-                 device="cuda"):
+                 device="cuda", cache: str = "bf16"):
         sb, se = shard_range(rank, layout.n_shards, world)
         self.B, self.q_len, self.H = B, q_len, H
         self.local = ShardedMlaDecoder(layout, B, q_len, H, pool_pages, max_pages, scale, lse_base, out_dtype,
-                                       part_dtype, shard_begin=sb, shard_end=se, device=device)
+                                       part_dtype, shard_begin=sb, shard_end=se, device=device, cache=cache)
         self.xchg = DcpExchange(world, rank, layout.n_shards, B * q_len, H, lse_base, strategy, wire_dtype,
                                 out_dtype, device, group)
         self.head_begin, self.head_end = self.xchg.head_begin, self.xchg.head_end

@@ -19,6 +19,15 @@
  *   8. dcp_pack_partials       head slice d of every held shard -> rank d's chunk
  *   9. dcp_lse_merge_packed    the head owner's merge, read from its receive buffer
  *  10. dcp_lse_rescale         the local step of the AllGather + ReduceScatter form
+ * and, for a cache that holds the latent rows in 4 bits (416 bytes a token
+ * instead of 1152), the same steps on that cache
+ *  11. dcp_kv_append_q4        owner-filtered write, quantising
+ *      dcp_kv_relayout_q4      the same from a paged bf16 prefill pool
+ *      dcp_kv_read_q4          cached rows back as bf16
+ *      dcp_mla_decode_partial_q4  partial attention over the 4-bit rows
+ * and, before any of them, the tables they read
+ *  12. dcp_block_tables        block tables, free pages, positions and slots of a
+ *                              step from the requests' lengths
  *
  * On one GPU the N context shards are N compact paged pools in one HBM
  * allocation (the "arena"), so the cross-rank steps (query all-gather,
@@ -88,7 +97,10 @@ enum {
   DCP_STATUS_BAD_REQUEST = 8,     /* request index outside [0, B) */
   DCP_STATUS_BAD_LENGTH = 16,     /* seq_len < q_len */
   DCP_STATUS_TIMEOUT = 32,        /* a kernel pipeline wait gave up (the call's outputs are invalid) */
-  DCP_STATUS_INTERNAL = 64        /* a kernel found its shared memory misaligned and did nothing (outputs invalid) */
+  DCP_STATUS_INTERNAL = 64,       /* a kernel found its shared memory misaligned and did nothing (outputs invalid) */
+  DCP_STATUS_NO_PAGES = 128,      /* dcp_block_tables: fewer free pages than the step needs */
+  DCP_STATUS_TOO_MANY_TOKENS = 256, /* dcp_block_tables: more new tokens than the token arrays hold */
+  DCP_STATUS_BAD_POOL = 512       /* dcp_block_tables: a free list that cannot be (head, count, pages given back) */
 };
 
 enum { DCP_LSE_BASE_E = 0, DCP_LSE_BASE_2 = 1 };
@@ -485,6 +497,150 @@ int32_t dcp_lse_merge_packed(int32_t world, int32_t n_held, int64_t rows, const 
 int32_t dcp_lse_rescale(int32_t n_shards, int32_t shard_begin, int32_t n_held, int32_t T, int32_t H, int32_t world,
                         const float* lse_all, const void* o_part, int32_t o_part_dtype, int32_t lse_base,
                         float* o_sum, float* lse, void* stream);
+
+/*
+ * 4-bit latent cache.
+ *
+ * A row of 576 dims takes DCP_Q4_ROW_BYTES = 416 bytes:
+ *   bytes [0, 256)    the codes of dims [0, 512) (c_K), 4 bits each: 64
+ *                     little-endian 32-bit words; word k holds dims 8k .. 8k + 7,
+ *                     dim 8k + 2i in bits [4i, 4i + 4) and dim 8k + 2i + 1 in
+ *                     bits [16 + 4i, 20 + 4i), i < 4, each as its code plus 8
+ *   bytes [256, 288)  32 scales, e4m3 (4 exponent bits, 3 mantissa bits, no
+ *                     infinity): scale g belongs to dims [16g, 16g + 16)
+ *   bytes [288, 416)  dims [512, 576) (k_R) as bf16, unquantised
+ * The row stands for code * scale in dims [0, 512); a product of a code in
+ * [-8, 7] and an e4m3 scale is exact in bf16.  A zero-filled row stands for 0.
+ *
+ * Quantisation of 16 dims x (bf16): scale = the e4m3 value nearest to
+ * min(max |x| / 7, 448); code = the integer nearest to x / scale, clamped to
+ * [-7, 7], and 0 where the scale is 0; ties to even in both.  So a group whose
+ * largest magnitude is at most 7 * 2^-10 is held as zeros, one above 3136 is
+ * clamped to 3136, an infinity is held as the largest value of its sign, and a
+ * NaN makes its group NaN.  The scale varies with the group, so no tensor-wide
+ * factor exists; the intended rows are normalised latents (entries of order 1).
+ *
+ * Pools, block tables and slots are those of the bf16 cache:
+ *   arena  uint8[shard_end - shard_begin, pool_pages * P, 416], 16-byte aligned
+ */
+enum { DCP_Q4_ROW_BYTES = 416 };
+
+/*
+ * dcp_kv_append_q4 — owner-filtered write of new latent rows into a 4-bit cache.
+ *
+ * Arguments, placement, device status and errors as dcp_kv_append, with the
+ * 4-bit arena.  One addition: an entry with pos == -1 and req == -1 is padding
+ * (dcp_block_tables writes it behind the last token) and is skipped without a
+ * status bit.  A (pos, req) pair must appear once at most: two rows written to
+ * one slot by the same call leave either of them or a mixture.
+ */
+int32_t dcp_kv_append_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                         const void* kv_new, const int64_t* pos, const int32_t* req, int64_t T,
+                         const int32_t* block_table, int32_t B, int64_t bt_stride, int64_t max_pages,
+                         void* arena, int64_t pool_pages, int32_t* status, void* stream);
+
+/*
+ * dcp_kv_relayout_q4 — prefill-to-decode relayout into a 4-bit cache: the rows
+ * of a paged bf16 prefill pool, quantised into their owners' pools.  Arguments,
+ * placement, device status and errors as dcp_kv_relayout, with the 4-bit arena;
+ * padding entries and repeated pairs as for dcp_kv_append_q4.
+ */
+int32_t dcp_kv_relayout_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                           const void* src_pool, int64_t src_pool_rows, int32_t src_page_size,
+                           const int32_t* src_block_table, int64_t src_bt_stride, int64_t src_max_pages,
+                           const int64_t* pos, const int32_t* req, int64_t T, int32_t B,
+                           const int32_t* block_table, int64_t bt_stride, int64_t max_pages, void* arena,
+                           int64_t pool_pages, int32_t* status, void* stream);
+
+/*
+ * dcp_kv_read_q4 — cached rows back as the bf16 values they stand for (exact).
+ *
+ *   pos, req   int64[T], int32[T]: the tokens to read, in any order, repeats
+ *              allowed; placement and device status as for dcp_kv_append_q4
+ *   kv  (out)  bf16[T, 576]: row t is written if a held shard owns token t and
+ *              its page is in the pool; the other rows (another shard's tokens,
+ *              padding, bad ones) are left as they were
+ * For a chunk that attends to its prefix with its own kernels, for moving a
+ * request to a bf16 pool, or for looking at what the cache holds.  T == 0 is a
+ * no-op.  Errors: DCP_ERR_INVALID as for dcp_kv_append_q4.
+ */
+int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                       const void* arena, int64_t pool_pages, const int64_t* pos, const int32_t* req,
+                       int64_t T, const int32_t* block_table, int32_t B, int64_t bt_stride, int64_t max_pages,
+                       void* kv, int32_t* status, void* stream);
+
+/*
+ * dcp_mla_decode_partial_q4 — dcp_mla_decode_partial over a 4-bit cache.
+ *
+ * k_p is the row the cache holds (dims [0, 512) code * scale, dims [512, 576)
+ * bf16), its first 512 dims the value; everything else (arguments, outputs,
+ * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
+ * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
+ * bytes.  Rows of a page past the request's length carry no weight whatever
+ * they hold, NaN included.
+ */
+int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                                  const void* q, int32_t B, int32_t q_len, int32_t H,
+                                  const void* arena, int64_t pool_pages,
+                                  const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                                  const int64_t* seq_lens, float scale, int32_t lse_base,
+                                  void* o_part, int32_t o_part_dtype, float* lse_part,
+                                  void* workspace, size_t workspace_bytes,
+                                  int32_t* status, void* stream);
+
+/* Workspace bytes dcp_mla_decode_partial_q4 needs (as dcp_mla_decode_workspace_size). */
+size_t dcp_mla_decode_workspace_size_q4(const dcp_layout_t* layout, int32_t shard_begin,
+                                        int32_t shard_end, int32_t B, int32_t q_len, int32_t H);
+
+/*
+ * dcp_block_tables — the tables of a step, from the requests' lengths.
+ *
+ * Sources: SGLang "Decode context parallelism", "Virtual KV layout" (a widened
+ * page of N * P positions is one physical page on every shard and one entry of
+ * the shared block table, so a request of x positions holds ceil(x / (N * P))
+ * pages); "PCP / DCP：计算、KV 布局与块轮转", section "KV cache 管理".
+ *
+ * Moves every request b from seq_lens[b] to new_lens[b] cached positions: a
+ * growing request takes pages from the free list and lists its new positions, a
+ * shrinking one (rejected draft tokens, a finished request going to 0) gives
+ * pages back.  Nothing is read on the host, so a step can be captured.
+ *
+ *   seq_lens    (in/out) int64[B]; becomes new_lens
+ *   new_lens    int64[B] (not the same array as seq_lens)
+ *   block_table (in/out) int32[B, bt_stride], columns k < max_pages.  Entries of
+ *               pages taken are filled, those of pages given back become -1, the
+ *               others are left as they are
+ *   free_pages  (in/out) int32[pool_pages], a ring of page ids; the free ones are
+ *               entries (head + i) % pool_pages, i < count
+ *   free_state  (in/out) int64[2] {head, count}.  Pages are taken from the head,
+ *               requests in order and each request's pages in order; pages given
+ *               back go behind the last free one in the same order, and can be
+ *               taken from the next call on
+ *   T           entries of the token arrays below
+ *   pos, req    (out, both or neither NULL) int64[T], int32[T]: the positions
+ *               [seq_lens[b], new_lens[b]) of the growing requests, requests in
+ *               order; entries behind the last token get pos = req = -1
+ *   owner, row, slot  (out, each may be NULL) int32[T], int64[T], int64[T]: as
+ *               dcp_slot_map's for those tokens; -1 behind the last one
+ *   cu_tokens   (out) int64[B + 1]: tokens of the requests before b
+ *   status      device word (required)
+ * With pos == NULL no token is listed and T is not looked at.
+ * The call happens as a whole or not at all: if a length is negative (or above
+ * 2^62 / B) (BAD_LENGTH) or needs more than max_pages pages (BAD_PAGE_INDEX), the
+ * free list is too short (NO_PAGES) or inconsistent (BAD_POOL), or there are more
+ * than T tokens (TOO_MANY_TOKENS), the lengths, the tables and the free list stay
+ * as they are, every token entry is -1 and cu_tokens is 0.  A table entry
+ * outside [0, pool_pages) is flagged (BAD_PAGE_ID): given back, it goes to the
+ * ring as it is; for a listed token, its slot is -1.
+ * Errors: DCP_ERR_INVALID for a bad layout, B < 1, max_pages outside
+ * [1, bt_stride], pool_pages outside [1, 2^31), T < 0, a null pointer, pos
+ * without req or owner / row / slot without them, or seq_lens == new_lens.
+ */
+int32_t dcp_block_tables(const dcp_layout_t* layout, int32_t B, int64_t* seq_lens, const int64_t* new_lens,
+                         int32_t* block_table, int64_t bt_stride, int64_t max_pages, int32_t* free_pages,
+                         int64_t* free_state, int64_t pool_pages, int64_t T, int64_t* pos, int32_t* req,
+                         int32_t* owner, int64_t* row, int64_t* slot, int64_t* cu_tokens, int32_t* status,
+                         void* stream);
 
 #ifdef __cplusplus
 }
