@@ -54,6 +54,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same test, suspended by the hardware for up to `ns` nanoseconds until the phase completes.
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase of `bar` with the given parity to complete.  Returns false
 // (and raises *abort) on timeout, or at once if *abort is already raised.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -246,6 +258,56 @@ __device__ __forceinline__ void tmem_ld16x2_sync(uint32_t taddr, uint32_t (&r)[3
       : "memory");
 }
 
+#define DCP_R8(r) "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+#define DCP_R16(r)                                                                                                 \
+  DCP_R8(r), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+
+// The same lane mapping with 16 or 8 columns per thread (threads 16-31 at
+// col + kSplit); r is complete on return.
+template <int kSplit>
+__device__ __forceinline__ void tmem_ld16x2_16_sync(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DCP_R16(r)
+      : "r"(taddr), "n"(kSplit)
+      : "memory");
+}
+
+// Two such loads of 16 columns and one wait.
+template <int kSplit>
+__device__ __forceinline__ void tmem_ld16x2_16_pair_sync(uint32_t taddr0, uint32_t (&r0)[16], uint32_t taddr1,
+                                                         uint32_t (&r1)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32], %34;\n\t"
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%33], %34;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DCP_R16(r0), DCP_R16(r1)
+      : "r"(taddr0), "r"(taddr1), "n"(kSplit)
+      : "memory");
+}
+
+template <int kSplit>
+__device__ __forceinline__ void tmem_ld16x2_8_sync(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DCP_R8(r)
+      : "r"(taddr), "n"(kSplit)
+      : "memory");
+}
+
+#undef DCP_R16
+#undef DCP_R8
+
+template <int kSplit>
+__device__ __forceinline__ void tmem_st16x2_8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %9, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "n"(kSplit)
+               : "memory");
+}
+
 // 16 columns per thread, same lane mapping (threads 16-31 at col + kSplit).
 template <int kSplit>
 __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -275,6 +337,13 @@ __device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[
 // their writes are visible.  With a programmatic dependent launch the grid may
 // start while the one before it finishes; without one this returns at once.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -306,17 +375,37 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
   return v;
 }
 
+__device__ __forceinline__ float2 ld_shared_f32x2(uint32_t saddr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(saddr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_shared_f32x2(uint32_t saddr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(saddr), "f"(a), "f"(b) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t saddr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(saddr) : "memory");
+  return v;
+}
+
 // Bulk copy of `bytes` (multiple of 16) from this CTA's shared memory to another
 // CTA's shared memory (`dst_cluster`, from mapa), credited on that CTA's
 // mbarrier (`bar_cluster`) with complete_tx.  Done by the copy engine: the
 // issuing thread does not wait for the slow cluster network.
-__device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, const void* src, uint32_t bytes,
+__device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
                                                   uint32_t bar_cluster) {
   asm volatile(
       "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
           dst_cluster),
-      "r"(smem_u32(src)), "r"(bytes), "r"(bar_cluster)
+      "r"(src), "r"(bytes), "r"(bar_cluster)
       : "memory");
+}
+__device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, const void* src, uint32_t bytes,
+                                                  uint32_t bar_cluster) {
+  bulk_copy_to_peer(dst_cluster, smem_u32(src), bytes, bar_cluster);
 }
 
 // ---------------------------------------------------------------- descriptors
