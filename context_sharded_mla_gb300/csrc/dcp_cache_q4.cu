@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(256) read_q4_kernel(Layout L, int32_t shard_be
   const uint2 codes = __ldg(reinterpret_cast<const uint2*>(from) + lane);
   const uint32_t scale = __ldg(from + kQ4ScaleOff + lane);
   const uint32_t rope = __ldg(reinterpret_cast<const uint32_t*>(from + kQ4RopeOff) + lane);
-  uint32_t s2[2], v[2][4];
-  q4_scales(scale, s2);
-  q4_values(codes.x, s2[0], v[0]);
-  q4_values(codes.y, s2[0], v[1]);
+  uint32_t s2[2], off2[2], v[2][4];
+  q4_scales(scale, s2, off2);
+  q4_values(codes.x, s2[0], off2[0], v[0]);
+  q4_values(codes.y, s2[0], off2[0], v[1]);
   unsigned char* to = kv + t * (kDk * 2);
 #pragma unroll
   for (int j = 0; j < 2; ++j)

@@ -381,6 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int w = warp - kDequantWarp0;
     const int r8 = lane & 7, pc = lane >> 3;
     const int nbox = kTile / a.box_rows;
+    const int box0 = kDequantRows * w / a.box_rows, box1 = (kDequantRows * w + 8) / a.box_rows;
     uint32_t m = 0, mphase = 0, ts = 0, tphase = 0;
     bool ok = true;
     for (uint32_t j = 0; j < ntiles; ++j) {
@@ -394,15 +395,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 4; ++e) {
         const int row = kDequantRows * w + 8 * (e >> 1) + r8;
         const int piece = pc + 4 * (e & 1);  // of this CTA's 8
-        const bool live = row < rr.valid && rr.y[(row - r8) / a.box_rows] >= 0;
+        const bool live = row < rr.valid && rr.y[e < 2 ? box0 : box1] >= 0;
         const uint4 code = ld_shared_v4(src + (uint32_t)row * 128 + (uint32_t)((piece ^ r8) << 4));
         const uint32_t two = ld_shared_u16(src + kRawCodeBytes + (uint32_t)row * 16 + 2 * piece);
-        uint32_t s2[2];
-        q4_scales(live ? two : 0u, s2);
-        q4_values(code.x, s2[0], x[e][0]);
-        q4_values(code.y, s2[0], x[e][1]);
-        q4_values(code.z, s2[1], x[e][2]);
-        q4_values(code.w, s2[1], x[e][3]);
+        uint32_t s2[2], o2[2];
+        q4_scales(live ? two : 0u, s2, o2);
+        q4_values(code.x, s2[0], o2[0], x[e][0]);
+        q4_values(code.y, s2[0], o2[0], x[e][1]);
+        q4_values(code.z, s2[1], o2[1], x[e][2]);
+        q4_values(code.w, s2[1], o2[1], x[e][3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kREmpty + m]);
@@ -623,6 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             rescale_rows(tmem + lane_addr + kOCol, alpha);
           }
+          tmem_st_wait();  // the own P is read back
           uint32_t mine[8];
           tmem_ld16x2_8_sync<8>(pc + 16 * rank, mine);
           scale_bf16x2(mine, alpha);
@@ -818,9 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (j >= 2 && !wwait(&bars[kPVDone + odd], ((j - 2) >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          tmem_st16x2_8<8>(tmem + lane_addr + kPCol + 32 * odd + 16 * rank, pk);
-          tmem_st_wait();
-          tc_fence_before();
+          tmem_st16x2_8<8>(tmem + lane_addr + kPCol + 32 * odd + 16 * rank, pk);  // complete before take_p releases it
           if (jj == 0) {
             has_next = nx.next(&u2, &t02, &nt2, &wh2, &ks2);
             if (has_next) {

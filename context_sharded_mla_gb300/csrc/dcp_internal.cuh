@@ -146,21 +146,25 @@ __device__ __forceinline__ float2 q4_scales_f32(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The same two scales, each as a bf16 pair (an e4m3's 4 significant bits fit).
-__device__ __forceinline__ void q4_scales(uint32_t two, uint32_t (&s2)[2]) {
+// The same two scales s, each as a bf16 pair (an e4m3's 4 significant bits fit), and
+// -136 s of each (17 * 8 s: at most 4 + 4 significant bits, exact as well).
+__device__ __forceinline__ void q4_scales(uint32_t two, uint32_t (&s2)[2], uint32_t (&off2)[2]) {
   const float2 f = q4_scales_f32(two);
   const __nv_bfloat162 a = __float2bfloat162_rn(f.x), b = __float2bfloat162_rn(f.y);
+  const __nv_bfloat162 ao = __float2bfloat162_rn(-136.f * f.x), bo = __float2bfloat162_rn(-136.f * f.y);
   s2[0] = *reinterpret_cast<const uint32_t*>(&a);
   s2[1] = *reinterpret_cast<const uint32_t*>(&b);
+  off2[0] = *reinterpret_cast<const uint32_t*>(&ao);
+  off2[1] = *reinterpret_cast<const uint32_t*>(&bo);
 }
 
 // The 8 values of one word of codes, as bf16 pairs in dim order.  With n in the
 // low mantissa bits of a bf16 of exponent 7, (n | 0x4300) = 128 + n, and
-// (128 + n) s - 136 s = (n - 8) s.  136 s = 17 * 8 s has at most 4 + 4
-// significant bits and (n - 8) s at most 7, so neither product is rounded.
-__device__ __forceinline__ void q4_values(uint32_t word, uint32_t s2, uint32_t (&v)[4]) {
+// (128 + n) s - 136 s = (n - 8) s, which has at most 7 significant bits: the fma
+// rounds nothing.
+__device__ __forceinline__ void q4_values(uint32_t word, uint32_t s2, uint32_t off2, uint32_t (&v)[4]) {
   const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-  const __nv_bfloat162 off = __hmul2(s, __float2bfloat162_rn(-136.f));
+  const __nv_bfloat162 off = *reinterpret_cast<const __nv_bfloat162*>(&off2);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t n = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
