@@ -459,76 +459,81 @@ def dcp_lse_rescale(lse_all, o_part, shard_begin, world, lse_base, o_sum, lse=No
         _ptr(o_sum), _ptr(lse), _stream(stream)))
 
 
-def _here(*tensors):
-    """The tensors lie on the current device (the one the library launches on)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor lies on {t.device}, but the current device is cuda:{dev}")
+def _at(t, name, dtype, shape, dev):
+    """Address of a tensor after _dev's checks; it also lies on the current device, where the library launches.
+    (One pass of cheap tests: a decode step's small calls take as long on the host as on the GPU.)"""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
 
 
-def _tokens(pos, req, block_table):
-    T = pos.numel()
-    _dev(pos, "pos", torch.int64, (T,))
-    _dev(req, "req", torch.int32, (T,))
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max pages]")
-    return T
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"stream belongs to {stream.device}, but the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
-def _arena_q4(layout, shard_begin, shard_end, arena, pool_pages):
-    _dev(arena, "arena", torch.uint8, (shard_end - shard_begin, pool_pages * layout.page_size, Q4_ROW_BYTES))
+def _table(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a [B, max pages] tensor")
+    return t.shape
 
 
 def dcp_kv_append_q4(layout, shard_begin, shard_end, kv_new, pos, req, block_table, max_pages, arena, pool_pages,
                      status, stream=None):
     """Owner-filtered write of kv_new [T, 576] bf16 into a 4-bit arena [shards, pool_pages*P, 416] uint8;
     entries with pos = req = -1 are padding."""
-    T = _tokens(pos, req, block_table)
-    _dev(kv_new, "kv_new", torch.bfloat16, (T, 576))
-    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
-    _dev(status, "status", torch.int32, (1,))
-    _here(kv_new, pos, req, block_table, arena, status)
-    B, stride = block_table.shape
-    _check("dcp_kv_append_q4", load_library().dcp_kv_append_q4(
-        ctypes.byref(layout), shard_begin, shard_end, _ptr(kv_new), _ptr(pos), _ptr(req), T, _ptr(block_table),
-        B, stride, max_pages, _ptr(arena), pool_pages, _ptr(status), _stream(stream)))
+    dev = torch.cuda.current_device()
+    T = pos.numel()
+    B, stride = _table(block_table, "block_table")
+    rc = load_library().dcp_kv_append_q4(
+        layout, shard_begin, shard_end, _at(kv_new, "kv_new", torch.bfloat16, (T, 576), dev),
+        _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T,
+        _at(block_table, "block_table", torch.int32, None, dev), B, stride, max_pages,
+        _at(arena, "arena", torch.uint8, (shard_end - shard_begin, pool_pages * layout.page_size, Q4_ROW_BYTES), dev),
+        pool_pages, _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check("dcp_kv_append_q4", rc)
 
 
 def dcp_kv_relayout_q4(layout, shard_begin, shard_end, src_pool, src_page_size, src_block_table, src_max_pages,
                        pos, req, block_table, max_pages, arena, pool_pages, status, stream=None):
     """Owner-filtered copy of tokens (pos, req) from a paged bf16 prefill pool [rows, 576] into a 4-bit arena."""
-    T = _tokens(pos, req, block_table)
-    _dev(src_pool, "src_pool", torch.bfloat16)
+    dev = torch.cuda.current_device()
+    T = pos.numel()
+    B, stride = _table(block_table, "block_table")
+    if _table(src_block_table, "src_block_table")[0] != B:
+        raise ValueError("src_block_table and block_table must have one row per request")
     if src_pool.dim() != 2 or src_pool.shape[1] != 576:
         raise ValueError("src_pool must be [rows, 576]")
-    _dev(src_block_table, "src_block_table", torch.int32)
-    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
-    _dev(status, "status", torch.int32, (1,))
-    B, stride = block_table.shape
-    if src_block_table.dim() != 2 or src_block_table.shape[0] != B:
-        raise ValueError("src_block_table and block_table must have one row per request")
-    _here(src_pool, src_block_table, pos, req, block_table, arena, status)
-    _check("dcp_kv_relayout_q4", load_library().dcp_kv_relayout_q4(
-        ctypes.byref(layout), shard_begin, shard_end, _ptr(src_pool), src_pool.shape[0], src_page_size,
-        _ptr(src_block_table), src_block_table.shape[1], src_max_pages, _ptr(pos), _ptr(req), T, B,
-        _ptr(block_table), stride, max_pages, _ptr(arena), pool_pages, _ptr(status), _stream(stream)))
+    rc = load_library().dcp_kv_relayout_q4(
+        layout, shard_begin, shard_end, _at(src_pool, "src_pool", torch.bfloat16, None, dev), src_pool.shape[0],
+        src_page_size, _at(src_block_table, "src_block_table", torch.int32, None, dev), src_block_table.shape[1],
+        src_max_pages, _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T, B,
+        _at(block_table, "block_table", torch.int32, None, dev), stride, max_pages,
+        _at(arena, "arena", torch.uint8, (shard_end - shard_begin, pool_pages * layout.page_size, Q4_ROW_BYTES), dev),
+        pool_pages, _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check("dcp_kv_relayout_q4", rc)
 
 
 def dcp_kv_read_q4(layout, shard_begin, shard_end, arena, pool_pages, pos, req, block_table, max_pages, kv, status,
                    stream=None):
     """kv [T, 576] bf16: the values a 4-bit arena holds for tokens (pos, req); rows of tokens that are not held
     (other shards', padding) are left as they were."""
-    T = _tokens(pos, req, block_table)
-    _dev(kv, "kv", torch.bfloat16, (T, 576))
-    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
-    _dev(status, "status", torch.int32, (1,))
-    _here(arena, pos, req, block_table, kv, status)
-    B, stride = block_table.shape
-    _check("dcp_kv_read_q4", load_library().dcp_kv_read_q4(
-        ctypes.byref(layout), shard_begin, shard_end, _ptr(arena), pool_pages, _ptr(pos), _ptr(req), T,
-        _ptr(block_table), B, stride, max_pages, _ptr(kv), _ptr(status), _stream(stream)))
+    dev = torch.cuda.current_device()
+    T = pos.numel()
+    B, stride = _table(block_table, "block_table")
+    rc = load_library().dcp_kv_read_q4(
+        layout, shard_begin, shard_end,
+        _at(arena, "arena", torch.uint8, (shard_end - shard_begin, pool_pages * layout.page_size, Q4_ROW_BYTES), dev),
+        pool_pages, _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T,
+        _at(block_table, "block_table", torch.int32, None, dev), B, stride, max_pages,
+        _at(kv, "kv", torch.bfloat16, (T, 576), dev), _at(status, "status", torch.int32, (1,), dev),
+        _raw_stream(stream, dev))
+    _check("dcp_kv_read_q4", rc)
 
 
 def dcp_mla_decode_workspace_size_q4(layout, shard_begin, shard_end, B, q_len, H) -> int:
@@ -539,28 +544,26 @@ def dcp_mla_decode_workspace_size_q4(layout, shard_begin, shard_end, B, q_len, H
 def dcp_mla_decode_partial_q4(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages,
                               seq_lens, scale, lse_base, o_part, lse_part, workspace, status, stream=None):
     """dcp_mla_decode_partial over a 4-bit arena [shards, pool_pages*P, 416] uint8."""
+    dev = torch.cuda.current_device()
     if q.dim() != 4:
         raise ValueError("q must be [B, q_len, H, 576]")
     B, q_len, H, _ = q.shape
     n = shard_end - shard_begin
-    _dev(q, "q", torch.bfloat16, (B, q_len, H, 576))
-    _arena_q4(layout, shard_begin, shard_end, arena, pool_pages)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int64, (B,))
-    _dev(o_part, "o_part", o_part.dtype, (n, B, q_len, H, 512))
-    _dev(lse_part, "lse_part", torch.float32, (n, B, q_len, H))
-    _dev(status, "status", torch.int32, (1,))
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        _dev(workspace, "workspace", torch.uint8)
-        ws_ptr, ws_bytes = _ptr(workspace), workspace.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if _table(block_table, "block_table")[0] != B:
         raise ValueError("block_table must have one row per request")
-    _here(q, arena, block_table, seq_lens, o_part, lse_part, workspace, status)
-    _check("dcp_mla_decode_partial_q4", load_library().dcp_mla_decode_partial_q4(
-        ctypes.byref(layout), shard_begin, shard_end, _ptr(q), B, q_len, H, _ptr(arena), pool_pages,
-        _ptr(block_table), block_table.shape[1], max_pages, _ptr(seq_lens), float(scale), lse_base,
-        _ptr(o_part), _dtype_code(o_part), _ptr(lse_part), ws_ptr, ws_bytes, _ptr(status), _stream(stream)))
+    o_code = _dtype_code(o_part)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _at(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
+    rc = load_library().dcp_mla_decode_partial_q4(
+        layout, shard_begin, shard_end, _at(q, "q", torch.bfloat16, (B, q_len, H, 576), dev), B, q_len, H,
+        _at(arena, "arena", torch.uint8, (n, pool_pages * layout.page_size, Q4_ROW_BYTES), dev), pool_pages,
+        _at(block_table, "block_table", torch.int32, None, dev), block_table.shape[1], max_pages,
+        _at(seq_lens, "seq_lens", torch.int64, (B,), dev), scale, lse_base,
+        _at(o_part, "o_part", o_part.dtype, (n, B, q_len, H, 512), dev), o_code,
+        _at(lse_part, "lse_part", torch.float32, (n, B, q_len, H), dev), ws, ws_bytes,
+        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check("dcp_mla_decode_partial_q4", rc)
 
 
 def dcp_block_tables(layout, seq_lens, new_lens, block_table, max_pages, free_pages, free_state, cu_tokens, status,
@@ -568,25 +571,27 @@ def dcp_block_tables(layout, seq_lens, new_lens, block_table, max_pages, free_pa
     """Moves the requests from seq_lens to new_lens (int64 [B], seq_lens updated): takes pages from and gives them
     back to the ring free_pages (int32 [pool pages], free_state int64 {head, count}), updates block_table, and lists
     the new tokens in pos / req (and owner / row / slot), cu_tokens int64 [B + 1]."""
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max pages]")
-    B, stride = block_table.shape
-    _dev(seq_lens, "seq_lens", torch.int64, (B,))
-    _dev(new_lens, "new_lens", torch.int64, (B,))
-    _dev(free_pages, "free_pages", torch.int32)
-    _dev(free_state, "free_state", torch.int64, (2,))
-    _dev(cu_tokens, "cu_tokens", torch.int64, (B + 1,))
-    _dev(status, "status", torch.int32, (1,))
-    T = 0 if pos is None else pos.numel()
-    for t, name, dtype in ((pos, "pos", torch.int64), (req, "req", torch.int32), (owner, "owner", torch.int32),
-                           (row, "row", torch.int64), (slot, "slot", torch.int64)):
-        if t is not None:
-            _dev(t, name, dtype, (T,))
-    if T == 0 and pos is not None:
-        raise ValueError("pos is empty: leave the token arrays out to list no tokens")
-    _here(seq_lens, new_lens, block_table, free_pages, free_state, cu_tokens, status, pos, req, owner, row, slot)
-    _check("dcp_block_tables", load_library().dcp_block_tables(
-        ctypes.byref(layout), B, _ptr(seq_lens), _ptr(new_lens), _ptr(block_table), stride, max_pages,
-        _ptr(free_pages), _ptr(free_state), free_pages.numel(), T, _ptr(pos), _ptr(req), _ptr(owner), _ptr(row),
-        _ptr(slot), _ptr(cu_tokens), _ptr(status), _stream(stream)))
+    dev = torch.cuda.current_device()
+    B, stride = _table(block_table, "block_table")
+    T, at_pos, at_req, at_owner, at_row, at_slot = 0, None, None, None, None, None
+    if pos is not None:
+        T = pos.numel()
+        if T == 0:
+            raise ValueError("pos is empty: leave the token arrays out to list no tokens")
+        at_pos = _at(pos, "pos", torch.int64, (T,), dev)
+    if req is not None:
+        at_req = _at(req, "req", torch.int32, (T,), dev)
+    if owner is not None:
+        at_owner = _at(owner, "owner", torch.int32, (T,), dev)
+    if row is not None:
+        at_row = _at(row, "row", torch.int64, (T,), dev)
+    if slot is not None:
+        at_slot = _at(slot, "slot", torch.int64, (T,), dev)
+    rc = load_library().dcp_block_tables(
+        layout, B, _at(seq_lens, "seq_lens", torch.int64, (B,), dev), _at(new_lens, "new_lens", torch.int64, (B,), dev),
+        _at(block_table, "block_table", torch.int32, None, dev), stride, max_pages,
+        _at(free_pages, "free_pages", torch.int32, None, dev), _at(free_state, "free_state", torch.int64, (2,), dev),
+        free_pages.numel(), T, at_pos, at_req, at_owner, at_row, at_slot,
+        _at(cu_tokens, "cu_tokens", torch.int64, (B + 1,), dev), _at(status, "status", torch.int32, (1,), dev),
+        _raw_stream(stream, dev))
+    _check("dcp_block_tables", rc)
