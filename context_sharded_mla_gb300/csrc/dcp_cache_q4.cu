@@ -7,19 +7,24 @@
 //
 // Quantisation of a group of 16 dims with largest magnitude A:
 //   s = e4m3(min(A / 7, 448)),  code = clamp(round(x / s), -7, 7)  (0 if s = 0),
-// both roundings to nearest, ties to even.  The codes are those of exact arithmetic
-// without a division per value: a bf16 x has 8 significant bits and s has 4, so
-// x / s is a tie n + 1/2 exactly or at least 2^-9 away from every tie, while
-// y = x * (1 / s) in fp32 is within 2^-19 of x / s (|x / s| < 8).  Rounding y to a
-// multiple of 2^-12 therefore restores a tie and makes none.  (With 16 fp32
-// divisions a lane the kernel was bound by them: 18 us for 32768 rows.)
+// both roundings to nearest, ties to even.  Both are those of exact arithmetic,
+// without a division: a bf16 x has 8 significant bits and s has 4, so x / s is a tie
+// n + 1/2 exactly or at least 2^-9 away from every tie, while x * (1 / s) in fp32 is
+// within 2^-19 of x / s (|x / s| < 8).  Rounding it to a multiple of 2^-11 therefore
+// restores a tie and makes none.  A / 7 likewise: rounded to 12 significant bits, it
+// lies on a midpoint of two e4m3 values only if it does exactly (those have 5).
+// (With 17 fp32 divisions a lane the kernel was bound by them: 122 us for 262143
+// rows, against 72 now.)
 //
 // A warp serves `per_warp` tokens: a lane each looks up their places, so that
-// positions, requests and block-table entries are one latency for all of them;
-// then lane g takes group g of each token (32 bytes in, 8 bytes of codes and a
-// scale byte out, or the other way), four tokens' loads ahead of their stores, and
-// no value crosses lanes; the 64 rope dims go through as 4 bytes a lane.
-// Memory-bound for long lists: 1152 + 416 bytes a token either way.
+// positions, requests and block-table entries are one latency for all of them; then
+// the whole warp takes a token at a time, several tokens' loads ahead of their stores.
+// Lane l has dims [8 l, 8 l + 8) and [256 + 8 l, 256 + 8 l + 8), one word of codes
+// each, so that every access is one run of the row: 512 bytes of bf16, 128 of codes.
+// A group is two neighbouring lanes' (one shuffle for its magnitude); the 64 rope
+// dims go through as 4 bytes a lane.  Memory-bound for long lists: 1152 + 416 bytes a
+// token either way; 262143 rows in 72 us written (5.7 TB/s) and 76 us read (5.4 TB/s).
+// A list of a few rows is two or three memory latencies, 4 us in a captured graph.
 #include "dcp_internal.cuh"
 
 using namespace dcp;
@@ -45,54 +50,87 @@ struct Table {
   int64_t stride, max_pages, pool_pages;
 };
 
-// Pool row (over all held pools) of token (p, b), or -1 for a padding entry
-// (p = b = -1), another shard's token, or a bad one (flagged).
-__device__ __forceinline__ int64_t held_row(int64_t p, int32_t b, const Layout& L, const Table& t, int32_t shard_begin,
-                                            int32_t shard_end, int32_t* status) {
-  if (p == -1 && b == -1) return -1;
+// Where a token goes: its block-table entry is loaded, but not looked at yet, so
+// that the loads of its row can go out in the same latency.
+struct Spot {
+  int64_t page;  // block-table entry
+  int64_t pool;  // first row of its shard's pool, -1: nothing to do
+  int64_t in_page;
+};
+
+// The spot of token (p, b); none for a padding entry (p = b = -1), another shard's
+// token, or a bad one (flagged).
+__device__ __forceinline__ Spot find_spot(int64_t p, int32_t b, const Layout& L, const Table& t, int32_t shard_begin,
+                                          int32_t shard_end, int32_t* status) {
+  if (p == -1 && b == -1) return Spot{-1, -1, 0};
   if (p < 0 || b < 0 || b >= t.B) {
     flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
-    return -1;
+    return Spot{-1, -1, 0};
   }
   const Place at = place_of(p, L);
-  if (at.owner < shard_begin || at.owner >= shard_end) return -1;
+  if (at.owner < shard_begin || at.owner >= shard_end) return Spot{-1, -1, 0};
   const int64_t pidx = at.row < INT32_MAX ? (int32_t)at.row / (int32_t)L.P : at.row / L.P;
   if (pidx >= t.max_pages) {
     flag(status, DCP_STATUS_BAD_PAGE_INDEX);
-    return -1;
+    return Spot{-1, -1, 0};
   }
-  const int64_t page = __ldg(t.bt + (int64_t)b * t.stride + pidx);
-  if (page < 0 || page >= t.pool_pages) {
+  return Spot{__ldg(t.bt + (int64_t)b * t.stride + pidx), (at.owner - shard_begin) * t.pool_pages * L.P,
+              at.row - pidx * L.P};
+}
+
+// Its row over all held pools, or -1 (a bad page is flagged).
+__device__ __forceinline__ int64_t row_of(const Spot& s, const Layout& L, const Table& t, int32_t* status) {
+  if (s.pool < 0) return -1;
+  if (s.page < 0 || s.page >= t.pool_pages) {
     flag(status, DCP_STATUS_BAD_PAGE_ID);
     return -1;
   }
-  return ((at.owner - shard_begin) * t.pool_pages + page) * L.P + (at.row - pidx * L.P);
+  return s.pool + s.page * L.P + s.in_page;
 }
 
-// 16 bf16 dims -> their two words of codes and the scale byte.
-__device__ __forceinline__ uint2 quantise16(const uint4 (&x)[2], uint32_t& scale) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(x);
-  __nv_bfloat162 top2 = __habs2(h[0]);
+// Largest magnitude of 8 bf16 values; a NaN among them gives NaN.
+__device__ __forceinline__ __nv_bfloat16 top8(const uint4& x) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+  const __nv_bfloat162 a = __hmax2_nan(__habs2(h[0]), __habs2(h[1])), b = __hmax2_nan(__habs2(h[2]), __habs2(h[3]));
+  const __nv_bfloat162 c = __hmax2_nan(a, b);
+  return __hmax_nan(c.x, c.y);
+}
+
+// A / 7 to 12 significant bits (an infinity stays one; a NaN's bits could wrap).
+__device__ __forceinline__ float seventh(float top) {
+  const float q = __uint_as_float((__float_as_uint(top * (1.f / 7.f)) + 0x800u) & 0xFFFFF000u);
+  return top != top ? top : q;
+}
+
+__device__ __forceinline__ float reciprocal(float s) {  // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// The word of codes of 8 bf16 values under scale s, whose group's largest magnitude is
+// `top`.  A sum with kSnap ends at a multiple of 2^-11, one with kInt at a whole number
+// that its low mantissa bits hold as code + 8.
+__device__ __forceinline__ uint32_t codes8(const uint4& x, float s, float top) {
+  constexpr float kSnap = 1.5f * 4096.f, kInt = 1.5f * 8388608.f + 8.f;
+  if (!(s > 0.f)) return 0x88888888u;  // scale 0 or NaN: every code 0
+  const float inv = reciprocal(s);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+  // only a scale that was clamped, or is one of the few smallest, leaves |x / s| above 7.5
+  const bool clamp = !(top * inv < 7.5f);
+  uint32_t w = 0;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) top2 = __hmax2_nan(top2, __habs2(h[k]));
-  // a NaN makes its whole group one (and e4m3's only NaN, 0x7f, its scale)
-  const float top = __bfloat162float(__hmax_nan(top2.x, top2.y));
-  scale = (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(top, 7.f), __NV_SATFINITE, __NV_E4M3);
-  const float s = q4_scales_f32(scale).x;
-  if (!(s > 0.f)) return make_uint2(0x88888888u, 0x88888888u);  // every code 0
-  const float inv = __frcp_rn(s);
-  constexpr float kSnap = 1.5f * 2048.f;               // + and - this: to a multiple of 2^-12
-  constexpr float kInt = 1.5f * 8388608.f + 8.f;       // + this: code + 8 in the low mantissa bits
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 f = __bfloat1622float2(h[k]);
-    const float a = fminf(fmaxf(f.x * inv, -7.f), 7.f), b = fminf(fmaxf(f.y * inv, -7.f), 7.f);
-    const uint32_t na = __float_as_uint(__fadd_rn(__fsub_rn(__fadd_rn(a, kSnap), kSnap), kInt)) & 15u;
-    const uint32_t nb = __float_as_uint(__fadd_rn(__fsub_rn(__fadd_rn(b, kSnap), kSnap), kInt)) & 15u;
-    w[k >> 2] |= (na | nb << 16) << (4 * (k & 3));
+  for (int k = 0; k < 4; ++k) {
+    float2 f = __bfloat1622float2(h[k]);
+    if (clamp) {
+      f.x = fminf(fmaxf(f.x, -7.f * s), 7.f * s);
+      f.y = fminf(fmaxf(f.y, -7.f * s), 7.f * s);
+    }
+    const uint32_t a = __float_as_uint(__fadd_rn(__fmaf_rn(f.x, inv, kSnap), kInt - kSnap));
+    const uint32_t b = __float_as_uint(__fadd_rn(__fmaf_rn(f.y, inv, kSnap), kInt - kSnap));
+    w |= __byte_perm(a, b, 0x5410) << (4 * k);
   }
-  return make_uint2(w[0], w[1]);
+  return w;
 }
 
 // The source row of a moved token, or -1: row t of kv_new, or the prefill pool's
@@ -124,7 +162,9 @@ struct PoolRows {
   }
 };
 
-constexpr int kAhead = 4;  // tokens whose loads are in flight before their stores
+// Tokens whose loads are in flight before their stores.  262143 rows: writing takes
+// 72 us with 4 and 91 with 8 (fewer warps fit), reading 88 and 76.
+constexpr int kStoreAhead = 4, kReadAhead = 8;
 
 template <class Src>
 __global__ void __launch_bounds__(256) store_q4_kernel(Layout L, int32_t shard_begin, int32_t shard_end, Src src,
@@ -136,35 +176,45 @@ __global__ void __launch_bounds__(256) store_q4_kernel(Layout L, int32_t shard_b
   const int lane = threadIdx.x & 31;
   const int n = (int)min((int64_t)per_warp, T - t0);  // not above 0: no token
   int64_t from = -1, to = -1;                         // lane: source and pool row of token t0 + lane
+  Spot spot{-1, -1, 0};
   if (lane < n) {
     const int64_t p = __ldg(pos + t0 + lane);
     const int32_t b = __ldg(req + t0 + lane);
-    to = held_row(p, b, L, tab, shard_begin, shard_end, status);
-    if (to >= 0) from = src.row(t0 + lane, p, b, status);
+    spot = find_spot(p, b, L, tab, shard_begin, shard_end, status);
+    if (spot.pool >= 0) from = src.row(t0 + lane, p, b, status);
   }
-  for (int i = 0; i < n; i += kAhead) {
-    uint4 x[kAhead][2];
-    uint32_t rope[kAhead];
-    int64_t f[kAhead];
+  for (int i = 0; i < n; i += kStoreAhead) {
+    uint4 x[kStoreAhead][2];
+    uint32_t rope[kStoreAhead];
+    int64_t f[kStoreAhead];
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
+    for (int e = 0; e < kStoreAhead; ++e) {
       f[e] = __shfl_sync(0xffffffffu, from, i + e);
       if (i + e >= n) f[e] = -1;
+      x[e][0] = x[e][1] = make_uint4(0, 0, 0, 0);
       if (f[e] < 0) continue;
       const unsigned char* row = src.base + f[e] * (kDk * 2);
-      x[e][0] = __ldg(reinterpret_cast<const uint4*>(row) + 2 * lane);
-      x[e][1] = __ldg(reinterpret_cast<const uint4*>(row) + 2 * lane + 1);
+      x[e][0] = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+      x[e][1] = __ldg(reinterpret_cast<const uint4*>(row) + 32 + lane);
       rope[e] = __ldg(reinterpret_cast<const uint32_t*>(row + kDv * 2) + lane);
     }
+    if (i == 0 && from >= 0) to = row_of(spot, L, tab, status);
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
+    for (int e = 0; e < kStoreAhead; ++e) {
       const int64_t r = __shfl_sync(0xffffffffu, to, i + e);
-      if (f[e] < 0) continue;
+      // largest magnitudes of this lane's two groups: its own 8 dims and its neighbour's
+      const __nv_bfloat162 mine = __nv_bfloat162(top8(x[e][0]), top8(x[e][1]));
+      const __nv_bfloat162 top2 = __hmax2_nan(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+      if (f[e] < 0 || r < 0) continue;
       unsigned char* row = arena + r * kQ4RowBytes;
-      uint32_t scale;
-      const uint2 codes = quantise16(x[e], scale);
-      reinterpret_cast<uint2*>(row)[lane] = codes;
-      row[kQ4ScaleOff + lane] = (unsigned char)scale;
+      const float2 top = __bfloat1622float2(top2);
+      const uint32_t scales = __nv_cvt_float2_to_fp8x2(make_float2(seventh(top.x), seventh(top.y)), __NV_SATFINITE,
+                                                       __NV_E4M3);
+      const float2 s = q4_scales_f32(scales);
+      reinterpret_cast<uint32_t*>(row)[lane] = codes8(x[e][0], s.x, top.x);
+      reinterpret_cast<uint32_t*>(row)[32 + lane] = codes8(x[e][1], s.y, top.y);
+      // an even lane writes the scale of group l / 2, its neighbour that of group 16 + l / 2
+      row[kQ4ScaleOff + 16 * (lane & 1) + (lane >> 1)] = (unsigned char)(lane & 1 ? scales >> 8 : scales);
       reinterpret_cast<uint32_t*>(row + kQ4RopeOff)[lane] = rope[e];
     }
   }
@@ -179,32 +229,35 @@ __global__ void __launch_bounds__(256) read_q4_kernel(Layout L, int32_t shard_be
   const int lane = threadIdx.x & 31;
   const int n = (int)min((int64_t)per_warp, T - t0);
   int64_t from = -1;  // lane: pool row of token t0 + lane
-  if (lane < n) from = held_row(__ldg(pos + t0 + lane), __ldg(req + t0 + lane), L, tab, shard_begin, shard_end, status);
-  for (int i = 0; i < n; i += kAhead) {
-    uint2 codes[kAhead];
-    uint32_t scale[kAhead], rope[kAhead];
-    int64_t f[kAhead];
+  if (lane < n)
+    from = row_of(find_spot(__ldg(pos + t0 + lane), __ldg(req + t0 + lane), L, tab, shard_begin, shard_end, status), L,
+                  tab, status);
+  for (int i = 0; i < n; i += kReadAhead) {
+    uint32_t codes[kReadAhead][2], scales[kReadAhead], rope[kReadAhead];
+    int64_t f[kReadAhead];
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
+    for (int e = 0; e < kReadAhead; ++e) {
       f[e] = __shfl_sync(0xffffffffu, from, i + e);
       if (i + e >= n) f[e] = -1;
       if (f[e] < 0) continue;
       const unsigned char* row = arena + f[e] * kQ4RowBytes;
-      codes[e] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-      scale[e] = __ldg(row + kQ4ScaleOff + lane);
+      codes[e][0] = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
+      codes[e][1] = __ldg(reinterpret_cast<const uint32_t*>(row) + 32 + lane);
+      scales[e] = __ldg(row + kQ4ScaleOff + (lane >> 1)) | (uint32_t)__ldg(row + kQ4ScaleOff + 16 + (lane >> 1)) << 8;
       rope[e] = __ldg(reinterpret_cast<const uint32_t*>(row + kQ4RopeOff) + lane);
     }
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
+    for (int e = 0; e < kReadAhead; ++e) {
       if (f[e] < 0) continue;
-      uint32_t s2[2], off2[2], v[2][4];
-      q4_scales(scale[e], s2, off2);
-      q4_values(codes[e].x, s2[0], off2[0], v[0]);
-      q4_values(codes[e].y, s2[0], off2[0], v[1]);
+      uint32_t s2[2], off2[2];
+      q4_scales(scales[e], s2, off2);
       unsigned char* row = kv + (t0 + i + e) * (kDk * 2);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        reinterpret_cast<uint4*>(row)[2 * lane + j] = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+      for (int j = 0; j < 2; ++j) {
+        uint32_t v[4];
+        q4_values(codes[e][j], s2[j], off2[j], v);
+        reinterpret_cast<uint4*>(row)[32 * j + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
       reinterpret_cast<uint32_t*>(row + kDv * 2)[lane] = rope[e];
     }
   }
