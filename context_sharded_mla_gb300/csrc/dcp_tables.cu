@@ -12,8 +12,9 @@
 // finds its request by bisection of the prefix sums in shared memory.  A long
 // list of tokens goes to a second launch with a thread per token, which bisects
 // cu_tokens.  Everything is integer and every entry has one writer, so the result
-// does not depend on any order.  Latency-bound but for long token lists, which
-// write 32 bytes a token.
+// does not depend on any order.  Latency-bound: 128 requests, 4 tokens each, take
+// 6 us in a captured graph, most of it the block's scan and one dependent load after
+// another; a long list of tokens adds a launch that writes 32 bytes a token.
 #include "dcp_internal.cuh"
 
 using namespace dcp;
@@ -47,28 +48,40 @@ struct Counts {
   int64_t tokens, take, give;
 };
 
+// Request b's lengths and their pages before and after.
+struct Request {
+  int64_t old_len, new_len, old_pages, new_pages;
+};
+
 __device__ __forceinline__ Counts operator+(const Counts& a, const Counts& b) {
   return Counts{a.tokens + b.tokens, a.take + b.take, a.give + b.give};
 }
 
+// Pages of x >= 0 positions, `span` of which share one (32-bit division where it does).
+__device__ __forceinline__ int64_t pages_of(int64_t x, int64_t span) {
+  if (x <= INT32_MAX && span <= INT32_MAX) return (int64_t)(((uint32_t)x + (uint32_t)span - 1) / (uint32_t)span);
+  return x / span + (x % span != 0);
+}
+
 // What request b needs for its new length; *bad gets the status bits of a length
 // that cannot be.
-__device__ __forceinline__ Counts needs(const TableArgs& a, int32_t b, int64_t& old_len, int64_t& new_len, int& bad) {
-  old_len = a.seq_lens[b];
-  new_len = a.new_lens[b];
-  const int64_t span = a.L.N * a.L.P;
+__device__ __forceinline__ Counts needs(const TableArgs& a, int32_t b, Request& q, int& bad) {
+  q = Request{a.seq_lens[b], a.new_lens[b], 0, 0};
   // (a length above 2^62 / B is none either: sums of B lengths stay in 64 bits)
   const int64_t most = (int64_t(1) << 62) / a.B;
-  if (old_len < 0 || new_len < 0 || old_len > most || new_len > most) {
+  if (q.old_len < 0 || q.new_len < 0 || q.old_len > most || q.new_len > most) {
     bad |= DCP_STATUS_BAD_LENGTH;
     return Counts{0, 0, 0};
   }
-  const int64_t po = old_len / span + (old_len % span != 0), pn = new_len / span + (new_len % span != 0);
-  if (po > a.max_pages || pn > a.max_pages) {
+  const int64_t span = a.L.N * a.L.P;
+  q.old_pages = pages_of(q.old_len, span);
+  q.new_pages = pages_of(q.new_len, span);
+  if (q.old_pages > a.max_pages || q.new_pages > a.max_pages) {
     bad |= DCP_STATUS_BAD_PAGE_INDEX;
     return Counts{0, 0, 0};
   }
-  return Counts{max(new_len - old_len, (int64_t)0), max(pn - po, (int64_t)0), max(po - pn, (int64_t)0)};
+  return Counts{max(q.new_len - q.old_len, (int64_t)0), max(q.new_pages - q.old_pages, (int64_t)0),
+                max(q.old_pages - q.new_pages, (int64_t)0)};
 }
 
 __device__ __forceinline__ Counts warp_scan(Counts x, int lane) {
@@ -140,19 +153,21 @@ __device__ __forceinline__ void write_token(const TableArgs& a, int64_t t, int64
 
 __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a) {
   __shared__ Counts sums[32];
-  __shared__ int64_t tok_s[kPlanThreads];   // exclusive prefix sums of the chunk's requests
+  __shared__ int64_t tok_s[kPlanThreads];  // exclusive prefix sums of the chunk's requests
   __shared__ int32_t take_s[kPlanThreads], give_s[kPlanThreads];
-  __shared__ int64_t old_s[kPlanThreads], new_s[kPlanThreads];
+  __shared__ int64_t len_s[kPlanThreads];  // their old lengths
+  __shared__ int64_t keep_s[kPlanThreads];  // the smaller of their old and new pages
   const int tid = threadIdx.x;
-  const int64_t span = a.L.N * a.L.P;
   const int64_t head = a.state[0], count = a.state[1], cap = a.pool_pages;
   int bad = 0;
-  // totals first: the call happens as a whole or not at all
-  Counts need{0, 0, 0}, part;
+  // Totals first: the call happens as a whole or not at all.  (A single chunk of
+  // requests is not looked at again afterwards.)
+  Counts need{0, 0, 0}, x{0, 0, 0}, end{0, 0, 0}, part{0, 0, 0};
+  Request q{0, 0, 0, 0};
   for (int32_t base = 0; base < a.B; base += kPlanThreads) {
     const int32_t b = base + tid;
-    int64_t o, n;
-    block_scan(b < a.B ? needs(a, b, o, n, bad) : Counts{0, 0, 0}, sums, &part);
+    x = b < a.B ? needs(a, b, q, bad) : Counts{0, 0, 0};
+    end = block_scan(x, sums, &part);
     need = need + part;
   }
   if (head < 0 || head >= cap || count < 0 || count > cap || need.give > cap - count)
@@ -165,18 +180,20 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
   Counts done{0, 0, 0};
   for (int32_t base = 0; base < a.B; base += kPlanThreads) {
     const int32_t b = base + tid;
-    int64_t o = 0, n = 0;
-    Counts x{0, 0, 0};
-    if (ok && b < a.B) x = needs(a, b, o, n, bad);
-    const Counts end = block_scan(x, sums, &part);
+    if (!ok) {
+      x = end = part = Counts{0, 0, 0};
+    } else if (a.B > kPlanThreads) {
+      x = b < a.B ? needs(a, b, q, bad) : Counts{0, 0, 0};
+      end = block_scan(x, sums, &part);
+    }
     tok_s[tid] = done.tokens + end.tokens - x.tokens;
     take_s[tid] = (int32_t)(end.take - x.take);   // at most pool_pages
     give_s[tid] = (int32_t)(end.give - x.give);
-    old_s[tid] = o;
-    new_s[tid] = n;
+    len_s[tid] = q.old_len;
+    keep_s[tid] = min(q.old_pages, q.new_pages);
     if (b < a.B) {
       a.cu[b + 1] = done.tokens + end.tokens;
-      if (ok) a.seq_lens[b] = n;
+      if (ok) a.seq_lens[b] = q.new_len;
     }
     __syncthreads();
     const int32_t here = min(kPlanThreads, a.B - base);
@@ -184,14 +201,14 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
     // returned ones do not, so the two never meet.
     for (int64_t i = tid; i < part.take; i += kPlanThreads) {
       const int32_t k = find(take_s, here, i);
-      const int64_t pidx = old_s[k] / span + (old_s[k] % span != 0) + (i - take_s[k]);
+      const int64_t pidx = keep_s[k] + (i - take_s[k]);
       int64_t at = head + done.take + i;
       if (at >= cap) at -= cap;
       a.bt[(int64_t)(base + k) * a.bt_stride + pidx] = a.ring[at];
     }
     for (int64_t i = tid; i < part.give; i += kPlanThreads) {
       const int32_t k = find(give_s, here, i);
-      const int64_t pidx = new_s[k] / span + (new_s[k] % span != 0) + (i - give_s[k]);
+      const int64_t pidx = keep_s[k] + (i - give_s[k]);
       int32_t* entry = a.bt + (int64_t)(base + k) * a.bt_stride + pidx;
       const int32_t page = *entry;
       if (page < 0 || page >= cap) flag(a.status, DCP_STATUS_BAD_PAGE_ID);
@@ -204,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
       __syncthreads();  // the pages just taken
       for (int64_t t = done.tokens + tid; t < done.tokens + part.tokens; t += kPlanThreads) {
         const int32_t k = find(tok_s, here, t);
-        write_token(a, t, old_s[k] + (t - tok_s[k]), base + k);
+        write_token(a, t, len_s[k] + (t - tok_s[k]), base + k);
       }
     }
     done = done + part;
