@@ -7,6 +7,8 @@ summed in fp32 with at most 2u each):
   lse     ds + 2^-20 max(1, |lse|)          (exp2 and log2 approximations, fp32 sums of positive terms)
   o       (2^-8 + 2 ds + 2^-16) sum_p w_p |v_p|, the 2^-8 being the softmax weights' rounding to bf16;
           + 2^-8 |o| for bf16 partials
+          + 2^-110 sum_p |v_p|: a weight is 2^(s - m) in fp32, which is 0 below 2^-126, for a reference m
+          at most 8 off the row's largest score (in powers of two), over a sum of at least 2^-8
 """
 
 import numpy as np
@@ -239,6 +241,7 @@ class Q4State:
                     w /= w.sum(1, keepdims=True)
                     ds = 576 * 2.0 ** -23 * SCALE * (np.abs(q[b, t]) @ np.abs(seen).T).max(1)
                     tol = (2.0 ** -8 + 2 * ds + 2.0 ** -16)[:, None] * (w @ np.abs(seen[:, :512]))
+                    tol = tol + 2.0 ** -110 * np.abs(seen[:, :512]).sum(0)
                     if bf16:
                         tol = tol + 2.0 ** -8 * np.abs(ro)
                     err = np.abs(go - ro)
