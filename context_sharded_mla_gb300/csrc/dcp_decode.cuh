@@ -179,7 +179,12 @@ struct SegIter {
   }
 };
 
-__device__ inline int64_t range_lo(int64_t T, int v, int V) { return (T * v) / V; }
+// First tile of range v of V (32-bit division where it does: a 64-bit one is some
+// hundred instructions, and the fixup makes a chain of them).
+__device__ __forceinline__ int64_t div_tiles(int64_t x, int64_t by) {
+  return ((x | by) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)by) : x / by;
+}
+__device__ inline int64_t range_lo(int64_t T, int v, int V) { return div_tiles(T * v, V); }
 
 // Two fp32 values in one 64-bit register pair, for the packed FP32 operations
 // of sm_100 (two lanes per instruction; each lane rounds as its scalar form).
@@ -335,7 +340,7 @@ __device__ __noinline__ void store_o_rows(const TcArgs& a, uint32_t o_addr, int 
 // serves boundary k (between ranges k and k + 1): the unit containing that
 // boundary's first tile, if the boundary falls inside it and no earlier boundary
 // does (the first boundary inside a unit merges all its pieces).  Blocks per
-// column: up to 12, each taking chunks of 8 query rows; thread 0 builds the
+// column: up to 12, each taking chunks of 8 query rows; the first warp builds the
 // unit's piece list in shared memory, then one warp per row merges the pieces
 // with 16-byte loads and stores (lane l owns dims [16 l, 16 l + 16)).
 constexpr int kFixupThreads = 256;
@@ -393,9 +398,9 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
   const int b = u / a.n_held, rs = u % a.n_held;
   const int64_t s = a.tile_start[u], e = a.tile_start[u + 1];
   const int64_t out_row0 = ((int64_t)rs * a.B + b) * a.R_total;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 32) {
     auto part_of = [&](int64_t x) {  // range containing tile x
-      int vv = (int)((x * V) / T);
+      int vv = (int)div_tiles(x * V, T);
       while (vv + 1 < V && range_lo(T, vv + 1, V) <= x) ++vv;
       while (vv > 0 && range_lo(T, vv, V) > x) --vv;
       return vv;
@@ -403,13 +408,17 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
     const int v0 = part_of(s), v1 = part_of(e - 1);
     int n = 0;
     if (v0 != v1) {
-      for (int vv = v0; vv <= v1 && n < kMaxPieces; ++vv) {
+      for (int base = v0; base <= v1 && n < kMaxPieces; base += 32) {
+        const int vv = base + lane;
         const int64_t rlo = range_lo(T, vv, V);
-        if (rlo == range_lo(T, vv + 1, V)) continue;  // empty range: no piece
-        piece_s[n++] = 2 * vv + (rlo >= s ? 0 : 1);
+        const bool piece = vv <= v1 && rlo != range_lo(T, vv + 1, V);  // an empty range has none
+        const uint32_t with = __ballot_sync(0xffffffffu, piece);
+        const int at = n + __popc(with & ((1u << lane) - 1));
+        if (piece && at < kMaxPieces) piece_s[at] = 2 * vv + (rlo >= s ? 0 : 1);
+        n = min(n + __popc(with), kMaxPieces);
       }
     }
-    npiece_s = n;
+    if (lane == 0) npiece_s = n;
   }
   __syncthreads();
   const int np = npiece_s;
