@@ -469,9 +469,15 @@ def _at(t, name, dtype, shape, dev):
     raise ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
 
 
+# cudaStream_t of a device's current stream: the lookup that torch's own generated code uses where it is there (0.1 us;
+# building a Stream object for it takes 1.1, an eighth of a small call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _raw_stream(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream belongs to {stream.device}, but the current device is cuda:{dev}")
     return stream.cuda_stream
