@@ -50,6 +50,7 @@ struct TcArgs {
   int32_t nraw;                  // raw tiles of a 4-bit cache in flight
   int32_t box_rows;              // KV TMA box height = min(P, 64)
   int64_t pool_rows, pool_pages;
+  int64_t max_rows;              // rows of a unit that are looked at, whatever its length says
   const int32_t* bt;
   int64_t bt_stride, max_pages;
   const int64_t* seq_lens;
@@ -95,8 +96,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(TcArgs a, int32_t* tile_star
     if (u < U) {
       bool bad = false;
       const int b = u / a.n_held, rs = u % a.n_held;
-      const int64_t n = unit_nvis_max(a, b, rs, &bad);
+      int64_t n = unit_nvis_max(a, b, rs, &bad);
       if (bad && rs == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
+      if (n > a.max_rows) {
+        flag(a.status, DCP_STATUS_BAD_PAGE_ID);  // pages past the table
+        n = a.max_rows;
+      }
       t = (int32_t)((n + kTile - 1) / kTile);
       if (t == 0) empty_s[atomicAdd(&n_empty_s, 1)] = u;  // at most 1024 per pass
     }
@@ -672,6 +677,7 @@ TcArgs device_args(const Plan& p, const DecodeCall& c, void* workspace) {
   a.Rg = p.Rg; a.ngroups = p.ngroups; a.V = p.V; a.nts = p.nts; a.nraw = p.nraw; a.box_rows = p.box_rows;
   a.q = static_cast<const __nv_bfloat16*>(c.q);
   a.pool_rows = c.pool_pages * c.layout->page_size; a.pool_pages = c.pool_pages;
+  a.max_rows = INT64_MAX;
   a.bt = c.block_table; a.bt_stride = c.bt_stride; a.max_pages = c.max_pages;
   a.seq_lens = c.seq_lens;
   a.scale_log2 = c.scale * kLog2e;

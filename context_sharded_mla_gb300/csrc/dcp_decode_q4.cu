@@ -128,17 +128,17 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_rest(bar, parity, abort_s));
 }
-// Rows of shard shard_begin + rs below position x (32-bit arithmetic where it
+// Rows of shard shard_begin + rs below position x, as far as the table goes (32-bit arithmetic where it
 // does; a 64-bit division is some hundred instructions).
 __device__ __noinline__ int64_t rows_below_long(const TcArgs& a, int rs, int64_t x) {
   return count_of(a.shard_begin + rs, x, a.L);
 }
 __device__ __forceinline__ int64_t rows_below(const TcArgs& a, int rs, int64_t x) {
   const int64_t span = a.L.N * a.L.I;
-  if (((x | span) >> 31) != 0) return rows_below_long(a, rs, x);
+  if (((x | span) >> 31) != 0) return min(rows_below_long(a, rs, x), a.max_rows);
   const uint32_t I = (uint32_t)a.L.I, n = (uint32_t)x / (uint32_t)span;
   const int32_t rest = (int32_t)((uint32_t)x - n * (uint32_t)span) - (a.shard_begin + rs) * (int32_t)I;
-  return (int64_t)n * I + min(max(rest, 0), (int32_t)I);
+  return min((int64_t)n * I + min(max(rest, 0), (int32_t)I), a.max_rows);
 }
 __device__ __forceinline__ int64_t unit_rows(const TcArgs& a, int32_t u) {
   const int64_t S = a.seq_lens[u / a.n_held];
@@ -946,7 +946,9 @@ extern "C" int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t
   if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, &p)) return DCP_ERR_CUDA;
   rc = check_workspace(p, workspace, workspace_bytes);
   if (rc != DCP_OK) return rc;
-  const TcArgs a = device_args(p, c, workspace);
+  TcArgs a = device_args(p, c, workspace);
+  // a length beyond the table costs no more than the table's pages
+  a.max_rows = std::min(max_pages, (int64_t)INT32_MAX) * layout->page_size;
   const uint64_t rows = (uint64_t)a.n_held * a.pool_rows;
   const uint32_t box = (uint32_t)p.box_rows;
   CUtensorMap tq64, tcode, tscale, trope;

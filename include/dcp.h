@@ -577,7 +577,9 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
- * they hold, NaN included.
+ * they hold, NaN included.  A request whose length needs more than max_pages
+ * pages is flagged (BAD_PAGE_ID) and read as far as the table goes; its outputs
+ * are invalid.
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,

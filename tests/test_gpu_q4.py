@@ -295,6 +295,17 @@ def test_partial_short_length_and_bad_page():
     assert bool(torch.isfinite(st.o).all())
 
 
+@pytest.mark.parametrize("length", [2 * 16 * 13 + 1, 2 ** 40, 2 ** 63 - 1])
+def test_length_beyond_the_table(length):
+    """A request that claims more pages than the table has is flagged; the others are right, and it takes no longer."""
+    st = Q4State([50, 400, 90], 16, 2, 2, 1, 16, seed=33, junk=False)
+    assert st.bt.shape[1] == 13
+    st.lens = [50, length, 90]
+    st.run()
+    assert int(st.status.item()) == 4
+    st.check(reqs=[0, 2], status=4)
+
+
 def test_wide_table_and_spare_columns():
     st = Q4State([300, 20], 8, 1, 2, 1, 8, seed=41, max_pages=100)
     st.run()
