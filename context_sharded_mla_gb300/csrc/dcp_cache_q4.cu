@@ -24,7 +24,7 @@
 // A group is two neighbouring lanes' (one shuffle for its magnitude); the 64 rope
 // dims go through as 4 bytes a lane.  Memory-bound for long lists: 1152 + 416 bytes a
 // token either way; 262143 rows in 72 us written (5.7 TB/s) and 76 us read (5.4 TB/s).
-// A list of a few rows is two or three memory latencies, 4 us in a captured graph.
+// A list of a few rows is two or three memory latencies, 2.7 us in a captured graph.
 #include "dcp_internal.cuh"
 
 using namespace dcp;
@@ -266,7 +266,9 @@ __global__ void __launch_bounds__(256) read_q4_kernel(Layout L, int32_t shard_be
 constexpr int kThreads = 256;  // 8 warps
 
 // Tokens a warp serves: one while the list does not fill the card (4864 warps are
-// 32 on each of 152 SMs), then as many as keep that many warps, up to 32.
+// 32 on each of 152 SMs), then as many as keep that many warps, up to 32.  Writing
+// 3708 rows takes 4.7 us with 1, 5.6 with 8 and 14.8 with 32; 32768 rows 22.2, 11.7
+// and 14.9; 262144 rows 183, 73 and 70.
 int tokens_per_warp(int64_t T) {
   int n = 1;
   while (n < 32 && T > 4864 * (int64_t)n) n *= 2;
