@@ -580,6 +580,18 @@ void plan_groups(int q_len, int H, Plan* p) {
   p->Rg = ((per + 15) / 16) * 16;
 }
 
+// Copy boxes and workspace of a plan whose ranges are set.
+void plan_workspace(const dcp_layout_t* layout, int n_held, int B, int R_total, Plan* p) {
+  const int P = layout->page_size;
+  p->box_rows = P >= kTile ? kTile : P;
+  const int64_t U = (int64_t)B * n_held;
+  p->ws_start_bytes = align256((size_t)(U + 1) * 4);
+  // With one range per row group no unit is cut, so no piece is ever written.
+  p->ws_piece_o_bytes = p->V > 1 ? align256((size_t)2 * p->V * R_total * kDv * 4) : 0;
+  p->ws_piece_lse_bytes = p->V > 1 ? align256((size_t)2 * p->V * R_total * 4) : 0;
+  p->ws_total = p->ws_start_bytes + p->ws_piece_o_bytes + p->ws_piece_lse_bytes;
+}
+
 // Stream-K ranges and workspace of a plan whose groups and shared memory are set.
 bool plan_ranges(const dcp_layout_t* layout, int n_held, int B, int q_len, int H, PairKernel& kernel, Plan* p) {
   const int R_total = q_len * H;
@@ -603,14 +615,7 @@ bool plan_ranges(const dcp_layout_t* layout, int n_held, int B, int q_len, int H
       if (cost(Vc) < 0.95 * cost(best)) best = Vc;
     p->V = best;
   }
-  const int P = layout->page_size;
-  p->box_rows = P >= kTile ? kTile : P;
-  const int64_t U = (int64_t)B * n_held;
-  p->ws_start_bytes = align256((size_t)(U + 1) * 4);
-  // With one range per row group no unit is cut, so no piece is ever written.
-  p->ws_piece_o_bytes = p->V > 1 ? align256((size_t)2 * p->V * R_total * kDv * 4) : 0;
-  p->ws_piece_lse_bytes = p->V > 1 ? align256((size_t)2 * p->V * R_total * 4) : 0;
-  p->ws_total = p->ws_start_bytes + p->ws_piece_o_bytes + p->ws_piece_lse_bytes;
+  plan_workspace(layout, n_held, B, R_total, p);
   return true;
 }
 

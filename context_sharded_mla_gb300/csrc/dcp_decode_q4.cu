@@ -120,10 +120,7 @@ __device__ __noinline__ bool wait_rest(uint64_t* bar, uint32_t parity, volatile 
   return true;
 }
 
-// One thread's wait, and warp-uniform ones (false after an abort).
-__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort_s) {
-  return mbar_try_wait(bar, parity) || wait_rest(bar, parity, abort_s);
-}
+// A warp-uniform wait (false after an abort).
 __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_s) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_rest(bar, parity, abort_s));
@@ -892,11 +889,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+}  // namespace
+
+#include "dcp_decode_q4_few.cuh"
+
+namespace {
+
 // ---------------------------------------------------------------------------- host side
+PairKernel g_few(reinterpret_cast<const void*>(&few_q4_kernel), kFewThreads);
 PairKernel g_kernel(reinterpret_cast<const void*>(&partial_q4_kernel), kThreads);
+
+// Whether a call takes the few-row kernel (its header has both sides' times).
+bool few_rows(int q_len, int H) { return q_len * H <= kFewRows; }
 
 bool make_plan(const dcp_layout_t* layout, int n_held, int B, int q_len, int H, Plan* p) {
   plan_groups(q_len, H, p);
+  if (few_rows(q_len, H)) {
+    const int sms = sm_count_current();
+    if (sms <= 0) return false;
+    p->nts = 0;
+    p->V = 2 * sms;  // two CTAs an SM
+    p->smem = sizeof(FewSmem);
+    plan_workspace(layout, n_held, B, q_len * H, p);
+    return true;
+  }
   p->nts = kMaxSlots;
   p->nraw = (int)((kSmemBudget - smem_layout(p->Rg, p->nts, 0).total) / kRawBytes);
   if (p->nraw > kMaxRaw) p->nraw = kMaxRaw;
@@ -949,6 +965,13 @@ extern "C" int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t
   TcArgs a = device_args(p, c, workspace);
   // a length beyond the table costs no more than the table's pages
   a.max_rows = std::min(max_pages, (int64_t)INT32_MAX) * layout->page_size;
+  if (few_rows(q_len, H)) {
+    if (!g_few.ensure_smem(p.smem)) return DCP_ERR_CUDA;
+    return launch_decode(p, a, kFewThreads, stream, [&](cudaLaunchConfig_t lc) {
+      lc.gridDim = dim3((unsigned)p.V);
+      return cudaLaunchKernelEx(&lc, few_q4_kernel, static_cast<const unsigned char*>(arena), a);
+    });
+  }
   const uint64_t rows = (uint64_t)a.n_held * a.pool_rows;
   const uint32_t box = (uint32_t)p.box_rows;
   CUtensorMap tq64, tcode, tscale, trope;
