@@ -359,43 +359,30 @@ __device__ __forceinline__ int32_t find_unit(const int32_t* start, int32_t U, in
 // serves boundary k (between ranges k and k + 1): the unit containing that
 // boundary's first tile, if the boundary falls inside it and no earlier boundary
 // does (the first boundary inside a unit merges all its pieces).  Blocks per
-// column: up to 12, each taking chunks of 8 query rows; the first warp builds the
-// unit's piece list in shared memory, then one warp per row merges the pieces
-// with 16-byte loads and stores (lane l owns dims [16 l, 16 l + 16)).
+// column: up to 12, each taking chunks of query rows; the first warp builds the
+// unit's piece list in shared memory, then the warps merge the pieces with 16-byte
+// loads and stores, a warp taking kQ quarters (128 dims) of a row and 8 / kQ pieces at
+// a time.  Whole rows (kQ = 4) serve many rows of few pieces: with quarters the blocks
+// are four times as many, 362 us against 348 for 32 requests of 32k tokens and 128
+// heads.  Quarters (kQ = 1) serve at most 16 rows, where one long request's unit has up
+// to 38 pieces and a warp's loads are a chain: 30 us against 48 for one request of 64k
+// tokens and 8 heads.
 constexpr int kFixupThreads = 256;
 constexpr int kMaxPieces = 512;
 
-constexpr int kFixupRows = kFixupThreads / 32;  // query rows per block: one per warp
+constexpr int kFixupWarps = kFixupThreads / 32;
+constexpr int kFixupFewRows = 16;  // most rows that are merged by quarters
 
+template <int kQ>
 __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
+  constexpr int kAhead = 8 / kQ, kParts = kDv / 128 / kQ;
   __shared__ int32_t piece_s[kMaxPieces];
   __shared__ int32_t npiece_s, unit_s;
   griddep_wait();  // a programmatic dependent of the partial kernel: its pieces are complete after this
   const int32_t U = a.B * a.n_held;
   const int V = a.V;
   const int64_t T = a.tile_start[U];
-  const int row0 = blockIdx.y * kFixupRows + (threadIdx.x >> 5);  // this warp's first query row
-  const int row_step = gridDim.y * kFixupRows;
   const int lane = threadIdx.x & 31;
-  auto store_row = [&](int64_t orow, const float (&v)[16]) {
-    if (a.o_bf16) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o_part) + orow * kDv + 16 * lane);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]);
-          w[i] = *reinterpret_cast<uint32_t*>(&t);
-        }
-        dst[h] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o_part) + orow * kDv + 16 * lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-  };
   if (threadIdx.x < 32) {
     const int k = blockIdx.x;
     const int64_t x = range_lo(T, k + 1, V);  // the boundary's first tile
@@ -437,47 +424,59 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
   }
   __syncthreads();
   const int np = npiece_s;
-  for (int row = row0; row < a.R_total; row += row_step) {
-    // Pieces two at a time: both pieces' lse and o loads are issued before
-    // either is used (the row's loads are one latency, not one per piece).
+  const int items = a.R_total * kParts;
+  for (int item = blockIdx.y * kFixupWarps + (threadIdx.x >> 5); item < items; item += gridDim.y * kFixupWarps) {
+    const int row = item / kParts, d = item % kParts * 128 + 4 * lane;  // (kQ = 4: and d + 128, + 256, + 384)
     float m = -INFINITY;
-    for (int k = 0; k < np; ++k) m = fmaxf(m, a.piece_lse[(int64_t)piece_s[k] * a.R_total + row]);
-    float acc[16];
+    for (int k = lane; k < np; k += 32) m = fmaxf(m, a.piece_lse[(int64_t)piece_s[k] * a.R_total + row]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float4 acc[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     float wsum = 0.f;
     if (m != -INFINITY) {
-      for (int k = 0; k < np; k += 2) {
-        const bool two = k + 1 < np;
-        const int64_t pr0 = (int64_t)piece_s[k] * a.R_total + row;
-        const int64_t pr1 = two ? (int64_t)piece_s[k + 1] * a.R_total + row : pr0;
-        const float4* src0 = reinterpret_cast<const float4*>(a.piece_o + pr0 * kDv + 16 * lane);
-        const float4* src1 = reinterpret_cast<const float4*>(a.piece_o + pr1 * kDv + 16 * lane);
-        float4 o0[4], o1[4];
+      for (int base = 0; base < np; base += kAhead) {
+        float4 o[kAhead][kQ];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o0[i] = src0[i];
-          o1[i] = src1[i];
+        for (int i = 0; i < kAhead; ++i) {
+          const float* src = a.piece_o + ((int64_t)piece_s[min(base + i, np - 1)] * a.R_total + row) * kDv + d;
+#pragma unroll
+          for (int q = 0; q < kQ; ++q)
+            o[i][q] = base + i < np ? *reinterpret_cast<const float4*>(src + 128 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float l0 = a.piece_lse[pr0];
-        const float l1 = two ? a.piece_lse[pr1] : -INFINITY;
-        const float w0 = l0 == -INFINITY ? 0.f : exp2f(l0 - m);
-        const float w1 = l1 == -INFINITY ? 0.f : exp2f(l1 - m);
-        wsum += w0 + w1;
+        const float l = lane < kAhead && base + lane < np
+                            ? a.piece_lse[(int64_t)piece_s[base + lane] * a.R_total + row]
+                            : -INFINITY;
+        const float w = l == -INFINITY ? 0.f : exp2f(l - m);  // lane i: piece base + i's
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[4 * i] = fmaf(w1, o1[i].x, fmaf(w0, o0[i].x, acc[4 * i]));
-          acc[4 * i + 1] = fmaf(w1, o1[i].y, fmaf(w0, o0[i].y, acc[4 * i + 1]));
-          acc[4 * i + 2] = fmaf(w1, o1[i].z, fmaf(w0, o0[i].z, acc[4 * i + 2]));
-          acc[4 * i + 3] = fmaf(w1, o1[i].w, fmaf(w0, o0[i].w, acc[4 * i + 3]));
+        for (int i = 0; i < kAhead; i += 2) {
+          const float w0 = __shfl_sync(0xffffffffu, w, i), w1 = __shfl_sync(0xffffffffu, w, i + 1);
+          wsum += w0 + w1;
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            acc[q].x = fmaf(w1, o[i + 1][q].x, fmaf(w0, o[i][q].x, acc[q].x));
+            acc[q].y = fmaf(w1, o[i + 1][q].y, fmaf(w0, o[i][q].y, acc[q].y));
+            acc[q].z = fmaf(w1, o[i + 1][q].z, fmaf(w0, o[i][q].z, acc[q].z));
+            acc[q].w = fmaf(w1, o[i + 1][q].w, fmaf(w0, o[i][q].w, acc[q].w));
+          }
         }
       }
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] *= inv;
-    store_row(out_row0 + row, acc);
-    if (lane == 0) {
+    for (int q = 0; q < kQ; ++q) {
+      const float4 r = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+      const int64_t at = (out_row0 + row) * kDv + d + 128 * q;
+      if (a.o_bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(r.x, r.y), y = __floats2bfloat162_rn(r.z, r.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o_part) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.o_part) + at) = r;
+      }
+    }
+    if (d == 0) {  // lane 0 of the row's first 128 dims
       const float lse2 = wsum > 0.f ? m + log2f(wsum) : -INFINITY;
       a.lse_part[out_row0 + row] = a.base2 ? lse2 : lse2 * kLn2;
     }
@@ -716,18 +715,20 @@ int32_t launch_decode(const Plan& p, const TcArgs& a, int threads, void* stream,
   lc.attrs = pdl;
   lc.numAttrs = 1;
   if (launch_main(lc) != cudaSuccess) return DCP_ERR_CUDA;
-  // Cut units need their pieces merged: one block column per range boundary,
-  // one warp per row up to 96 rows, blocks looping over further row chunks.
-  // With one range per row group nothing is cut and no fixup runs.
+  // Cut units need their pieces merged: one block column per range boundary, blocks
+  // looping over chunks of rows.  With one range per row group nothing is cut and no
+  // fixup runs.
   if (p.V > 1) {
-    const unsigned fix_y = (unsigned)std::min((a.R_total + kFixupRows - 1) / kFixupRows, 12);
+    const bool few = a.R_total <= kFixupFewRows;
+    const int items = few ? a.R_total * (kDv / 128) : a.R_total;
+    const unsigned fix_y = (unsigned)std::min((items + kFixupWarps - 1) / kFixupWarps, 12);
     cudaLaunchConfig_t lf = {};
     lf.gridDim = dim3((unsigned)(p.V - 1), fix_y);
     lf.blockDim = dim3(kFixupThreads);
     lf.stream = st;
     lf.attrs = pdl;
     lf.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lf, fixup_kernel, a) != cudaSuccess) return DCP_ERR_CUDA;
+    if (cudaLaunchKernelEx(&lf, few ? fixup_kernel<1> : fixup_kernel<4>, a) != cudaSuccess) return DCP_ERR_CUDA;
     return launch_status(3);
   }
   return launch_status(2);

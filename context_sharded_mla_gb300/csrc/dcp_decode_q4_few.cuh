@@ -21,7 +21,7 @@
 //
 // Measured with 8 rows against the pair kernel, us (calls in a captured graph): 32
 // requests of 64k tokens 385 / 565, 32 of 4k 42 / 66, 64 of 2k 45 / 80, 16 of 1k 19 / 32;
-// one request of 64k 48 / 41, of 1k 21 / 20 (more ranges to join).  Bound by its own
+// one request of 64k 30 / 41, of 1k 20 / 20.  Bound by its own
 // instructions: 54 % of the issue slots with 16 warps an SM, shared-memory loads 57 %.
 // Two tiles a step share the query's operands, 367 against 381 for the longest, but
 // hold the ring's slots longer: 46 against 45 and 21 against 18.5 for the short ones.
