@@ -260,6 +260,13 @@ CASES = {
     "held": dict(lens=[900, 40, 7], H=40, q_len=2, N=6, I=1, P=128, begin=2, end=5),
     "chunk": dict(lens=[700, 64], H=32, q_len=64, N=2, I=1, P=64, base=1),
     "one-shard": dict(lens=[2500, 63], H=64, q_len=1, N=1, I=1, P=256),
+    # at most 16 query rows: the other kernel
+    "few-verify": dict(lens=[3, 4, 100, 1777], H=5, q_len=3, N=3, I=2, P=32, part_dtype=torch.bfloat16, base=1),
+    "few-held": dict(lens=[900, 40, 7], H=8, q_len=2, N=6, I=1, P=128, begin=2, end=5),
+    "few-one-shard": dict(lens=[5000, 63], H=16, q_len=1, N=1, I=1, P=256),
+    "few-chunk": dict(lens=[700, 64, 65, 16], H=1, q_len=16, N=2, I=1, P=8, base=1),
+    "few-long": dict(lens=[40000, 12345], H=15, q_len=1, N=8, I=1, P=64, part_dtype=torch.bfloat16),
+    "few-same-request": dict(lens=[9000], H=16, q_len=1, N=16, I=16, P=16),
 }
 
 
@@ -273,21 +280,23 @@ def test_partial(name):
     assert torch.equal(first[0], st.o) and torch.equal(first[1], st.lse)
 
 
+@pytest.mark.parametrize("H", [24, 6])
 @pytest.mark.parametrize("kv_scale", [2.0 ** -6, 8.0])
-def test_partial_small_and_large_rows(kv_scale):
+def test_partial_small_and_large_rows(kv_scale, H):
     """Flat softmax, and one that is almost one key (scores of order 100)."""
-    st = Q4State([600, 1300], 24, 2, 4, 1, 16, kv_scale=kv_scale, seed=21)
+    st = Q4State([600, 1300], H, 2, 4, 1, 16, kv_scale=kv_scale, seed=21)
     st.run()
     st.check()
 
 
-def test_partial_short_length_and_bad_page():
-    st = Q4State([50, 2, 400], 16, 4, 2, 1, 16, seed=31)
+@pytest.mark.parametrize("H", [16, 4])
+def test_partial_short_length_and_bad_page(H):
+    st = Q4State([50, 2, 400], H, 4, 2, 1, 16, seed=31)
     st.run()                                # request 1 is shorter than q_len: flagged, empty
     assert int(st.status.item()) == 16
     assert bool((st.o[:, 1] == 0).all()) and bool(torch.isneginf(st.lse[:, 1]).all())
     st.check(reqs=[0, 2], status=16)
-    st = Q4State([50, 90, 400], 16, 1, 2, 1, 16, seed=32, junk=False)
+    st = Q4State([50, 90, 400], 3 * H, 1, 2, 1, 16, seed=32, junk=False)
     st.bt[1, 1] = st.pool
     st.run()
     assert int(st.status.item()) == 4
@@ -295,10 +304,11 @@ def test_partial_short_length_and_bad_page():
     assert bool(torch.isfinite(st.o).all())
 
 
+@pytest.mark.parametrize("H", [16, 8])
 @pytest.mark.parametrize("length", [2 * 16 * 13 + 1, 2 ** 40, 2 ** 63 - 1])
-def test_length_beyond_the_table(length):
+def test_length_beyond_the_table(length, H):
     """A request that claims more pages than the table has is flagged; the others are right, and it takes no longer."""
-    st = Q4State([50, 400, 90], 16, 2, 2, 1, 16, seed=33, junk=False)
+    st = Q4State([50, 400, 90], H, 2, 2, 1, 16, seed=33, junk=False)
     assert st.bt.shape[1] == 13
     st.lens = [50, length, 90]
     st.run()
@@ -343,10 +353,11 @@ def test_partial_on_a_side_stream_and_in_a_graph():
     st.check()
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("H", [16, 8])
+def test_two_streams_at_once(H):
     """Two calls in flight on different streams, each with its own workspace and outputs."""
     a = Q4State([3000, 1000], 96, 1, 4, 1, 64, seed=61)
-    b = Q4State([2500, 1500, 10], 16, 2, 2, 1, 16, seed=62)
+    b = Q4State([2500, 1500, 10], H, 2, 2, 1, 16, seed=62)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     dcp = _dcp()
@@ -364,13 +375,14 @@ def test_two_streams_at_once():
     b.check()
 
 
-def test_rows_past_four_gigabytes():
+@pytest.mark.parametrize("H", [16, 24])
+def test_rows_past_four_gigabytes(H):
     """Pages at the far end of pools of more than 2^32 bytes in all."""
     dcp = _dcp()
     N, P, pool = 2, 64, 90000                        # 2 x 5.76M rows of 416 bytes: 4.8 GB
     lay = dcp.Layout(N, 1, P)
     arena = torch.zeros(N, pool * P, 416, dtype=torch.uint8, device="cuda")
-    S, H = 300, 16
+    S = 300
     bt = torch.tensor([[pool - 1, 5, pool - 2]], dtype=torch.int32, device="cuda")
     rows = random_rows(S, 71)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -59,10 +59,11 @@ def test_running_max_jumps(name, H, q_len):
     st.check()
 
 
-def test_many_short_requests():
+@pytest.mark.parametrize("H", [16, 17])
+def test_many_short_requests(H):
     """More units of work than pairs of CTAs, most of one tile or of none."""
     lens = [int(x) for x in np.random.default_rng(91).integers(1, 140, size=700)]
-    st = Q4State(lens, 16, 1, 4, 1, 8, seed=92)
+    st = Q4State(lens, H, 1, 4, 1, 8, seed=92)
     st.run()
     st.check()
 
