@@ -151,7 +151,8 @@ __device__ __forceinline__ float2 q4_scales_f32(uint32_t two) {
 __device__ __forceinline__ void q4_scales(uint32_t two, uint32_t (&s2)[2], uint32_t (&off2)[2]) {
   const float2 f = q4_scales_f32(two);
   const __nv_bfloat162 a = __float2bfloat162_rn(f.x), b = __float2bfloat162_rn(f.y);
-  const __nv_bfloat162 ao = __float2bfloat162_rn(-136.f * f.x), bo = __float2bfloat162_rn(-136.f * f.y);
+  const __nv_bfloat162 k = __float2bfloat162_rn(-136.f);
+  const __nv_bfloat162 ao = __hmul2(a, k), bo = __hmul2(b, k);
   s2[0] = *reinterpret_cast<const uint32_t*>(&a);
   s2[1] = *reinterpret_cast<const uint32_t*>(&b);
   off2[0] = *reinterpret_cast<const uint32_t*>(&ao);
