@@ -364,14 +364,14 @@ __device__ __forceinline__ int32_t find_unit(const int32_t* start, int32_t U, in
 // loads and stores, a warp taking kQ quarters (128 dims) of a row and 8 / kQ pieces at
 // a time.  Whole rows (kQ = 4) serve many rows of few pieces: with quarters the blocks
 // are four times as many, 362 us against 348 for 32 requests of 32k tokens and 128
-// heads.  Quarters (kQ = 1) serve at most 16 rows, where one long request's unit has up
-// to 38 pieces and a warp's loads are a chain: 30 us against 48 for one request of 64k
-// tokens and 8 heads.
+// heads.  Halves (kQ = 2) serve at most 16 rows, where one long request's unit has up to
+// 38 pieces and a warp's loads are a chain.  Whole rows / halves / quarters, 8 heads:
+// one request of 64k tokens 36 / 31 / 30 us, of 8k 21 / 18 / 18; 64 of 2k 45 / 44 / 48.
 constexpr int kFixupThreads = 256;
 constexpr int kMaxPieces = 512;
 
 constexpr int kFixupWarps = kFixupThreads / 32;
-constexpr int kFixupFewRows = 16;  // most rows that are merged by quarters
+constexpr int kFixupFewRows = 16;  // most rows that are merged by halves
 
 template <int kQ>
 __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
   const int np = npiece_s;
   const int items = a.R_total * kParts;
   for (int item = blockIdx.y * kFixupWarps + (threadIdx.x >> 5); item < items; item += gridDim.y * kFixupWarps) {
-    const int row = item / kParts, d = item % kParts * 128 + 4 * lane;  // (kQ = 4: and d + 128, + 256, + 384)
+    const int row = item / kParts, d = item % kParts * (128 * kQ) + 4 * lane;  // and 128 on for each further quarter
     float m = -INFINITY;
     for (int k = lane; k < np; k += 32) m = fmaxf(m, a.piece_lse[(int64_t)piece_s[k] * a.R_total + row]);
 #pragma unroll
@@ -720,7 +720,7 @@ int32_t launch_decode(const Plan& p, const TcArgs& a, int threads, void* stream,
   // fixup runs.
   if (p.V > 1) {
     const bool few = a.R_total <= kFixupFewRows;
-    const int items = few ? a.R_total * (kDv / 128) : a.R_total;
+    const int items = a.R_total * (few ? 2 : 1);
     const unsigned fix_y = (unsigned)std::min((items + kFixupWarps - 1) / kFixupWarps, 12);
     cudaLaunchConfig_t lf = {};
     lf.gridDim = dim3((unsigned)(p.V - 1), fix_y);
@@ -728,7 +728,7 @@ int32_t launch_decode(const Plan& p, const TcArgs& a, int threads, void* stream,
     lf.stream = st;
     lf.attrs = pdl;
     lf.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lf, few ? fixup_kernel<1> : fixup_kernel<4>, a) != cudaSuccess) return DCP_ERR_CUDA;
+    if (cudaLaunchKernelEx(&lf, few ? fixup_kernel<2> : fixup_kernel<4>, a) != cudaSuccess) return DCP_ERR_CUDA;
     return launch_status(3);
   }
   return launch_status(2);

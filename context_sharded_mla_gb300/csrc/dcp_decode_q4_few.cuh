@@ -20,8 +20,8 @@
 // conflicts at the row stride of 416 bytes, and P's pairs adjacent.
 //
 // Measured with 8 rows against the pair kernel, us (calls in a captured graph): 32
-// requests of 64k tokens 385 / 565, 32 of 4k 42 / 66, 64 of 2k 45 / 80, 16 of 1k 19 / 32;
-// one request of 64k 30 / 41, of 1k 20 / 20.  Bound by its own
+// requests of 64k tokens 382 / 565, 32 of 4k 41 / 66, 64 of 2k 44 / 80, 16 of 1k 17 / 32;
+// one request of 64k 31 / 41, of 1k 20 / 20.  Bound by its own
 // instructions: 54 % of the issue slots with 16 warps an SM, shared-memory loads 57 %.
 // Two tiles a step share the query's operands, 367 against 381 for the longest, but
 // hold the ring's slots longer: 46 against 45 and 21 against 18.5 for the short ones.
