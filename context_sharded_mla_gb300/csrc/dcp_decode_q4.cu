@@ -31,7 +31,8 @@
 // (its warps waited for instructions more than for anything else); 80 KB of code
 // 2620 / 389; fewer instructions in the softmax 2390 / 374; products issued by an
 // elected lane of a converged warp (370 ns for the 18, against 817 from a lane's own
-// branch) 2270 / 358; the next query loaded in whole lines 2290 / 349.  Reading the
+// branch) 2270 / 358; the next query loaded in whole lines 2290 / 349; fewer conversions
+// of scales and a shorter fixup 2282 / 344.  Reading the
 // peer's scores with loads from its shared memory instead of copies (65 bytes a cycle
 // alone) held up the warps' other loads: 3160 / 456.
 //
