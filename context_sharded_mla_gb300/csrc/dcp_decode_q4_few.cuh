@@ -25,8 +25,9 @@
 // instructions: 54 % of the issue slots with 16 warps an SM, shared-memory loads 57 %.
 // Two tiles a step share the query's operands, 367 against 381 for the longest, but
 // hold the ring's slots longer: 46 against 45 and 21 against 18.5 for the short ones.
-// With two sets of 16 rows the operands leave room for one CTA an SM, so 17 rows and
-// more take the pair kernel.
+// With two sets of 16 rows (two slots, the first warp loading) 32 rows took 27 against the
+// pair kernel's 34 for 16 requests of 1k tokens, but 28 against 20 for one of 1k and 338
+// against 310 for 32 of 32k: 17 rows and more take the pair kernel.
 namespace {
 
 constexpr int kFewRows = 16;                       // most query rows
