@@ -35,6 +35,7 @@ constexpr int kSlotBytes = kRopeOff + kRopeHalfBytes;      // 36 KB per tile slo
 constexpr int kHalfRows = 16;                 // rows served by one softmax warp (two threads per row)
 constexpr int kMaxGroupRows = 128;
 constexpr int64_t kMaxQueryRows = 65536;      // q_len * H per request (512 row groups)
+constexpr int64_t kMaxUnitRows = 1 << 30;     // rows of a unit; a pool of more is beyond any card's memory
 constexpr int kXRowBytes = kTile * 4;         // one row of a partial score tile (fp32)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -50,7 +51,7 @@ struct TcArgs {
   int32_t nraw;                  // raw tiles of a 4-bit cache in flight
   int32_t box_rows;              // KV TMA box height = min(P, 64)
   int64_t pool_rows, pool_pages;
-  int64_t max_rows;              // rows of a unit that are looked at, whatever its length says
+  int64_t max_rows;              // rows a unit's table row can hold: no more are looked at, whatever its length says
   const int32_t* bt;
   int64_t bt_stride, max_pages;
   const int64_t* seq_lens;
@@ -632,6 +633,11 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_row
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of a unit that its row of the block table can hold.
+int64_t table_rows(const dcp_layout_t* layout, int64_t max_pages) {
+  return std::min(std::min(max_pages, kMaxUnitRows) * layout->page_size, kMaxUnitRows);
+}
+
 bool page_size_ok(int P) { return P >= 8 && P % 8 == 0 && (P % kTile == 0 || kTile % P == 0); }
 
 // Host checks of a partial decode's arguments (all but the workspace).
@@ -653,6 +659,10 @@ int32_t check_decode_args(const DecodeCall& c) {
   if (n_held * pool_rows >= INT32_MAX || (int64_t)c.B * c.q_len * c.H >= INT32_MAX ||
       (int64_t)c.B * n_held >= INT32_MAX / 2)
     return DCP_ERR_UNSUPPORTED;
+  // The lengths are only known on the device: with every unit as long as its table row, the
+  // planner's sums of tiles stay in 32 bits.
+  const int64_t unit_tiles = (table_rows(c.layout, c.max_pages) + kTile - 1) / kTile;
+  if ((int64_t)c.B * n_held * unit_tiles >= INT32_MAX) return DCP_ERR_UNSUPPORTED;
   return DCP_OK;
 }
 
@@ -681,7 +691,7 @@ TcArgs device_args(const Plan& p, const DecodeCall& c, void* workspace) {
   a.Rg = p.Rg; a.ngroups = p.ngroups; a.V = p.V; a.nts = p.nts; a.nraw = p.nraw; a.box_rows = p.box_rows;
   a.q = static_cast<const __nv_bfloat16*>(c.q);
   a.pool_rows = c.pool_pages * c.layout->page_size; a.pool_pages = c.pool_pages;
-  a.max_rows = INT64_MAX;
+  a.max_rows = table_rows(c.layout, c.max_pages);
   a.bt = c.block_table; a.bt_stride = c.bt_stride; a.max_pages = c.max_pages;
   a.seq_lens = c.seq_lens;
   a.scale_log2 = c.scale * kLog2e;

@@ -963,9 +963,7 @@ extern "C" int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t
   if (!make_plan(layout, shard_end - shard_begin, B, q_len, H, &p)) return DCP_ERR_CUDA;
   rc = check_workspace(p, workspace, workspace_bytes);
   if (rc != DCP_OK) return rc;
-  TcArgs a = device_args(p, c, workspace);
-  // a length beyond the table costs no more than the table's pages
-  a.max_rows = std::min(max_pages, (int64_t)INT32_MAX) * layout->page_size;
+  const TcArgs a = device_args(p, c, workspace);
   if (few_rows(q_len, H)) {
     if (!g_few.ensure_smem(p.smem)) return DCP_ERR_CUDA;
     return launch_decode(p, a, kFewThreads, stream, [&](cudaLaunchConfig_t lc) {

@@ -265,7 +265,11 @@ int32_t dcp_kv_relayout(const dcp_layout_t* layout, int32_t shard_begin, int32_t
  *              and are meaningless after the call
  * Rows of a page past the request's length are read but carry zero weight;
  * they must hold finite values (a zero-initialised pool and dcp_kv_append
- * guarantee that).  Supported: 1 <= H, q_len * H <= 65536, B >= 1.  A large
+ * guarantee that).  A request whose length needs more than max_pages pages is
+ * flagged (BAD_PAGE_ID) and read as far as the table goes; its outputs are
+ * invalid.  Supported: 1 <= H, q_len * H <= 65536, B >= 1, and a table of fewer
+ * than 2^31 tiles of 64 rows over all requests and held shards (B * shards *
+ * max_pages * P / 64; above it DCP_ERR_UNSUPPORTED).  A large
  * q_len is a chunked extend in the all-gather-Q form: the chunk's query tokens
  * attend to every shard's rows exactly as decode tokens do, causally in global
  * positions (vLLM-Ascend "上下文并行（CP）", chunked prefill: the work after
@@ -577,9 +581,7 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
- * they hold, NaN included.  A request whose length needs more than max_pages
- * pages is flagged (BAD_PAGE_ID) and read as far as the table goes; its outputs
- * are invalid.
+ * they hold, NaN included.
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,
