@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kMaThreads, 1)
         for (int p = 0; p < n; ++p) {
           const float l = live ? __ldg(a.lse_part + p * rows + t * a.H + h) : -INFINITY;
           w[p * kMaTok + lane] = l;
-          m = fmaxf(m, l);
+          m = fmax_nan(m, l);
         }
         float z = 0.f;
         for (int p = 0; p < n; ++p) {
@@ -513,9 +513,9 @@ __global__ void __launch_bounds__(kMaThreads, 1)
           w[p * kMaTok + lane] = e;
           z += e;
         }
-        const float inv = z > 0.f ? 1.f / z : 0.f;
+        const float inv = z != 0.f ? 1.f / z : 0.f;  // a NaN stays one
         for (int p = 0; p < n; ++p) w[p * kMaTok + lane] *= inv;
-        if (live && a.lse) a.lse[t * a.H + h] = z > 0.f ? m + (kBase2 ? log2f(z) : logf(z)) : -INFINITY;
+        if (live && a.lse) a.lse[t * a.H + h] = z != 0.f ? m + (kBase2 ? log2f(z) : logf(z)) : -INFINITY;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&g_full[buf]);

@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(256) pack_kernel(int32_t n_held, int32_t T, in
 // sum_{s held} base^(lse_{shard_begin + s} - L) o_part[s] is written, f32, to row
 // (t, h % Hd) of block h / Hd of o_sum [world][T][Hd][512], and L to the same
 // place of lse_out [world][T][Hd].  A row whose shards are all empty gets 0 and
-// -inf; an empty held shard has zero weight and its o row is not read.
+// -inf; an empty held shard has zero weight and its o row is not read.  A NaN among the
+// row's lse makes L NaN, and with it every block of o_sum but those of empty shards.
 template <int kInBf16, int kBase2>
 __global__ void __launch_bounds__(256) rescale_kernel(int32_t n_shards, int32_t shard_begin, int32_t n_held, int32_t T,
                                                       int32_t H, int32_t Hd, const float* __restrict__ lse_all,
@@ -63,9 +64,9 @@ __global__ void __launch_bounds__(256) rescale_kernel(int32_t n_shards, int32_t 
   const int d = h / Hd;
   const int64_t drow = ((int64_t)d * T + t) * Hd + (h - d * Hd);
   float m = -INFINITY;
-  for (int r = lane; r < n_shards; r += 32) m = fmaxf(m, __ldg(lse_all + (int64_t)r * rows + row));
+  for (int r = lane; r < n_shards; r += 32) m = fmax_nan(m, __ldg(lse_all + (int64_t)r * rows + row));
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  for (int s = 16; s > 0; s >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;

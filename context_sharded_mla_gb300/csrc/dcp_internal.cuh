@@ -54,6 +54,14 @@ __device__ inline void flag(int32_t* status, int32_t bit) {
   if (status) atomicOr(status, bit);
 }
 
+// The larger of two values, or NaN if either is one (fmaxf drops it).  A part whose lse
+// is NaN is not an empty part: the merged row has to become NaN.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Counts kernel launches made by this library (reported by dcp_launch_count).
 void note_launches(int64_t n);
 

@@ -56,11 +56,11 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(Parts parts, int32_t n_p
   const int64_t row = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  // pass 1: m = max_r lse_r
+  // pass 1: m = max_r lse_r (NaN if one of them is, and so are the row and its lse then)
   float m = -INFINITY;
-  for (int r = lane; r < n_parts; r += 32) m = fmaxf(m, parts.lse_at(r, row));
+  for (int r = lane; r < n_parts; r += 32) m = fmax_nan(m, parts.lse_at(r, row));
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  for (int s = 16; s > 0; s >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;

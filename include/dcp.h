@@ -309,7 +309,8 @@ size_t dcp_mla_decode_workspace_size(const dcp_layout_t* layout, int32_t shard_b
  *   o        [rows, 512] f32 or bf16 (o_dtype)
  *   lse      f32[rows] in the same base (may be NULL if not wanted)
  * A part with lse = -inf has zero weight; a row whose parts are all -inf gets
- * o = 0 and lse = -inf.  rows == 0 is a no-op.  Errors: DCP_ERR_INVALID.
+ * o = 0 and lse = -inf.  A row with a part whose lse is NaN gets NaN, in o and in
+ * lse.  rows == 0 is a no-op.  Errors: DCP_ERR_INVALID.
  */
 int32_t dcp_lse_merge(int32_t n_parts, int64_t rows, const void* o_part, int32_t o_part_dtype,
                       const float* lse_part, int32_t lse_base, void* o, int32_t o_dtype,
@@ -420,8 +421,8 @@ int32_t dcp_absorb_o(int64_t T, int32_t H, const void* o, int32_t o_dtype, const
  *   lse (out) f32 [T, H], the merged lse in the partials' base (may be NULL)
  *   status    device word (may be NULL); DCP_STATUS_TIMEOUT if a pipeline wait
  *             gave up (v is then invalid)
- * A row whose parts are all empty gives v = 0 and lse = -inf.  T == 0 is a
- * no-op.  Errors: DCP_ERR_INVALID on n_parts outside [1, 64], T < 0, H outside
+ * A row whose parts are all empty gives v = 0 and lse = -inf, one with a part
+ * whose lse is NaN gives NaN.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID on n_parts outside [1, 64], T < 0, H outside
  * [1, 65535], a bad dtype or base, or a null / misaligned (16-byte) pointer.
  */
 int32_t dcp_lse_merge_absorb_o(int32_t n_parts, int64_t T, int32_t H, const void* o_part, int32_t o_part_dtype,
@@ -494,7 +495,9 @@ int32_t dcp_lse_merge_packed(int32_t world, int32_t n_held, int64_t rows, const 
  *             lse); a reduce-scatter (sum) of o_sum over the ranks leaves rank d
  *             the merged o of its heads
  *   lse       (out, may be NULL) f32 [world, T, Hd]: L in the same layout
- * A row whose shards are all empty gets o_sum = 0 and L = -inf.  T == 0 is a
+ * A row whose shards are all empty gets o_sum = 0 and L = -inf.  If the lse of a
+ * shard is NaN, so are L and o_sum's row on every rank with a shard of the row
+ * that is not empty, and with them their sum.  T == 0 is a
  * no-op.  Errors: DCP_ERR_INVALID on bad sizes (shard_begin + n_held >
  * n_shards, H % world != 0, ...), dtype or base, or a null / misaligned pointer.
  */
