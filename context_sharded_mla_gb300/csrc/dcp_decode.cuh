@@ -429,9 +429,9 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
   for (int item = blockIdx.y * kFixupWarps + (threadIdx.x >> 5); item < items; item += gridDim.y * kFixupWarps) {
     const int row = item / kParts, d = item % kParts * (128 * kQ) + 4 * lane;  // and 128 on for each further quarter
     float m = -INFINITY;
-    for (int k = lane; k < np; k += 32) m = fmaxf(m, a.piece_lse[(int64_t)piece_s[k] * a.R_total + row]);
+    for (int k = lane; k < np; k += 32) m = fmax_nan(m, a.piece_lse[(int64_t)piece_s[k] * a.R_total + row]);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    for (int x = 16; x > 0; x >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
     float4 acc[kQ];
 #pragma unroll
     for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
         }
       }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;  // a NaN stays one
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       const float4 r = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kFixupThreads) fixup_kernel(TcArgs a) {
       }
     }
     if (d == 0) {  // lane 0 of the row's first 128 dims
-      const float lse2 = wsum > 0.f ? m + log2f(wsum) : -INFINITY;
+      const float lse2 = wsum != 0.f ? m + log2f(wsum) : -INFINITY;
       a.lse_part[out_row0 + row] = a.base2 ? lse2 : lse2 * kLn2;
     }
   }

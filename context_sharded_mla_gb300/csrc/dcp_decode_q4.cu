@@ -843,13 +843,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool writes = row < rows_here;
         const int64_t out_base = ((int64_t)rs * a.B + b) * a.R_total + g * Rg;
         const int64_t piece_base = (int64_t)(2 * v + kslot) * a.R_total + g * Rg;
-        const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+        const float inv = l_row != 0.f ? 1.f / l_row : 0.f;  // 0: no key seen; a NaN stays one
         // staging for the output rows: this warp's part of the buffer the last tile's
         // peer scores were read from
         store_rows_q4(a, tmem + lane_addr + kOCol, rows_here, whole, out_base, piece_base, r0, 256 * (int)rank + 128 * h,
                       inv, s_own + ((jl & 1) ? 0u : sl.sbuf));
         if (writes && h == 0 && rank == 0) {
-          const float lse2 = l_row > 0.f ? m_ref + log2f(l_row) : -INFINITY;
+          const float lse2 = l_row != 0.f ? m_ref + log2f(l_row) : -INFINITY;
           if (whole)
             a.lse_part[out_base + row] = a.base2 ? lse2 : lse2 * kLn2;
           else

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_q4_kernel(const unsigned c
         const float4 x = *reinterpret_cast<const float4*>(&sm.lsum[row][0]);
         const float4 y = *reinterpret_cast<const float4*>(&sm.lsum[row][4]);
         const float l_row = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
-        const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+        const float inv = l_row != 0.f ? 1.f / l_row : 0.f;  // 0: no key seen; a NaN stays one
         const int d0 = 64 * w + 16 * t;
         if (whole && a.o_bf16) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o_part) + (out_base + row) * kDv + d0);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_q4_kernel(const unsigned c
                                            o[4 * i + 2][2 * h + c] * inv, o[4 * i + 3][2 * h + c] * inv);
         }
         if (w == 0 && t == 0) {
-          const float lse2 = l_row > 0.f ? m_ref[h] + log2f(l_row) : -INFINITY;
+          const float lse2 = l_row != 0.f ? m_ref[h] + log2f(l_row) : -INFINITY;
           if (whole)
             a.lse_part[out_base + row] = a.base2 ? lse2 : lse2 * kLn2;
           else

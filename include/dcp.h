@@ -422,8 +422,9 @@ int32_t dcp_absorb_o(int64_t T, int32_t H, const void* o, int32_t o_dtype, const
  *   status    device word (may be NULL); DCP_STATUS_TIMEOUT if a pipeline wait
  *             gave up (v is then invalid)
  * A row whose parts are all empty gives v = 0 and lse = -inf, one with a part
- * whose lse is NaN gives NaN.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID on n_parts outside [1, 64], T < 0, H outside
- * [1, 65535], a bad dtype or base, or a null / misaligned (16-byte) pointer.
+ * whose lse is NaN gives NaN.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID on
+ * n_parts outside [1, 64], T < 0, H outside [1, 65535], a bad dtype or base, or a
+ * null / misaligned (16-byte) pointer.
  */
 int32_t dcp_lse_merge_absorb_o(int32_t n_parts, int64_t T, int32_t H, const void* o_part, int32_t o_part_dtype,
                                const float* lse_part, int32_t lse_base, const void* w_vc, void* v, int32_t v_dtype,
@@ -497,9 +498,9 @@ int32_t dcp_lse_merge_packed(int32_t world, int32_t n_held, int64_t rows, const 
  *   lse       (out, may be NULL) f32 [world, T, Hd]: L in the same layout
  * A row whose shards are all empty gets o_sum = 0 and L = -inf.  If the lse of a
  * shard is NaN, so are L and o_sum's row on every rank with a shard of the row
- * that is not empty, and with them their sum.  T == 0 is a
- * no-op.  Errors: DCP_ERR_INVALID on bad sizes (shard_begin + n_held >
- * n_shards, H % world != 0, ...), dtype or base, or a null / misaligned pointer.
+ * that is not empty, and with them their sum.  T == 0 is a no-op.  Errors:
+ * DCP_ERR_INVALID on bad sizes (shard_begin + n_held > n_shards, H % world != 0,
+ * ...), dtype or base, or a null / misaligned pointer.
  */
 int32_t dcp_lse_rescale(int32_t n_shards, int32_t shard_begin, int32_t n_held, int32_t T, int32_t H, int32_t world,
                         const float* lse_all, const void* o_part, int32_t o_part_dtype, int32_t lse_base,
@@ -584,7 +585,8 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
- * they hold, NaN included.
+ * they hold, NaN included; a NaN among the rows a query row sees, or in the query
+ * row itself, makes its o and lse NaN.
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,

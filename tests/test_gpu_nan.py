@@ -123,3 +123,81 @@ def test_merge_absorb(n, T, H, base):
         outs.append((v, l))
     for clean, got in zip(*outs):
         compare(clean, got, bad)
+
+
+# ---------------------------------------------------------------- partial decodes
+def runs(st, spoil):
+    """(o, lse) of a Q4State without and with what `spoil` writes into its arena or query."""
+    out = []
+    for bad in (False, True):
+        if bad:
+            spoil(st)
+        st.o.fill_(5.0)
+        st.lse.fill_(5.0)
+        st.run()
+        assert int(st.status.item()) == 0
+        out.append((st.o.clone(), st.lse.clone()))
+    return out
+
+
+def slot_of(st, b, p):
+    """(held shard, pool row) of position p of request b."""
+    from oracle import layout
+    r, row = int(layout.owner(p, st.N, st.I)), int(layout.local_row(p, st.N, st.I))
+    return r, int(st.bt[b][row // st.P]) * st.P + row % st.P
+
+
+# byte of a cached row: a scale of each CTA's half of the dims, rope dims of each half
+PLACES = {"first scale": (256, 0x7F), "last scale": (287, 0xFF), "rope": (288 + 1, 0x7F), "last rope": (288 + 127, 0xFF)}
+
+
+@pytest.mark.parametrize("place", list(PLACES))
+@pytest.mark.parametrize("H,q_len", [(16, 1), (17, 1), (128, 1), (96, 3), (5, 2)])
+@pytest.mark.parametrize("N,lens,at", [
+    (1, [700], [(0, 699)]),                                     # one shard, the newest key
+    (1, [9000, 300, 77], [(0, 5), (0, 8990), (2, 40)]),         # units cut by range boundaries
+    (4, [3000, 61, 4], [(0, 1001), (1, 0), (2, 1)]),
+])
+def test_q4_visible_nan(N, lens, at, H, q_len, place):
+    from test_gpu_q4 import Q4State
+    st = Q4State(lens, H, q_len, N, 1, 64, seed=7 + H, base=1)
+    byte, value = PLACES[place]
+
+    def spoil(st):
+        for b, p in at:
+            r, row = slot_of(st, b, p)
+            st.arena[r, row, byte] = value
+            if byte >= 288:                                     # a bf16 NaN: exponent bits and a mantissa bit
+                st.arena[r, row, byte - 1] = 0xC0
+
+    (o, lse), (o2, lse2) = runs(st, spoil)
+    bad = torch.zeros(o.shape[:-1], dtype=torch.bool)
+    for b, p in at:
+        for t in range(q_len):
+            if p <= lens[b] - q_len + t:
+                bad[slot_of(st, b, p)[0], b, t] = True
+    seen = [(b, p) for b, p in at if p <= lens[b] - q_len]      # by every query token
+    for t in range(q_len):                                      # (a key that only later tokens see: see below)
+        if len(seen) == len(at):
+            compare(o[:, :, t], o2[:, :, t], bad[:, :, t])
+            compare(lse[:, :, t], lse2[:, :, t], bad[:, :, t])
+        else:
+            assert bool(torch.isnan(o2[:, :, t][bad[:, :, t]]).all()) and bool(torch.isnan(lse2[:, :, t][bad[:, :, t]]).all())
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("H,q_len", [(16, 1), (17, 1), (128, 2)])
+def test_q4_nan_and_infinite_queries(H, q_len, value):
+    """A query row with a NaN, or whose scores are all infinite or NaN, is NaN; the rows beside it are not."""
+    from test_gpu_q4 import Q4State
+    st = Q4State([4000, 90], H, q_len, 2, 1, 64, seed=3)
+
+    def spoil(st):
+        st.q[0, 0, 3, 17] = value
+        st.q[1, q_len - 1, H - 1, 575] = value
+
+    (o, lse), (o2, lse2) = runs(st, spoil)
+    bad = torch.zeros(o.shape[:-1], dtype=torch.bool)
+    bad[:, 0, 0, 3] = bad[:, 1, q_len - 1, H - 1] = True
+    compare(o, o2, bad)
+    compare(lse, lse2, bad)
