@@ -738,13 +738,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int64_t out_base = ((int64_t)rs * a.B + b) * a.R_total + g * Rg;
         const int64_t piece_base = (int64_t)(2 * v + kslot) * a.R_total + g * Rg;
         const int64_t out_row = out_base + row, piece_row = piece_base + row;
-        const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+        const float inv = l_row != 0.f ? 1.f / l_row : 0.f;  // 0: no key seen; a NaN stays one
         // staging for the fp32 rows: this warp's rows of the buffer the last tile's
         // peer scores were read from
         store_o_rows(a, tmem + lane_addr + kOCol, rows_here, whole, out_base, piece_base, r0, 256 * (int)rank + 128 * h,
                      inv, smem_u32(x_s) + ((jl & 1) ^ 1) * sl.xbuf + (uint32_t)r0 * kXRowBytes);
         if (writes && h == 0 && rank == 0) {
-          const float lse2 = l_row > 0.f ? m_ref + log2f(l_row) : -INFINITY;
+          const float lse2 = l_row != 0.f ? m_ref + log2f(l_row) : -INFINITY;
           if (whole)
             a.lse_part[out_row] = a.base2 ? lse2 : lse2 * kLn2;
           else

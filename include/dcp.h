@@ -253,6 +253,8 @@ int32_t dcp_kv_relayout(const dcp_layout_t* layout, int32_t shard_begin, int32_t
  *   lse_r   = ln sum_{p in V_r} exp(s_p)      (log2 of the same sum if lse_base == 1)
  *   o_r     = sum_{p in V_r} exp(s_p - lse_e) * k_p[0:512]
  *   V_r empty -> lse_r = -inf, o_r = 0.
+ * A NaN among the rows a query row sees, or in the query row itself, makes its
+ * lse_r and o_r NaN.
  *
  *   q          bf16[B, q_len, H, 576]
  *   arena      bf16[shard_end - shard_begin, pool_pages * P, 576]
@@ -585,8 +587,7 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
- * they hold, NaN included; a NaN among the rows a query row sees, or in the query
- * row itself, makes its o and lse NaN.
+ * they hold, NaN included.
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,

@@ -201,3 +201,30 @@ def test_q4_nan_and_infinite_queries(H, q_len, value):
     bad[:, 0, 0, 3] = bad[:, 1, q_len - 1, H - 1] = True
     compare(o, o2, bad)
     compare(lse, lse2, bad)
+
+
+@pytest.mark.parametrize("dim", [0, 300, 530, 575])
+@pytest.mark.parametrize("name,over", [
+    ("tiny", dict(B=3, S=700, H=7)), ("k3", dict(B=2, S=9000)), ("dsv3", dict(B=2, S=5000)), ("ragged", dict(B=3, S=3000, S_min=400)),
+])
+def test_bf16_visible_nan(name, over, dim):
+    """The same in the bf16 cache; a NaN in a query row as well."""
+    import workloads
+    from harness import GpuState
+    from oracle import layout
+    st = GpuState(workloads.config(name, **over))
+    cfg, d = st.cfg, st.dec
+    outs, bad = [], torch.zeros(cfg.N, cfg.B, cfg.q_len, cfg.H, dtype=torch.bool)
+    for spoil in (False, True):
+        if spoil:
+            for b, p in ((0, 5), (1, int(st.S[1]) - cfg.q_len)):       # seen by every query token
+                r, row = int(layout.owner(p, cfg.N, cfg.I)), int(layout.local_row(p, cfg.N, cfg.I))
+                d.arena[r, int(st.bt[b, row // cfg.P]) * cfg.P + row % cfg.P, dim] = NAN
+                bad[r, b] = True
+            st.q[cfg.B - 1, 0, 2, dim] = NAN
+            bad[:, cfg.B - 1, 0, 2] = True
+        o, lse = st.decode()
+        outs.append((d.o_part.clone(), d.lse_part.clone(), o.clone(), lse.clone()))
+        assert d.status_bits() == 0
+    for clean, got, rows in zip(*outs, (bad, bad, bad.any(0), bad.any(0))):
+        compare(clean, got, rows)
