@@ -143,6 +143,15 @@ __device__ __forceinline__ int64_t unit_rows(const TcArgs& a, int32_t u) {
   return S < a.q_len ? 0 : rows_below(a, u % a.n_held, S);
 }
 
+// Which of a dequantising warp's two 8-row groups of tile j are on a bad page (bits 0 and 1),
+// or ~0 after an abort.  For a whole warp; out of line because only NaN scores ask for it.
+__device__ __noinline__ uint32_t bad_groups(uint64_t* full, const unsigned char* flags, uint32_t j, uint32_t nts,
+                                            volatile int* abort_s) {
+  const uint32_t ts = j % nts;
+  if (!all_wait(full + ts, (j / nts) & 1, abort_s)) return ~0u;  // has passed: the scores are there
+  return flags[kDequantWarps * ts];
+}
+
 constexpr float kNoRef = -1e30f;  // a row that has seen no key: 2^(s - kNoRef) is only formed for s = -inf
 
 // 2^d for a whole number d <= 8, exactly; 0 below 2^-126.
@@ -229,6 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   RawRows* raw_rows = reinterpret_cast<RawRows*>(smem + sl.rows);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + sl.misc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + sl.misc + 4);
+  // [slot][dequantising warp]: bit e, the warp's 8-row group e of the tile is on a bad page
+  unsigned char* tile_flags = smem + sl.misc + 16;
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -387,6 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const RawRows& rr = raw_rows[m];
       const uint32_t src = smem_u32(raw) + m * kRawBytes;
       const int32_t y = lane < nbox ? rr.y[lane] : -1;  // lane q: first pool row of box q
+      // the warp's 8-row groups that are below the length but on a bad page
+      const uint32_t bad = (kDequantRows * w < rr.valid && rr.y[box0] < 0 ? 1u : 0u) |
+                           (kDequantRows * w + 8 < rr.valid && rr.y[box1] < 0 ? 2u : 0u);
       // the tile's values, ready in registers before its slot is free
       uint32_t x[4][4][4];
 #pragma unroll
@@ -422,6 +436,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           st_shared_v4(dst + (uint32_t)((4 * (piece & 1) + k) ^ r8) * 16, x[e][k][0], x[e][k][1], x[e][k][2], x[e][k][3]);
+      }
+      if (lane == 0) tile_flags[kDequantWarps * ts + w] = (unsigned char)bad;
+      if (bad != 0) {
+        // No copy brings the rope dims of a bad page: NaN there makes the keys' scores NaN,
+        // which is what the softmax looks at the flags for.
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (bad >> e & 1)
+            st_shared_v4(smem_u32(slot) + kRopeOff + (uint32_t)(kDequantRows * w + 8 * e) * 64 + 16 * lane, ~0u, ~0u, ~0u,
+                         ~0u);
       }
       fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
       __syncwarp();
@@ -756,17 +780,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 16; ++k)
               if (k >= lim) s[k] = __float_as_uint(-INFINITY);
           }
-          float mx = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])), my = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
+          float mx = fmax_nan(__uint_as_float(s[0]), __uint_as_float(s[1]));
+          float my = fmax_nan(__uint_as_float(s[2]), __uint_as_float(s[3]));
 #pragma unroll
           for (int k = 4; k < 16; k += 4) {
-            mx = fmax3(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-            my = fmax3(my, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+            mx = fmax3_nan(mx, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+            my = fmax3_nan(my, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
           }
-          mx = fmaxf(mx, my);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));  // the row's other 16 keys
-          const float mt = mx * a.scale_log2;  // scale > 0: the max commutes with the scaling
-          const bool raise = mt > m_ref + kRescaleThreshold;     // also the row's first visible key
+          mx = fmax_nan(mx, my);
+          mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));  // the row's other 16 keys
+          float mt = mx * a.scale_log2;  // scale > 0: the max commutes with the scaling
+          bool raise = !(mt <= m_ref + kRescaleThreshold);  // also the row's first visible key, and NaN
           if (__any_sync(0xffffffffu, raise)) {
+            if (__any_sync(0xffffffffu, mx != mx)) {
+              // Keys on a bad page leave the softmax; the maximum is that of the rest, without
+              // the NaN that the cache or the query holds.
+              const uint32_t bad = bad_groups(&bars[kTFull], tile_flags + 2 * rank + h, j, nts, abort_s);
+              if (bad == ~0u) { ok = false; break; }
+              mx = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                if (bad >> (k >> 3) & 1) s[k] = __float_as_uint(-INFINITY);
+                mx = fmaxf(mx, __uint_as_float(s[k]));
+              }
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              mt = mx * a.scale_log2;
+              raise = mt > m_ref + kRescaleThreshold;
+            }
             float alpha = 1.f;
             if (raise) {
               const float m_new = ceilf(mt);

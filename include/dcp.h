@@ -277,7 +277,8 @@ int32_t dcp_kv_relayout(const dcp_layout_t* layout, int32_t shard_begin, int32_t
  * positions (vLLM-Ascend "上下文并行（CP）", chunked prefill: the work after
  * gathering Q is the decode work).
  * Errors: DCP_ERR_INVALID on bad sizes/pointers/dtype/base, DCP_ERR_WORKSPACE
- * if the workspace is too small.  Device status: BAD_LENGTH, BAD_PAGE_ID.
+ * if the workspace is too small.  Device status: BAD_LENGTH, BAD_PAGE_ID (a
+ * block-table entry outside the pool: that request's outputs are invalid).
  */
 int32_t dcp_mla_decode_partial(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                const void* q, int32_t B, int32_t q_len, int32_t H,
@@ -587,7 +588,8 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * page sizes, masks, device status, errors) is dcp_mla_decode_partial's, with
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
- * they hold, NaN included.
+ * they hold, NaN included, and neither do rows below it whose block-table entry
+ * lies outside the pool (BAD_PAGE_ID).
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,
