@@ -152,6 +152,31 @@ __device__ __noinline__ uint32_t bad_groups(uint64_t* full, const unsigned char*
   return flags[kDequantWarps * ts];
 }
 
+// NaN among eight e4m3 scales (all bits below the sign set): not 0.
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t a, uint32_t b) {
+  return (((a & 0x7F7F7F7Fu) + 0x01010101u) | ((b & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+}
+
+// The NaN values of a tile become 0, by a whole warp, between the tile's two products.  A
+// NaN scale has made the scores of its key NaN, and so the weight in every row that sees the
+// key; a row that does not has weight 0, which a NaN value would still turn into NaN.
+__device__ __noinline__ void zero_nan_values(uint32_t slot) {
+#pragma unroll 1
+  for (uint32_t at = slot + 16 * (threadIdx.x & 31); at < slot + kRopeOff; at += 512) {
+    const uint4 v = ld_shared_v4(at);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+      const uint32_t num = __heq2_mask(x, x);  // 0 in the half of a NaN
+      w[i] &= num;
+    }
+    st_shared_v4(at, w[0], w[1], w[2], w[3]);
+  }
+  fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
+  __syncwarp();
+}
+
 constexpr float kNoRef = -1e30f;  // a row that has seen no key: 2^(s - kNoRef) is only formed for s = -inf
 
 // 2^d for a whole number d <= 8, exactly; 0 below 2^-126.
@@ -238,7 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   RawRows* raw_rows = reinterpret_cast<RawRows*>(smem + sl.rows);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + sl.misc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + sl.misc + 4);
-  // [slot][dequantising warp]: bit e, the warp's 8-row group e of the tile is on a bad page
+  // [slot][dequantising warp], about the warp's 16 rows of the tile: bit e, its 8-row group e is on a
+  // bad page; bit 2, a scale among them is NaN
   unsigned char* tile_flags = smem + sl.misc + 16;
 
   const int tid = threadIdx.x;
@@ -402,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bad = (kDequantRows * w < rr.valid && rr.y[box0] < 0 ? 1u : 0u) |
                            (kDequantRows * w + 8 < rr.valid && rr.y[box1] < 0 ? 2u : 0u);
       // the tile's values, ready in registers before its slot is free
-      uint32_t x[4][4][4];
+      uint32_t x[4][4][4], scales[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = kDequantRows * w + 8 * (e >> 1) + r8;
@@ -411,12 +437,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint4 code = ld_shared_v4(src + (uint32_t)row * 128 + (uint32_t)((piece ^ r8) << 4));
         const uint32_t two = ld_shared_u16(src + kRawCodeBytes + (uint32_t)row * 16 + 2 * piece);
         uint32_t s2[2], o2[2];
+        scales[e] = two;
         q4_scales(live ? two : 0u, s2, o2);
         q4_values(code.x, s2[0], o2[0], x[e][0]);
         q4_values(code.y, s2[0], o2[0], x[e][1]);
         q4_values(code.z, s2[1], o2[1], x[e][2]);
         q4_values(code.w, s2[1], o2[1], x[e][3]);
       }
+      // (rows that do not count may say so, too: their values are 0 already)
+      const uint32_t nan = e4m3_nans(scales[0] | scales[1] << 16, scales[2] | scales[3] << 16);
+      const uint32_t flags = bad | (__any_sync(0xffffffffu, nan != 0) ? 4u : 0u);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kREmpty + m]);
       if (!all_wait(&bars[kTEmpty + ts], tphase ^ 1, abort_s)) { ok = false; break; }
@@ -437,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k)
           st_shared_v4(dst + (uint32_t)((4 * (piece & 1) + k) ^ r8) * 16, x[e][k][0], x[e][k][1], x[e][k][2], x[e][k][3]);
       }
-      if (lane == 0) tile_flags[kDequantWarps * ts + w] = (unsigned char)bad;
+      if (lane == 0) tile_flags[kDequantWarps * ts + w] = (unsigned char)flags;
       if (bad != 0) {
         // No copy brings the rope dims of a bad page: NaN there makes the keys' scores NaN,
         // which is what the softmax looks at the flags for.
@@ -533,19 +563,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       it.init(a.tile_start, U, lo, hi);
       int32_t u, t0, nt, ks;
       bool wh;
-      uint32_t j = 0, ts = 0;
+      uint32_t j = 0, ts = 0, tphase = 0;
       int seg = 0;
       bool ok = true;
       while (ok && it.next(&u, &t0, &nt, &wh, &ks)) {
 #pragma unroll 1
         for (int jj = 0; jj < nt; ++jj, ++j) {
-          // P(j) ready; the first product of a segment also needs the previous
-          // segment's O read out
+          // the tile's flags; P(j) ready; the first product of a segment also needs the
+          // previous segment's O read out
+          if (!all_wait(&bars[kTFull + ts], tphase, abort_s)) { ok = false; break; }
+          const uint32_t flags = *reinterpret_cast<const volatile uint32_t*>(tile_flags + kDequantWarps * ts);
           if (!all_wait(&bars[kPFull + (j & 1)], (j >> 1) & 1, abort_s) ||
               (jj == 0 && seg >= 1 && !all_wait(&bars[kOFree], (seg - 1) & 1, abort_s))) {
             ok = false;
             break;
           }
+          if (flags & 0x04040404u) zero_nan_values(smem_u32(ring) + ts * kSlotBytes);
           tc_fence_after();
           if (elect_one()) {
             const uint32_t pa = tmem + kPCol + 32 * (j & 1);  // P(j): 64 bf16 = 32 columns
@@ -557,7 +590,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma_commit(&bars[kPVDone + (j & 1)]);
           }
           __syncwarp();
-          if (++ts == (uint32_t)nts) ts = 0;
+          if (++ts == (uint32_t)nts) {
+            ts = 0;
+            tphase ^= 1;
+          }
         }
         ++seg;
       }

@@ -245,29 +245,48 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_q4_kernel(const unsigned c
         float mx[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(s[2 * h], s[2 * h + 1]);
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+          mx[h] = fmax_nan(s[2 * h], s[2 * h + 1]);
+          mx[h] = fmax_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmax_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
           if (t == 0) sm.wmax[g + 8 * h][w] = mx[h];
           lim[h] -= kTile;
         }
         few_sync();
         // ---- P
         float alpha[2];
-        bool raised = false;
+        bool raised = false, nan = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float4 x = *reinterpret_cast<const float4*>(&sm.wmax[g + 8 * h][0]);
           const float4 y = *reinterpret_cast<const float4*>(&sm.wmax[g + 8 * h][4]);
-          const float mt = fmaxf(fmax3(fmax3(x.x, x.y, x.z), x.w, y.x), fmax3(y.y, y.z, y.w)) * a.scale_log2;
+          const float mt =
+              fmax_nan(fmax3_nan(fmax3_nan(x.x, x.y, x.z), x.w, y.x), fmax3_nan(y.y, y.z, y.w)) * a.scale_log2;
           alpha[h] = 1.f;
-          if (mt > m_ref[h] + kRescaleThreshold) {  // also the row's first visible key
-            alpha[h] = exp2f(m_ref[h] - mt);
-            m_ref[h] = mt;
+          if (!(mt <= m_ref[h] + kRescaleThreshold)) {  // also the row's first visible key, and NaN
             raised = true;
+            if (mt == mt) {
+              alpha[h] = exp2f(m_ref[h] - mt);
+              m_ref[h] = mt;
+            } else {
+              nan = true;
+            }
           }
         }
         if (__any_sync(0xffffffffu, raised)) {
+          // A NaN scale has made its key's score NaN in every row that sees the key (the last row sees
+          // every live key, so all warps meet it here); it becomes 0 for the rows that do not, whose
+          // weight 0 a NaN value would still turn into NaN.
+          if (__any_sync(0xffffffffu, nan)) {
+            const uint32_t at = tile_s + (8 * w + (lane >> 2)) * kQ4RowBytes + kQ4ScaleOff + 8 * t;
+            const float2 two = ld_shared_f32x2(at);
+            const uint32_t lo = __float_as_uint(two.x), hi = __float_as_uint(two.y);
+            // 0xFF in the bytes that are NaN (all bits below the sign set)
+            const uint32_t bad_lo = __vcmpeq4(lo & 0x7F7F7F7Fu, 0x7F7F7F7Fu), bad_hi = __vcmpeq4(hi & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (bad_lo | bad_hi) {
+              st_shared_f32x2(at, __uint_as_float(lo & ~bad_lo), __uint_as_float(hi & ~bad_hi));
+              fence_proxy_async_smem();  // before the next copy into the slot
+            }
+          }
           l[0] *= alpha[0];
           l[1] *= alpha[1];
 #pragma unroll

@@ -266,8 +266,9 @@ int32_t dcp_kv_relayout(const dcp_layout_t* layout, int32_t shard_begin, int32_t
  *              bytes, 256-byte aligned; its contents need not be initialised
  *              and are meaningless after the call
  * Rows of a page past the request's length are read but carry zero weight;
- * they must hold finite values (a zero-initialised pool and dcp_kv_append
- * guarantee that).  A request whose length needs more than max_pages pages is
+ * they must hold finite values (a zero-initialised pool and dcp_kv_append of
+ * finite rows guarantee that), and so must rows that only later query tokens of
+ * the call see.  A request whose length needs more than max_pages pages is
  * flagged (BAD_PAGE_ID) and read as far as the table goes; its outputs are
  * invalid.  Supported: 1 <= H, q_len * H <= 65536, B >= 1, and a table of fewer
  * than 2^31 tiles of 64 rows over all requests and held shards (B * shards *
@@ -589,7 +590,8 @@ int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t 
  * the 4-bit arena and a workspace of dcp_mla_decode_workspace_size_q4(...)
  * bytes.  Rows of a page past the request's length carry no weight whatever
  * they hold, NaN included, and neither do rows below it whose block-table entry
- * lies outside the pool (BAD_PAGE_ID).
+ * lies outside the pool (BAD_PAGE_ID).  A row that only later query tokens of the
+ * call see does nothing to the earlier ones, NaN or not.
  */
 int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                                   const void* q, int32_t B, int32_t q_len, int32_t H,

@@ -228,3 +228,31 @@ def test_bf16_visible_nan(name, over, dim):
         assert d.status_bits() == 0
     for clean, got, rows in zip(*outs, (bad, bad, bad.any(0), bad.any(0))):
         compare(clean, got, rows)
+
+
+@pytest.mark.parametrize("place", list(PLACES))
+@pytest.mark.parametrize("H,q_len", [(8, 2), (1, 16), (5, 3), (6, 3), (9, 7), (128, 4), (16, 64), (96, 5)])
+@pytest.mark.parametrize("N,lens", [(1, [700, 64]), (1, [9000, 130, 65]), (4, [3000, 261, 68])])
+def test_q4_nan_that_only_later_tokens_see(N, lens, H, q_len, place):
+    """Draft tokens' rows hold NaN: the query tokens before them keep their bits, the others are NaN."""
+    from test_gpu_q4 import Q4State
+    st = Q4State(lens, H, q_len, N, 1, 16, seed=9 + H, base=1)
+    byte, value = PLACES[place]
+    at = [(b, S - 1 - k) for b, S in enumerate(lens) for k in ((0,), (q_len - 2,), (q_len // 2, 0))[b % 3]]
+
+    def spoil(st):
+        for b, p in at:
+            r, row = slot_of(st, b, p)
+            st.arena[r, row, byte] = value
+            if byte >= 288:
+                st.arena[r, row, byte - 1] = 0xC0
+
+    (o, lse), (o2, lse2) = runs(st, spoil)
+    bad = torch.zeros(o.shape[:-1], dtype=torch.bool)
+    for b, p in at:
+        for t in range(q_len):
+            if p <= lens[b] - q_len + t:
+                bad[slot_of(st, b, p)[0], b, t] = True
+    assert bool(bad.any()) and not bool(bad.all())
+    compare(o, o2, bad)
+    compare(lse, lse2, bad)
