@@ -62,7 +62,7 @@ struct Spot {
 // token, or a bad one (flagged).
 __device__ __forceinline__ Spot find_spot(int64_t p, int32_t b, const Layout& L, const Table& t, int32_t shard_begin,
                                           int32_t shard_end, int32_t* status) {
-  if (p == -1 && b == -1) return Spot{-1, -1, 0};
+  if (is_padding(p, b)) return Spot{-1, -1, 0};
   if (p < 0 || b < 0 || b >= t.B) {
     flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
     return Spot{-1, -1, 0};

@@ -50,6 +50,9 @@ inline Layout to_layout(const dcp_layout_t* l) {
   return Layout{l->n_shards, l->interleave, l->page_size};
 }
 
+// An entry of a token list behind its last token (dcp_block_tables fills lists up with them).
+__device__ __forceinline__ bool is_padding(int64_t pos, int32_t req) { return pos == -1 && req == -1; }
+
 __device__ inline void flag(int32_t* status, int32_t bit) {
   if (status) atomicOr(status, bit);
 }

@@ -56,7 +56,7 @@ __global__ void slot_map_kernel(Layout L, const int64_t* __restrict__ pos,
   const int32_t b = req[t];
   int64_t own = -1, r = -1, s = -1;
   if (p < 0) {
-    flag(status, DCP_STATUS_BAD_POSITION);
+    if (!is_padding(p, b)) flag(status, DCP_STATUS_BAD_POSITION);
   } else {
     own = owner_of(p, L);
     r = local_row_of(p, L);
@@ -94,6 +94,7 @@ __global__ void kv_append_kernel(Layout L, int32_t shard_begin, int32_t shard_en
   if (t >= T) return;
   const int64_t p = __ldg(pos + t);
   const int32_t b = __ldg(req + t);
+  if (is_padding(p, b)) return;
   if (p < 0 || b < 0 || b >= B) {
     if (lane == 0) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
     return;
@@ -145,6 +146,7 @@ __global__ void kv_relayout_kernel(Layout L, int32_t shard_begin, int32_t shard_
   if (t >= T) return;
   const int64_t p = __ldg(pos + t);
   const int32_t b = __ldg(req + t);
+  if (is_padding(p, b)) return;
   if (p < 0 || b < 0 || b >= B) {
     if (lane == 0) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
     return;

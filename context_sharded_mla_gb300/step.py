@@ -97,12 +97,13 @@ class ShardedMlaDecoder:
 
 
 class BlockTables:
-    """Lengths, block table and free pages of B requests, all on the device.
+    """Lengths, block table and free pages of B requests, all on the device, for either cache.
 
     ``update(new_lens)`` moves the requests to their new lengths and fills ``pos``
     and ``req`` (``max_tokens`` entries; -1 behind the last new token) and
     ``cu_tokens``; ``block_table`` and ``seq_lens`` are what the append and the
-    partial decode read.  With max_tokens 0 no tokens are listed."""
+    partial decode read.  The padded lists go to the append as they are, with as many
+    rows (those behind the last token are not read).  With max_tokens 0 no tokens are listed."""
 
     def __init__(self, layout: Layout, B: int, pool_pages: int, max_pages: int, max_tokens: int, device="cuda"):
         dev = torch.device(device)

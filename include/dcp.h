@@ -51,6 +51,9 @@
  *    length the block table cannot hold) OR a DCP_STATUS_* bit into the
  *    caller's device word `*status` and skip the offending read or write.
  *    `status` is sticky: the library never clears it.  No kernel traps.
+ *  - In a list of tokens (pos, req), an entry with pos == -1 and req == -1 is
+ *    padding: it is skipped without a status bit (dcp_slot_map writes owner, row
+ *    and slot -1 for it).  dcp_block_tables fills its lists up with such entries.
  *  - bf16 means IEEE bfloat16 stored as 16-bit words; f32 is IEEE binary32.
  *  - Tensors are dense and row-major ("C order") in the shapes given.
  *
@@ -138,7 +141,7 @@ int64_t dcp_count(const dcp_layout_t* layout, int32_t shard, int64_t x);
  * "Decode context parallelism", "Virtual KV layout" (one shared block table;
  * a widened page of N*P positions maps to one physical page on every shard).
  *
- *   pos          int64[T]  request-global positions (>= 0)
+ *   pos          int64[T]  request-global positions (>= 0; -1 with req -1: padding)
  *   req          int32[T]  request index of each token, in [0, B)
  *   block_table  int32[B, bt_stride]; entry [b][k] is the physical page (same
  *                id on every shard) holding local rows [k*P, (k+1)*P) of b;
@@ -182,9 +185,10 @@ int32_t dcp_slot_map(const dcp_layout_t* layout, const int64_t* pos, const int32
  * + row % P with row = (pos / (N*I)) * I + pos % I; tokens of other shards are
  * skipped (another device holds them) and their block-table entries are not
  * read.  Device status: a negative position (BAD_POSITION) or a request outside
- * [0, B) (BAD_REQUEST) is flagged for any token; a local row past max_pages
- * (BAD_PAGE_INDEX) or a page id outside [0, pool_pages) (BAD_PAGE_ID) for a
- * held token; each skips only that token.  T == 0 is a no-op.  Errors:
+ * [0, B) (BAD_REQUEST) is flagged for any token that is no padding; a local row
+ * past max_pages (BAD_PAGE_INDEX) or a page id outside [0, pool_pages)
+ * (BAD_PAGE_ID) for a held token; each skips only that token.  T == 0 is a no-op.
+ * Errors:
  * DCP_ERR_INVALID for a bad layout or shard range, T < 0, B < 1, max_pages
  * outside [1, bt_stride], pool_pages < 1, a null pointer with T > 0, or kv_new
  * / arena not 16-byte aligned.
@@ -541,9 +545,7 @@ enum { DCP_Q4_ROW_BYTES = 416 };
  * dcp_kv_append_q4 — owner-filtered write of new latent rows into a 4-bit cache.
  *
  * Arguments, placement, device status and errors as dcp_kv_append, with the
- * 4-bit arena.  One addition: an entry with pos == -1 and req == -1 is padding
- * (dcp_block_tables writes it behind the last token) and is skipped without a
- * status bit.  A (pos, req) pair must appear once at most: two rows written to
+ * 4-bit arena.  A (pos, req) pair must appear once at most: two rows written to
  * one slot by the same call leave either of them or a mixture.
  */
 int32_t dcp_kv_append_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
@@ -555,7 +557,7 @@ int32_t dcp_kv_append_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_
  * dcp_kv_relayout_q4 — prefill-to-decode relayout into a 4-bit cache: the rows
  * of a paged bf16 prefill pool, quantised into their owners' pools.  Arguments,
  * placement, device status and errors as dcp_kv_relayout, with the 4-bit arena;
- * padding entries and repeated pairs as for dcp_kv_append_q4.
+ * repeated pairs as for dcp_kv_append_q4.
  */
 int32_t dcp_kv_relayout_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
                            const void* src_pool, int64_t src_pool_rows, int32_t src_page_size,
