@@ -108,6 +108,12 @@ __device__ __forceinline__ float reciprocal(float s) {  // within 1 ulp
   return r;
 }
 
+// Quotients from here on are clamped before they are rounded.  x / s is at most 7.46875 or
+// at least 7.5 (8 significant bits over 4), so the limit is one between the two that a
+// reciprocal one ulp off cannot cross.  (7.5 itself is crossed: it would become code 8, in
+// the next dim's bits.)
+constexpr float kClampFrom = 7.499f;
+
 // The word of codes of 8 bf16 values under scale s, whose group's largest magnitude is
 // `top`.  A sum with kSnap ends at a multiple of 2^-11, one with kInt at a whole number
 // that its low mantissa bits hold as code + 8.
@@ -117,7 +123,7 @@ __device__ __forceinline__ uint32_t codes8(const uint4& x, float s, float top) {
   const float inv = reciprocal(s);
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
   // only a scale that was clamped, or is one of the few smallest, leaves |x / s| above 7.5
-  const bool clamp = !(top * inv < 7.5f);
+  const bool clamp = !(top * inv < kClampFrom);
   uint32_t w = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
