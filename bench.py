@@ -781,21 +781,40 @@ def run_e2e(args, cfg, st, dist, acct):
                        "the device computes; every copy runs every step inside the timed region"}
 
 
+def source_hash(path):
+    """First 16 hex digits of the sha256 of a kernel's source and, after it, the headers beside it that it includes
+    (and those that they include), each once, in the order of their first #include."""
+    import hashlib
+    import re
+    todo, seen, h = [os.path.abspath(path)], set(), hashlib.sha256()
+    while todo:
+        src = todo.pop(0)
+        if src in seen:
+            continue
+        seen.add(src)
+        with open(src, "rb") as f:
+            text = f.read()
+        h.update(text)
+        for name in re.findall(rb'^[ \t]*#[ \t]*include[ \t]+"([^"/]+)"', text, re.M):
+            header = os.path.join(os.path.dirname(src), name.decode())
+            if os.path.exists(header):
+                todo.append(header)
+    return h.hexdigest()[:16]
+
+
 def recorded_traffic(key):
-    """DRAM bytes per launch of a kernel from a committed ncu summary, if it matches the current source."""
+    """DRAM bytes per launch of a kernel from a committed ncu summary, if it matches the current source (headers too)."""
     path = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(path):
         return None
     try:
         with open(path) as f:
             rec = json.load(f)
-        import hashlib
         entry = rec.get(key)
         if not entry:
             return None
         src = os.path.join(ROOT, entry.get("source", "context_sharded_mla_gb300/csrc/dcp_decode.cu"))
-        h = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
-        if entry.get("source_sha") != h:
+        if entry.get("source_sha") != source_hash(src):
             return None
         scale = entry.get("scale_to_full", 1.0)
         return int(entry["dram_bytes_per_launch"] * scale)
