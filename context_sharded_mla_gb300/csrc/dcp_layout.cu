@@ -94,9 +94,8 @@ __global__ void kv_append_kernel(Layout L, int32_t shard_begin, int32_t shard_en
   if (t >= T) return;
   const int64_t p = __ldg(pos + t);
   const int32_t b = __ldg(req + t);
-  if (is_padding(p, b)) return;
   if (p < 0 || b < 0 || b >= B) {
-    if (lane == 0) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
+    if (lane == 0 && !is_padding(p, b)) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
     return;
   }
   int64_t own, row;
@@ -146,9 +145,8 @@ __global__ void kv_relayout_kernel(Layout L, int32_t shard_begin, int32_t shard_
   if (t >= T) return;
   const int64_t p = __ldg(pos + t);
   const int32_t b = __ldg(req + t);
-  if (is_padding(p, b)) return;
   if (p < 0 || b < 0 || b >= B) {
-    if (lane == 0) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
+    if (lane == 0 && !is_padding(p, b)) flag(status, p < 0 ? DCP_STATUS_BAD_POSITION : DCP_STATUS_BAD_REQUEST);
     return;
   }
   int64_t own, row, src_pidx, src_off;
