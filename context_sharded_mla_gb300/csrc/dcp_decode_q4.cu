@@ -981,7 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 namespace {
 
 // ---------------------------------------------------------------------------- host side
-PairKernel g_few(reinterpret_cast<const void*>(&few_q4_kernel), kFewThreads);
+SmemLimit g_few_smem;
 PairKernel g_kernel(reinterpret_cast<const void*>(&partial_q4_kernel), kThreads);
 
 // Whether a call takes the few-row kernel (its header has both sides' times).
@@ -1049,7 +1049,7 @@ extern "C" int32_t dcp_mla_decode_partial_q4(const dcp_layout_t* layout, int32_t
   if (rc != DCP_OK) return rc;
   const TcArgs a = device_args(p, c, workspace);
   if (few_rows(q_len, H)) {
-    if (!g_few.ensure_smem(p.smem)) return DCP_ERR_CUDA;
+    if (!g_few_smem.ensure(reinterpret_cast<const void*>(&few_q4_kernel), p.smem)) return DCP_ERR_CUDA;
     return launch_decode(p, a, kFewThreads, stream, [&](cudaLaunchConfig_t lc) {
       lc.gridDim = dim3((unsigned)p.V);
       return cudaLaunchKernelEx(&lc, few_q4_kernel, static_cast<const unsigned char*>(arena), a);

@@ -259,6 +259,12 @@ int32_t dcp_kv_relayout(const dcp_layout_t* layout, int32_t shard_begin, int32_t
  *   V_r empty -> lse_r = -inf, o_r = 0.
  * A NaN among the rows a query row sees, or in the query row itself, makes its
  * lse_r and o_r NaN.
+ * Precision: both products multiply bf16 by bf16 and add in f32; scores, maxima,
+ * sums and o are f32.  The weights exp(s_p - m) are rounded to bf16 before they
+ * multiply the values (o is off by up to 2^-8 sum_p w_p |v_p| from that, w_p the
+ * normalised weights), while their sum, and with it lse, takes them unrounded.
+ * Scores are meant to stay below 2^24 in magnitude, where f32 still tells 1 from
+ * 0; from about 2^30 on a weight may overflow and the row become NaN.
  *
  *   q          bf16[B, q_len, H, 576]
  *   arena      bf16[shard_end - shard_begin, pool_pages * P, 576]
