@@ -32,7 +32,7 @@
 // 2620 / 389; fewer instructions in the softmax 2390 / 374; products issued by an
 // elected lane of a converged warp (370 ns for the 18, against 817 from a lane's own
 // branch) 2270 / 358; the next query loaded in whole lines 2290 / 349; fewer conversions
-// of scales and a shorter fixup 2282 / 344.  Reading the
+// of scales and a shorter fixup 2285 / 343; bad pages and NaN told apart 2294 / 344.  Reading the
 // peer's scores with loads from its shared memory instead of copies (65 bytes a cycle
 // alone) held up the warps' other loads: 3160 / 456.
 //
@@ -40,8 +40,9 @@
 //   0-7    softmax, exchange, epilogue (16 rows each, two threads per row)
 //   8-11   dequantise: warp 8 + w turns rows [16 w, 16 w + 16) of a raw tile into
 //          the 128-byte-swizzled bf16 chunks both products read; a row past the
-//          request's length or on a bad page is written as zeros.  Warp 8 also
-//          loads the tile's rope dims (bf16 in the cache) by TMA.
+//          request's length or on a bad page is written as zeros, and what the
+//          softmax has to know of bad pages is marked.  Warp 8 also loads the
+//          tile's rope dims (bf16 in the cache) by TMA.
 //   12     producer: page table, raw tiles
 //   13     QK issuer (and loader of the query's rope operand), TMEM owner
 //   14     PV issuer

@@ -19,15 +19,16 @@
 // same; the orders here make every load of the codes a run of 8 or 4 bytes without bank
 // conflicts at the row stride of 416 bytes, and P's pairs adjacent.
 //
-// Measured with 8 rows against the pair kernel, us (calls in a captured graph): 32
-// requests of 64k tokens 382 / 565, 32 of 4k 41 / 66, 64 of 2k 44 / 80, 16 of 1k 17 / 32;
-// one request of 64k 31 / 41, of 1k 20 / 20.  Bound by its own
-// instructions: 54 % of the issue slots with 16 warps an SM, shared-memory loads 57 %.
-// Two tiles a step share the query's operands, 367 against 381 for the longest, but
-// hold the ring's slots longer: 46 against 45 and 21 against 18.5 for the short ones.
-// With two sets of 16 rows (two slots, the first warp loading) 32 rows took 27 against the
-// pair kernel's 34 for 16 requests of 1k tokens, but 28 against 20 for one of 1k and 338
-// against 310 for 32 of 32k: 17 rows and more take the pair kernel.
+// Measured with 8 rows against the pair kernel, us (calls in a captured graph, caches of
+// quantised N(0, 1) rows): 32 requests of 64k tokens 383 / 533, 32 of 4k 43 / 66, 64 of 2k
+// 45 / 76, 16 of 1k 20 / 33; one request of 64k 34 / 39, of 8k 20.5 / 22.5, of 1k 22.5 /
+// 20.5.  Bound by its own instructions: 55 % of the issue slots with 16 warps an SM,
+// shared-memory loads 55 %.
+// Variants, on a cache of zeros.  Two tiles a step share the query's operands, 367 against
+// 381 for the longest, but hold the ring's slots longer: 46 against 45 and 21 against 18.5
+// for the short ones.  With two sets of 16 rows (two slots, the first warp loading) 32 rows
+// took 27 against the pair kernel's 34 for 16 requests of 1k tokens, but 28 against 20 for
+// one of 1k and 338 against 310 for 32 of 32k: 17 rows and more take the pair kernel.
 namespace {
 
 constexpr int kFewRows = 16;                       // most query rows

@@ -103,7 +103,8 @@ class BlockTables:
     and ``req`` (``max_tokens`` entries; -1 behind the last new token) and
     ``cu_tokens``; ``block_table`` and ``seq_lens`` are what the append and the
     partial decode read.  The padded lists go to the append as they are, with as many
-    rows (those behind the last token are not read).  With max_tokens 0 no tokens are listed."""
+    rows (those behind the last token are not read).  With max_tokens 0 no tokens are listed.
+    A request of length 0 has o = 0 and lse = -inf in the decode, which flags it BAD_LENGTH."""
 
     def __init__(self, layout: Layout, B: int, pool_pages: int, max_pages: int, max_tokens: int, device="cuda"):
         dev = torch.device(device)
