@@ -13,7 +13,9 @@ Functions (same names as the C ABI):
   dcp_absorb_o, dcp_lse_merge_absorb_o, dcp_a2a_chunk_bytes, dcp_pack_partials,
   dcp_lse_merge_packed, dcp_lse_rescale, dcp_kv_append_q4, dcp_kv_relayout_q4,
   dcp_kv_read_q4, dcp_mla_decode_partial_q4, dcp_mla_decode_workspace_size_q4,
-  dcp_block_tables
+  dcp_block_tables, dcp_q_norm_rope, dcp_kv_norm_rope_append, dcp_kv_norm_rope_append_q4,
+  dcp_mla_key_weights, dcp_mla_key_weights_q4, dcp_evict_select, dcp_kv_compact,
+  dcp_kv_compact_q4
 """
 
 from __future__ import annotations
@@ -33,13 +35,16 @@ __all__ = [
     "dcp_a2a_chunk_bytes", "dcp_pack_partials", "dcp_lse_merge_packed", "dcp_lse_rescale", "dcp_lse_merge_absorb_o",
     "dcp_kv_append_q4", "dcp_kv_relayout_q4", "dcp_kv_read_q4", "dcp_mla_decode_partial_q4",
     "dcp_mla_decode_workspace_size_q4", "dcp_block_tables", "Q4_ROW_BYTES",
-    "DCP_LSE_BASE_E", "DCP_LSE_BASE_2", "DCP_F32", "DCP_BF16", "STATUS_BITS",
+    "dcp_q_norm_rope", "dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4", "dcp_mla_key_weights",
+    "dcp_mla_key_weights_q4", "dcp_evict_select", "dcp_kv_compact", "dcp_kv_compact_q4",
+    "DCP_LSE_BASE_E", "DCP_LSE_BASE_2", "DCP_F32", "DCP_BF16", "DCP_ROPE_PAIRS", "DCP_ROPE_HALVES", "STATUS_BITS",
 ]
 
 DCP_OK, DCP_ERR_INVALID, DCP_ERR_UNSUPPORTED, DCP_ERR_CUDA, DCP_ERR_WORKSPACE = 0, -1, -2, -3, -4
 DCP_ERR_TOO_LARGE = -5
 DCP_LSE_BASE_E, DCP_LSE_BASE_2 = 0, 1
 DCP_F32, DCP_BF16 = 0, 1
+DCP_ROPE_PAIRS, DCP_ROPE_HALVES = 0, 1   # position dims that rotate together: (2i, 2i + 1) or (i, i + 32)
 STATUS_BITS = {1: "BAD_POSITION", 2: "BAD_PAGE_INDEX", 4: "BAD_PAGE_ID", 8: "BAD_REQUEST", 16: "BAD_LENGTH",
                32: "TIMEOUT", 64: "INTERNAL", 128: "NO_PAGES", 256: "TOO_MANY_TOKENS", 512: "BAD_POOL"}
 Q4_ROW_BYTES = 416   # one latent row of a 4-bit cache
@@ -96,7 +101,17 @@ _SIGNATURES = {
                                          _P, _F, _I32, _P, _I32, _P, _P, _SZ, _P, _P]),
     "dcp_mla_decode_workspace_size_q4": (_SZ, [_LP, _I32, _I32, _I32, _I32, _I32]),
     "dcp_block_tables": (_I32, [_LP, _I32, _P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "dcp_q_norm_rope": (_I32, [_I64, _I32, _P, _I64, _P, _P, _I32, _F, _P, _I32, _P, _P, _P]),
+    "dcp_evict_select": (_I32, [_LP, _I32, _I32, _I32, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P]),
 }
+for _name in ("dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4"):
+    _SIGNATURES[_name] = (_I32, [_LP, _I32, _I32, _P, _I64, _P, _I32, _F, _P, _I32, _P, _P, _P, _I64, _P, _I32, _I64,
+                                 _I64, _P, _I64, _P, _P])
+for _name in ("dcp_mla_key_weights", "dcp_mla_key_weights_q4"):
+    _SIGNATURES[_name] = (_I32, [_LP, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _P, _I64, _I64, _P, _F, _I32, _P,
+                                 _P, _F, _P, _I64, _P, _P])
+for _name in ("dcp_kv_compact", "dcp_kv_compact_q4"):
+    _SIGNATURES[_name] = (_I32, [_LP, _I32, _I32, _P, _I64, _I32, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P])
 
 
 def library_path() -> str:
@@ -601,3 +616,172 @@ def dcp_block_tables(layout, seq_lens, new_lens, block_table, max_pages, free_pa
         _at(cu_tokens, "cu_tokens", torch.int64, (B + 1,), dev), _at(status, "status", torch.int32, (1,), dev),
         _raw_stream(stream, dev))
     _check("dcp_block_tables", rc)
+
+
+def _strided(t, name, width, dev):
+    """(address, row stride in elements) of a bf16 view [..., width] on the current device with equally strided rows."""
+    stride = _rows(t, name, width)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr(), stride
+
+
+def _gamma(gamma, width, dev):
+    """(address, dtype code) of optional norm weights."""
+    if gamma is None:
+        return None, DCP_BF16
+    return _at(gamma, "gamma", gamma.dtype, (width,), dev), _dtype_code(gamma)
+
+
+def dcp_q_norm_rope(q, pos, out, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, status=None,
+                    stream=None):
+    """out [T, H, 192] bf16 = q [T, H, 192], each head's 192 dims RMS-normed (gamma [192]; None: no norm) and its last 64
+    rotated by pos [T] times inv_freq f32 [32] (None: no rotation).  q may be a view with equally strided rows; out may
+    be q.  Rows of tokens with pos -1 are left as they are."""
+    dev = torch.cuda.current_device()
+    if not isinstance(out, torch.Tensor) or out.dim() != 3:
+        raise ValueError("out must be [T, H, 192]")
+    T, H, _ = out.shape
+    at_q, stride = _strided(q, "q", 192, dev)
+    if q.shape != out.shape:
+        raise ValueError(f"q must have out's shape {tuple(out.shape)}, got {tuple(q.shape)}")
+    at_gamma, code = _gamma(gamma, 192, dev)
+    rc = load_library().dcp_q_norm_rope(
+        T, H, at_q, stride, _at(pos, "pos", torch.int64, (T,), dev), at_gamma, code, eps,
+        None if inv_freq is None else _at(inv_freq, "inv_freq", torch.float32, (32,), dev), rope_style,
+        _at(out, "out", torch.bfloat16, (T, H, 192), dev),
+        None if status is None else _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check("dcp_q_norm_rope", rc)
+
+
+def _norm_rope_append(name, width, dtype, layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena,
+                      pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos, stream):
+    dev = torch.cuda.current_device()
+    T = pos.numel()
+    B, stride = _table(block_table, "block_table")
+    at_kv, kv_stride = _strided(kv, "kv", 576, dev)
+    if kv.shape != (T, 576):
+        raise ValueError(f"kv must have shape {(T, 576)}, got {tuple(kv.shape)}")
+    at_gamma, code = _gamma(gamma, 512, dev)
+    rc = getattr(load_library(), name)(
+        layout, shard_begin, shard_end, at_kv, kv_stride, at_gamma, code, eps,
+        None if inv_freq is None else _at(inv_freq, "inv_freq", torch.float32, (32,), dev), rope_style,
+        None if rope_pos is None else _at(rope_pos, "rope_pos", torch.int64, (T,), dev),
+        _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T,
+        _at(block_table, "block_table", torch.int32, None, dev), B, stride, max_pages,
+        _at(arena, "arena", dtype, (shard_end - shard_begin, pool_pages * layout.page_size, width), dev), pool_pages,
+        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check(name, rc)
+
+
+def dcp_kv_norm_rope_append(layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena, pool_pages,
+                            status, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, rope_pos=None,
+                            stream=None):
+    """dcp_kv_append of a projection's rows kv [T, 576] bf16 (a view with equally strided rows): dims [0, 512) RMS-normed
+    (gamma [512]; None: no norm), dims [512, 576) rotated by rope_pos (None: pos) times inv_freq f32 [32] (None: no
+    rotation), rounded once and written into their owners' pools."""
+    _norm_rope_append("dcp_kv_norm_rope_append", 576, torch.bfloat16, layout, shard_begin, shard_end, kv, pos, req,
+                      block_table, max_pages, arena, pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos,
+                      stream)
+
+
+def dcp_kv_norm_rope_append_q4(layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena, pool_pages,
+                               status, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, rope_pos=None,
+                               stream=None):
+    """dcp_kv_norm_rope_append into a 4-bit arena [shards, pool_pages*P, 416] uint8."""
+    _norm_rope_append("dcp_kv_norm_rope_append_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, kv, pos,
+                      req, block_table, max_pages, arena, pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos,
+                      stream)
+
+
+def _key_weights(name, width, dtype, layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages,
+                 seq_lens, scale, lse_base, lse, weights, status, old_lens, decay, stream):
+    dev = torch.cuda.current_device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B, q_len, H, 576]")
+    B, q_len, H, _ = q.shape
+    n = shard_end - shard_begin
+    if _table(block_table, "block_table")[0] != B:
+        raise ValueError("block_table must have one row per request")
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3 or weights.shape[:2] != (n, B):
+        raise ValueError(f"weights must be [{n}, {B}, max_pages * P or more]")
+    rc = getattr(load_library(), name)(
+        layout, shard_begin, shard_end, _at(q, "q", torch.bfloat16, (B, q_len, H, 576), dev), B, q_len, H,
+        _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
+        _at(block_table, "block_table", torch.int32, None, dev), block_table.shape[1], max_pages,
+        _at(seq_lens, "seq_lens", torch.int64, (B,), dev), scale, lse_base,
+        _at(lse, "lse", torch.float32, (B, q_len, H), dev),
+        None if old_lens is None else _at(old_lens, "old_lens", torch.int64, (B,), dev), decay,
+        _at(weights, "weights", torch.float32, None, dev), weights.shape[2],
+        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check(name, rc)
+
+
+def dcp_mla_key_weights(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale,
+                        lse_base, lse, weights, status, old_lens=None, decay=1.0, stream=None):
+    """weights [shards, B, >= max_pages * P] f32: to every cached row the softmax weight that the queries q [B, q_len, H,
+    576] give it under their merged lse [B, q_len, H], summed over them, is added; rows at positions below old_lens (int64
+    [B]; None: 0) keep decay times what they had, the others start from 0."""
+    _key_weights("dcp_mla_key_weights", 576, torch.bfloat16, layout, shard_begin, shard_end, q, arena, pool_pages,
+                 block_table, max_pages, seq_lens, scale, lse_base, lse, weights, status, old_lens, decay, stream)
+
+
+def dcp_mla_key_weights_q4(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale,
+                           lse_base, lse, weights, status, old_lens=None, decay=1.0, stream=None):
+    """dcp_mla_key_weights over a 4-bit arena [shards, pool_pages*P, 416] uint8."""
+    _key_weights("dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, q, arena,
+                 pool_pages, block_table, max_pages, seq_lens, scale, lse_base, lse, weights, status, old_lens, decay,
+                 stream)
+
+
+def _unit_rows(t, name, n, B):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[:2] != (n, B):
+        raise ValueError(f"{name} must be [{n}, {B}, rows]")
+    return t.shape[2]
+
+
+def dcp_evict_select(layout, shard_begin, shard_end, seq_lens, new_lens, sinks, recent, weights, kept, status,
+                     stream=None):
+    """kept [shards, B, rows] int32: the local rows (ascending) that each shard keeps when requests go from seq_lens to
+    new_lens (int64 [B]): those below position `sinks`, of the last `recent` positions, and the heaviest of weights
+    [shards, B, rows] f32."""
+    dev = torch.cuda.current_device()
+    B = seq_lens.numel()
+    n = shard_end - shard_begin
+    rc = load_library().dcp_evict_select(
+        layout, shard_begin, shard_end, B, _at(seq_lens, "seq_lens", torch.int64, (B,), dev),
+        _at(new_lens, "new_lens", torch.int64, (B,), dev), sinks, recent,
+        _at(weights, "weights", torch.float32, None, dev), _unit_rows(weights, "weights", n, B),
+        _at(kept, "kept", torch.int32, None, dev), _unit_rows(kept, "kept", n, B),
+        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check("dcp_evict_select", rc)
+
+
+def _compact(name, width, dtype, layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages,
+             status, weights, stream):
+    dev = torch.cuda.current_device()
+    B, stride = _table(block_table, "block_table")
+    n = shard_end - shard_begin
+    rc = getattr(load_library(), name)(
+        layout, shard_begin, shard_end, _at(kept, "kept", torch.int32, None, dev), _unit_rows(kept, "kept", n, B), B,
+        _at(new_lens, "new_lens", torch.int64, (B,), dev), _at(block_table, "block_table", torch.int32, None, dev),
+        stride, max_pages, _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
+        None if weights is None else _at(weights, "weights", torch.float32, None, dev),
+        0 if weights is None else _unit_rows(weights, "weights", n, B),
+        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+    _check(name, rc)
+
+
+def dcp_kv_compact(layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages, status,
+                   weights=None, stream=None):
+    """Row i of every shard and request becomes its row kept[shard, b, i] >= i, in place, for the rows that new_lens (int64
+    [B]) leaves; weights [shards, B, rows] f32 move with them.  block_table still holds the pages of the old lengths."""
+    _compact("dcp_kv_compact", 576, torch.bfloat16, layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages,
+             arena, pool_pages, status, weights, stream)
+
+
+def dcp_kv_compact_q4(layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages, status,
+                      weights=None, stream=None):
+    """dcp_kv_compact on a 4-bit arena [shards, pool_pages*P, 416] uint8."""
+    _compact("dcp_kv_compact_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, kept, new_lens, block_table,
+             max_pages, arena, pool_pages, status, weights, stream)

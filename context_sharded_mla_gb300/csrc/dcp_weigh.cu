@@ -1,0 +1,773 @@
+// dcp_weigh.cu — the attention weight of every cached row, summed over a call's queries:
+//
+//   w[r][b][i] = decay * w[r][b][i] + sum_{rows (t, h) that see p} exp2(c * q . k_i - lse2[t, h])
+//
+// Sources: "MLA 的 Decode Context Parallelism", section 2 (576-d single-head scores);
+// lse is the merged one, so no maximum and no second pass are needed.
+//
+// The product is laid out with the KEYS on the accumulator's lanes and the query rows on
+// its columns: a key's whole sum is then one thread's, over its own TMEM lane, in a fixed
+// order, and a key that must not count (past the length, NaN) touches no other.
+//
+// A pair of CTAs (two SMs) holds up to 256 query rows in shared memory, half in each, and
+// runs one product of 256 keys x Rg rows (cta_group::2): each SM brings 128 keys of its
+// own and reads the other half of the queries from its peer.  Per SM and tile that is
+// 147 KB of keys for 128 * Rg * 576 multiply-adds: memory-bound up to about 256 rows (2 *
+// 576 * Rg flop for 1152 bytes against 280 flop/byte), tensor-bound above.  Keys stream
+// through a ring of 16-KB chunks (128 keys x 64 dims); the chunks of a tile are consumed
+// in order, so a product starts when its first chunk is there.
+//
+// More than 256 rows: groups of at most 256, one after the other over a block of kBlock
+// tiles (1.2 MB a pair, 90 MB over the card: the later groups find them in L2), each
+// chunk of the queries replaced as soon as the last product with it is done.
+//
+// The 4-bit cache: 416-byte rows land raw, eight warps turn 64 dims of a row each (a lane
+// a key) into bf16 operands and write them to TMEM, where the product takes its A operand
+// from (lanes are keys there too); no dequantised tile is stored.  Groups of 128 rows.
+//
+// Work: the pair-tiles (2 x 128 rows of one request) of all requests in a row, cut into as
+// many equal runs as there are pairs.  A run's start is found from the lengths by every
+// CTA for itself (a block-wide scan, 1 us), so the call is one launch with no workspace.
+#include "dcp_decode.cuh"
+
+namespace {
+
+constexpr int kKeys = 128;                 // keys a CTA brings to a tile
+constexpr int kChunks = kDk / kChunkDims;  // 9
+constexpr int kStageBytes = kKeys * 128;   // 16 KB: 128 keys x 64 dims
+constexpr int kMaxStages = 12;
+constexpr int kBlock = 4;                  // pair-tiles of a block when there is more than one row group
+constexpr int kRawTile = kKeys * kQ4RowBytes;
+constexpr int kMaxRaw = 3;
+constexpr int kASlots = 8;                 // 32-column operand slots in TMEM (4-bit cache)
+constexpr int kACol = 256;
+constexpr uint32_t kAllCols = 512;
+
+// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8-15 dequantise
+constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kDequantWarp = 8;
+constexpr int kThreads = 256, kThreadsQ4 = 512;
+
+struct WeighArgs {
+  Layout L;
+  int32_t shard_begin, n_held;
+  int32_t B, q_len, H, R;       // R = q_len * H
+  int32_t Rg, ngroups;          // columns a group, groups
+  int32_t stages;               // ring stages (bf16) or raw tiles (4-bit)
+  int32_t box_rows, nbox;       // rows a copy (min(P, 64)), copies a tile
+  int32_t npairs;
+  int64_t pool_rows, pool_pages, max_rows;
+  const unsigned char* arena;
+  const int32_t* bt;
+  int64_t bt_stride, max_pages;
+  const int64_t* seq_lens;
+  float scale_log2;
+  int32_t base2;
+  const float* lse;
+  const int64_t* old_lens;
+  float decay;
+  float* weights;
+  int64_t w_stride;
+  int32_t* status;
+};
+
+// ---------------------------------------------------------------- pair forms of the PTX wrappers
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx_cluster(uint32_t bar_cluster, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+__device__ __forceinline__ void mma_pair_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+          d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once this thread's products so far are complete.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// ---------------------------------------------------------------- barriers and shared memory
+enum : int {
+  kFull = 0,                            // key chunk in both CTAs (bf16; counted at the leader)
+  kEmpty = kFull + kMaxStages,          // its products are done
+  kQFull = kEmpty + kMaxStages,         // query chunk in both CTAs (at the leader)
+  kQEmpty = kQFull + kChunks,
+  kSFull = kQEmpty + kChunks,           // scores of a tile
+  kSFree = kSFull + 2,                  // read by the sums' warps of both CTAs (at the leader)
+  kAFull = kSFree + 2,                  // 4-bit: operand slot written in both CTAs (at the leader)
+  kAEmpty = kAFull + kASlots,
+  kRFull = kAEmpty + kASlots,           // 4-bit: raw tile landed
+  kRFree = kRFull + kMaxRaw,
+  kNumBars = kRFree + kMaxRaw
+};
+
+struct Smem {
+  uint32_t q, ring, bars, lse, acc, misc, total;
+};
+// Queries (9 chunks of Rg / 2 rows), the ring, barriers, lse of the group's rows (a copy a warp: no
+// barrier among warps that may give up a wait), a block's sums.
+__host__ __device__ inline Smem smem_of(int Rg, int stages, int stage_bytes) {
+  Smem s;
+  s.q = 0;
+  s.ring = (uint32_t)kChunks * Rg / 2 * 128;
+  s.bars = s.ring + (uint32_t)stages * stage_bytes;
+  s.lse = s.bars + (kNumBars * 8 + 15) / 16 * 16;
+  s.acc = s.lse + 4 * 256 * 4;
+  s.misc = s.acc + kBlock * kKeys * 4;
+  s.total = s.misc + 128;
+  return s;
+}
+
+// ---------------------------------------------------------------- work
+// Rows of a request on the shards, from one division.
+struct Shape {
+  int64_t S, full, rem;  // S = full / I * (N * I) + rem
+  __device__ void set(const WeighArgs& a, int64_t S_) {
+    S = S_;
+    const int64_t blk = a.L.N * a.L.I;
+    const int64_t k = S_ > 0 ? div_tiles(S_, blk) : 0;
+    full = k * a.L.I;
+    rem = S_ > 0 ? S_ - k * blk : 0;
+  }
+  __device__ int64_t count(const WeighArgs& a, int rs) const {
+    int64_t x = rem - (a.shard_begin + rs) * a.L.I;
+    x = x < 0 ? 0 : (x > a.L.I ? a.L.I : x);
+    return full + x;
+  }
+  __device__ int32_t rows(const WeighArgs& a, int rs) const {  // none of a request shorter than its queries
+    if (S < a.q_len) return 0;
+    const int64_t n = count(a, rs);
+    return (int32_t)(n < a.max_rows ? n : a.max_rows);
+  }
+  __device__ int32_t tiles(const WeighArgs& a, int rs) const { return (rows(a, rs) + kKeys - 1) / kKeys; }
+  __device__ int32_t pair_tiles(const WeighArgs& a) const {
+    int32_t t = 0;
+    for (int rs = 0; rs < a.n_held; ++rs) t += tiles(a, rs);
+    return (t + 1) / 2;
+  }
+};
+
+// A pair's run, tile by tile: blocks of pair-tiles of one request, and in a block every row
+// group in turn.  Each role of a CTA walks it for itself.
+struct Walk {
+  int32_t b, left;           // request; pair-tiles left, this block's included
+  int32_t pt, npt;           // block's first pair-tile, pair-tiles of the request
+  int32_t nblk, g, i;        // pair-tiles of the block, row group, pair-tile within the block
+  int32_t rs0, t0, rs, t;    // this CTA's tile: shard and tile of it, at the block's start and now (rs == n_held: none)
+  Shape sh;
+  int64_t S_next;            // the next request's length, already loaded
+
+  __device__ void advance(const WeighArgs& a, int32_t by) {
+    t += by;
+    while (rs < a.n_held) {
+      const int32_t n = sh.tiles(a, rs);
+      if (t < n) break;
+      t -= n;
+      ++rs;
+    }
+  }
+  __device__ void block(const WeighArgs& a) {
+    nblk = min(left, npt - pt);
+    if (a.ngroups > 1) nblk = min(nblk, kBlock);
+    g = i = 0;
+    rs0 = rs;
+    t0 = t;
+  }
+  __device__ void request(const WeighArgs& a, int64_t S) {
+    sh.set(a, S);
+    npt = sh.pair_tiles(a);
+    S_next = b + 1 < a.B ? __ldg(a.seq_lens + b + 1) : 0;
+  }
+  __device__ bool start(const WeighArgs& a, int32_t b_, int32_t pt_, int32_t n, int rank) {
+    left = n;
+    if (n <= 0) return false;
+    b = b_;
+    pt = pt_;
+    request(a, __ldg(a.seq_lens + b));
+    rs = 0;
+    t = 0;
+    advance(a, 2 * pt + rank);
+    block(a);
+    return true;
+  }
+  __device__ bool next(const WeighArgs& a, int rank) {
+    if (++i < nblk) {
+      advance(a, 2);
+      return true;
+    }
+    i = 0;
+    if (++g < a.ngroups) {
+      rs = rs0;
+      t = t0;
+      return true;
+    }
+    left -= nblk;
+    pt += nblk;
+    if (left <= 0) return false;
+    if (pt < npt) {
+      advance(a, 2);  // from the last tile of the block
+    } else {
+      do {
+        if (++b >= a.B) return false;
+        request(a, S_next);
+      } while (npt == 0);
+      pt = 0;
+      rs = 0;
+      t = 0;
+      advance(a, rank);
+    }
+    block(a);
+    return true;
+  }
+  __device__ bool first() const { return i == 0; }
+  __device__ bool last() const { return i == nblk - 1; }
+};
+
+// Where copy `box` of the walk's tile starts: its page id, loaded here and looked at later.
+__device__ __forceinline__ int32_t box_row(const WeighArgs& a, const Walk& w, int box) {
+  if (w.rs >= a.n_held || box >= a.nbox) return -1;
+  const int32_t rho = w.t * kKeys + box * a.box_rows;
+  return rho < w.sh.rows(a, w.rs) ? rho : -1;
+}
+__device__ __forceinline__ int32_t page_of(const WeighArgs& a, const Walk& w, int32_t rho) {
+  return rho < 0 ? -1 : __ldg(a.bt + (int64_t)w.b * a.bt_stride + rho / (int32_t)a.L.P);
+}
+// Its first row over all held pools; -1: nothing to copy (a bad page is flagged).
+__device__ __forceinline__ int32_t pool_row(const WeighArgs& a, int32_t rs, int32_t rho, int32_t page) {
+  if (rho < 0) return -1;
+  if (page < 0 || page >= a.pool_pages) {
+    flag(a.status, DCP_STATUS_BAD_PAGE_ID);
+    return -1;
+  }
+  return (int32_t)(rs * a.pool_rows + page * a.L.P + rho % (int32_t)a.L.P);
+}
+
+// One 64-dim chunk of a 4-bit row: 8 words of codes and 4 scales -> 32 bf16 pairs.
+__device__ __forceinline__ void dequant_chunk(uint32_t row_s, int c, uint32_t (&v)[32]) {
+  if (c == kChunks - 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 x = ld_shared_v4(row_s + kQ4RopeOff + 16 * k);
+      v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+    }
+    return;
+  }
+  const uint4 lo = ld_shared_v4(row_s + 32 * c), hi = ld_shared_v4(row_s + 32 * c + 16);
+  const uint32_t four = ld_shared_u32(row_s + kQ4ScaleOff + 4 * c);
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t s2[2], off2[2];
+    q4_scales(half ? four >> 16 : four & 0xFFFFu, s2, off2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t p[4];
+      q4_values(w[4 * half + k], s2[k >> 1], off2[k >> 1], p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[16 * half + 4 * k + e] = p[e];
+    }
+  }
+}
+
+template <bool kQ4>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : kThreads, 1)
+    weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv, WeighArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  constexpr int kBlockThreads = kQ4 ? kThreadsQ4 : kThreads, kWarps = kBlockThreads / 32;
+  __shared__ int32_t warp_sums[kWarps];
+  __shared__ int32_t start_s[3];
+  if ((smem_u32(smem) & 1023u) != 0) {  // every CTA of the launch sees the same base: all leave
+    if (threadIdx.x == 0) flag(a.status, DCP_STATUS_INTERNAL);
+    return;
+  }
+  const Smem sl = smem_of(a.Rg, a.stages, kQ4 ? kRawTile : kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sl.bars);
+  float* lse_s = reinterpret_cast<float*>(smem + sl.lse) + 256 * (threadIdx.x >> 5 & 3);
+  float* acc_s = reinterpret_cast<float*>(smem + sl.acc);
+  uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + sl.misc);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + sl.misc + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+
+  if (tid == 0) {
+    *abort_s = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&bars[kFull + i], 2);
+      mbar_init(&bars[kEmpty + i], 1);
+    }
+    for (int i = 0; i < kChunks; ++i) {
+      mbar_init(&bars[kQFull + i], 2);
+      mbar_init(&bars[kQEmpty + i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[kSFull + i], 1);
+      mbar_init(&bars[kSFree + i], 8);
+    }
+    for (int i = 0; i < kASlots; ++i) {
+      mbar_init(&bars[kAFull + i], 8);
+      mbar_init(&bars[kAEmpty + i], 1);
+    }
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(&bars[kRFull + i], 1);
+      mbar_init(&bars[kRFree + i], 8);
+    }
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_base_s)),
+                 "r"(kAllCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  // ---- this pair's run of pair-tiles: a scan over the requests
+  {
+    const int32_t per = (a.B + kBlockThreads - 1) / kBlockThreads;
+    const int32_t b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int32_t mine = 0;
+    for (int32_t b = b0; b < b1; ++b) {
+      Shape sh;
+      sh.set(a, __ldg(a.seq_lens + b));
+      mine += sh.pair_tiles(a);
+      if (blockIdx.x == 0) {
+        if (sh.S < a.q_len) flag(a.status, DCP_STATUS_BAD_LENGTH);
+        else if (sh.full + a.L.I > a.max_rows)  // only then can a shard have more rows than its table
+          for (int rs = 0; rs < a.n_held; ++rs)
+            if (sh.count(a, rs) > a.max_rows) flag(a.status, DCP_STATUS_BAD_PAGE_ID);
+      }
+    }
+    int32_t incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    if (tid == 0) start_s[2] = 0;
+    __syncthreads();
+    int32_t before = incl - mine, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sums[w];
+      total += warp_sums[w];
+    }
+    const int32_t lo = (int32_t)((int64_t)total * pair / a.npairs), hi = (int32_t)((int64_t)total * (pair + 1) / a.npairs);
+    if (lo < hi && before <= lo && lo < before + mine) {
+      int32_t b = b0, x = lo - before;
+      for (; b < b1; ++b) {
+        Shape sh;
+        sh.set(a, __ldg(a.seq_lens + b));
+        const int32_t n = sh.pair_tiles(a);
+        if (x < n) break;
+        x -= n;
+      }
+      start_s[0] = b;
+      start_s[1] = x;
+      start_s[2] = hi - lo;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs are set up, the start is known
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const uint32_t lead = mapa_shared(smem_u32(bars), 0);  // the leader's barriers
+  Walk w;
+  const bool any = w.start(a, start_s[0], start_s[1], start_s[2], rank);
+  const uint32_t q_chunk = (uint32_t)a.Rg / 2 * 128;
+
+  if (warp == kKeyWarp && any) {
+    // ------------------------------------------------------------------ keys in
+    // A lane a copy; the next tile's page ids are on their way while this one's copies go out.
+    if (lane == 0) prefetch_tmap(&tmap_kv);
+    int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
+    uint32_t st = 0, ph = 0;
+    bool ok = true, more = true;
+    uint32_t tiles = 0;
+    while (more && ok) {
+      const int32_t y = pool_row(a, w.rs, rho, page);
+      more = w.next(a, rank);
+      rho = more ? box_row(a, w, lane) : -1;
+      page = page_of(a, w, rho);
+      const uint32_t who = __ballot_sync(0xffffffffu, y >= 0);
+      if (kQ4) {
+        ok = warp_wait(&bars[kRFree + st], ph ^ 1, abort_s, lane);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull + st], __popc(who) * a.box_rows * kQ4RowBytes);
+        __syncwarp();
+        if (y >= 0)
+          bulk_load(smem + sl.ring + st * kRawTile + lane * a.box_rows * kQ4RowBytes, a.arena + (int64_t)y * kQ4RowBytes,
+                    a.box_rows * kQ4RowBytes, &bars[kRFull + st]);
+        if (++st == (uint32_t)a.stages) {
+          st = 0;
+          ph ^= 1;
+        }
+      } else {
+        for (int c = 0; c < kChunks && ok; ++c) {
+          ok = warp_wait_cluster(&bars[kEmpty + st], ph ^ 1, abort_s, lane);
+          if (!ok) break;
+          const uint32_t full = lead + 8 * (kFull + st);
+          if (lane == 0) expect_tx_cluster(full, __popc(who) * a.box_rows * 128);
+          __syncwarp();
+          if (y >= 0)
+            tma_load_2d_pair(smem_u32(smem) + sl.ring + st * kStageBytes + lane * a.box_rows * 128, &tmap_kv, full,
+                             c * kChunkDims, y);
+          if (++st == (uint32_t)a.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      ++tiles;
+    }
+    // every slot's last release lands before the CTA may leave
+    if (ok) {
+      const uint32_t uses = kQ4 ? tiles : tiles * kChunks;
+      for (uint32_t s = 0; s < (uint32_t)a.stages && s < uses; ++s) {
+        const uint32_t n = (uses - 1 - s) / a.stages;  // its last use
+        if (!warp_wait_cluster(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s, lane)) break;
+      }
+    }
+  } else if (warp == kQueryWarp && any) {
+    // ------------------------------------------------------------------ queries in
+    if (lane == 0) prefetch_tmap(&tmap_q);
+    uint32_t ph = 0;
+    bool ok = true, more = true;
+    while (more && ok) {
+      if (w.first()) {
+        const int32_t y = w.b * a.R + w.g * a.Rg + rank * (a.Rg / 2);
+        for (int c = 0; c < kChunks && ok; ++c) {
+          ok = warp_wait_cluster(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+          if (ok && lane == 0) {
+            expect_tx_cluster(lead + 8 * (kQFull + c), q_chunk);
+            tma_load_2d_pair(smem_u32(smem) + sl.q + c * q_chunk, &tmap_q, lead + 8 * (kQFull + c), c * kChunkDims, y);
+          }
+        }
+        ph ^= 1;
+      }
+      more = w.next(a, rank);
+    }
+    for (int c = 0; c < kChunks && ok; ++c) ok = warp_wait_cluster(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+  } else if (warp == kMmaWarp && any && rank == 0) {
+    // ------------------------------------------------------------------ products (the leader's alone)
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(2 * kKeys, a.Rg, 0, 0);
+      const uint64_t kdesc = sw128_desc(smem_u32(smem) + sl.ring, 16, 1024);
+      const uint64_t qdesc = sw128_desc(smem_u32(smem) + sl.q, 16, 1024);
+      uint32_t st = 0, ph = 0, qph = 0, j = 0;
+      bool ok = true, more = true;
+      while (more && ok) {
+        const bool first = w.first(), last = w.last();
+        const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
+        ok = mbar_wait_cluster(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
+        for (int c = 0; c < kChunks && ok; ++c) {
+          if (first) ok = mbar_wait_cluster(&bars[kQFull + c], qph, abort_s);
+          ok = ok && mbar_wait_cluster(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = qdesc + c * (q_chunk >> 4);
+#pragma unroll
+          for (int k = 0; k < kChunkDims / 16; ++k) {
+            if (kQ4)
+              mma_pair_ts(d, tmem + kACol + 32 * st + 8 * k, qd + 2 * k, idesc, (c | k) != 0);
+            else
+              mma_pair_ss(d, kdesc + st * (kStageBytes >> 4) + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
+          }
+          commit_pair(&bars[(kQ4 ? kAEmpty : kEmpty) + st]);
+          if (last) commit_pair(&bars[kQEmpty + c]);
+          if (++st == (uint32_t)(kQ4 ? kASlots : a.stages)) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        commit_pair(&bars[kSFull + buf]);
+        if (first) qph ^= 1;
+        ++j;
+        more = w.next(a, rank);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4 && any) {
+    // ------------------------------------------------------------------ sums: a thread a key
+    const float c = a.scale_log2;
+    const uint64_t c2 = f2_pack(__float_as_uint(c), __float_as_uint(c));
+    bool ok = true, more = true;
+    uint32_t j = 0;
+    while (more && ok) {
+      const int32_t ncols = min(a.Rg, a.R - w.g * a.Rg);
+      if (w.first()) {
+        __syncwarp();  // the columns' lse of the group before have been used
+        for (int k = lane; k < ncols; k += 32) {
+          const float l = __ldg(a.lse + (int64_t)w.b * a.R + w.g * a.Rg + k);
+          // a row that saw nothing adds 2^-inf
+          lse_s[k] = l == -INFINITY ? -INFINITY : -(a.base2 ? l : l * kLog2e);
+        }
+        __syncwarp();
+      }
+      // this thread's key
+      const int32_t row = w.t * kKeys + warp * 32 + lane;
+      const bool done = w.g == a.ngroups - 1;
+      bool live = w.rs < a.n_held && row < w.sh.rows(a, w.rs);
+      int32_t page = 0, col0 = 0;
+      float old = 0.f;
+      float* wp = nullptr;
+      if (live) {
+        const int32_t I = (int32_t)a.L.I, k = row / I;
+        const int64_t p = ((int64_t)k * a.L.N + a.shard_begin + w.rs) * I + (row - k * I);
+        const int64_t hidden = p - (w.sh.S - a.q_len);  // query tokens [0, hidden) come before this key
+        if (hidden > 0) {
+          const int64_t x = hidden * a.H - (int64_t)w.g * a.Rg;
+          col0 = (int32_t)(x < 0 ? 0 : (x > a.Rg ? a.Rg : x));
+        }
+        if (done) {
+          page = __ldg(a.bt + (int64_t)w.b * a.bt_stride + row / (int32_t)a.L.P);
+          wp = a.weights + ((int64_t)w.rs * a.B + w.b) * a.w_stride + row;
+          if (a.old_lens && a.decay != 0.f && p < __ldg(a.old_lens + w.b)) old = a.decay * *wp;
+        }
+      }
+      const uint32_t buf = j & 1;
+      ok = warp_wait(&bars[kSFull + buf], (j >> 1) & 1, abort_s, lane);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t s_addr = tmem + ((uint32_t)(warp * 32) << 16) + (kQ4 ? 128 : 256) * buf;
+      const bool masked = __any_sync(0xffffffffu, col0 > 0);
+      uint64_t sum[2] = {0, 0};
+      for (int k0 = 0; k0 < ncols; k0 += 32) {
+        uint32_t r[32];
+        tmem_ld32_sync(s_addr + k0, r);
+        if (!masked && k0 + 32 <= ncols) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 l = *reinterpret_cast<const float4*>(lse_s + k0 + 4 * k);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t x = f2_fma(f2_pack(r[4 * k + 2 * e], r[4 * k + 2 * e + 1]), c2,
+                                        f2_pack(__float_as_uint(e ? l.z : l.x), __float_as_uint(e ? l.w : l.y)));
+              uint32_t x0, x1;
+              f2_unpack(x, x0, x1);
+              sum[e] = f2_add(sum[e], f2_pack(__float_as_uint(fast_exp2(__uint_as_float(x0))),
+                                              __float_as_uint(fast_exp2(__uint_as_float(x1)))));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float e[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col = k0 + k + h;
+              const bool in = col >= col0 && col < ncols;
+              e[h] = in ? fast_exp2(fmaf(__uint_as_float(r[k + h]), c, lse_s[in ? col : 0])) : 0.f;
+            }
+            sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(__float_as_uint(e[0]), __float_as_uint(e[1])));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lead + 8 * (kSFree + buf));
+      uint32_t x0, x1;
+      f2_unpack(f2_add(sum[0], sum[1]), x0, x1);
+      float s = __uint_as_float(x0) + __uint_as_float(x1);
+      if (a.ngroups > 1) {  // this thread's own entry
+        float* acc = acc_s + w.i * kKeys + warp * 32 + lane;
+        if (w.g > 0) s += *acc;
+        *acc = s;
+      }
+      if (done && live && page >= 0 && page < a.pool_pages) *wp = old + s;
+      ++j;
+      more = w.next(a, rank);
+    }
+  } else if (kQ4 && warp >= kDequantWarp && any) {
+    // ------------------------------------------------------------------ 4-bit rows -> operands in TMEM
+    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of every second chunk.
+    const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
+    uint32_t rb = 0, rph = 0, n = 0;  // raw tile and its parity; chunks so far
+    bool ok = true, more = true;
+    while (more && ok) {
+      const bool have = w.rs < a.n_held;  // a CTA may have no tile in the last pair-tile of a request
+      ok = warp_wait(&bars[kRFull + rb], rph, abort_s, lane);
+      const uint32_t row_s = smem_u32(smem) + sl.ring + rb * kRawTile + (quarter * 32 + lane) * kQ4RowBytes;
+      for (int c = 0; c < kChunks && ok; ++c, ++n) {
+        if ((n & 1) != (uint32_t)set) continue;
+        const uint32_t slot = n % kASlots;
+        ok = warp_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s, lane);
+        if (!ok) break;
+        if (have) {
+          uint32_t v[32];
+          dequant_chunk(row_s, c, v);
+          tc_fence_after();
+          tmem_st32(lane_addr + 32 * slot, v);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lead + 8 * (kAFull + slot));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kRFree + rb]);
+      if (++rb == (uint32_t)a.stages) {
+        rb = 0;
+        rph ^= 1;
+      }
+      more = w.next(a, rank);
+    }
+    // the operand slots' last releases land before the CTA may leave
+    for (uint32_t s = 0; s < kASlots && s < n && ok; ++s) {
+      const uint32_t uses = (n - 1 - s) / kASlots;
+      ok = warp_wait(&bars[kAEmpty + s], uses & 1, abort_s, lane);
+    }
+  }
+  __syncthreads();
+  if (*abort_s) {
+    if (tid == 0) flag(a.status, DCP_STATUS_TIMEOUT);
+    const uint64_t t0 = globaltimer();  // copies and products in flight land before memory is given back
+    while (globaltimer() - t0 < 100000) {
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAllCols) : "memory");
+}
+
+PairKernel g_bf16(reinterpret_cast<const void*>(&weigh_kernel<false>), kThreads);
+PairKernel g_q4(reinterpret_cast<const void*>(&weigh_kernel<true>), kThreadsQ4);
+
+struct WeighCall {
+  const dcp_layout_t* layout;
+  int32_t shard_begin, shard_end;
+  const void* q;
+  int32_t B, q_len, H;
+  const void* arena;
+  int64_t pool_pages;
+  const int32_t* block_table;
+  int64_t bt_stride, max_pages;
+  const int64_t* seq_lens;
+  float scale;
+  int32_t lse_base;
+  const float* lse;
+  const int64_t* old_lens;
+  float decay;
+  float* weights;
+  int64_t w_stride;
+  int32_t* status;
+  void* stream;
+};
+
+template <bool kQ4>
+int32_t weigh(const WeighCall& c) {
+  // the partial decode's checks, with the weights in the place of its outputs
+  const DecodeCall d{c.layout, c.shard_begin, c.shard_end, c.q, c.B, c.q_len, c.H, c.arena, c.pool_pages,
+                     c.block_table, c.bt_stride, c.max_pages, c.seq_lens, c.scale, c.lse_base, c.arena ? const_cast<void*>(c.arena) : nullptr,
+                     DCP_F32, c.weights, c.status, c.stream};
+  const int32_t rc = check_decode_args(d);
+  if (rc != DCP_OK) return rc;
+  if (!c.lse || !(c.decay >= 0.f) || !(c.decay < INFINITY) || c.w_stride / c.layout->page_size < c.max_pages)
+    return DCP_ERR_INVALID;
+  WeighArgs a;
+  a.L = to_layout(c.layout);
+  a.shard_begin = c.shard_begin;
+  a.n_held = c.shard_end - c.shard_begin;
+  a.B = c.B;
+  a.q_len = c.q_len;
+  a.H = c.H;
+  a.R = c.q_len * c.H;
+  // groups of at most 256 (128) rows, as equal as multiples of 32 allow (half of them in each CTA)
+  const int most = kQ4 ? 128 : 256;
+  const int groups = (a.R + most - 1) / most;
+  a.Rg = ((a.R + groups - 1) / groups + 31) / 32 * 32;
+  a.ngroups = (a.R + a.Rg - 1) / a.Rg;
+  const int stage_bytes = kQ4 ? kRawTile : kStageBytes, most_stages = kQ4 ? kMaxRaw : kMaxStages;
+  a.stages = (int32_t)(kSmemBudget - 1024 - smem_of(a.Rg, 0, 0).total) / stage_bytes;  // 1 KB: the static variables
+  a.stages = std::min(a.stages, (int32_t)most_stages);
+  const size_t smem = smem_of(a.Rg, a.stages, stage_bytes).total;
+  a.box_rows = std::min(c.layout->page_size, kTile);
+  a.nbox = kKeys / a.box_rows;
+  PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
+  a.npairs = kernel.max_active_clusters(smem);
+  if (a.npairs < 1) return DCP_ERR_CUDA;
+  a.pool_pages = c.pool_pages;
+  a.pool_rows = c.pool_pages * c.layout->page_size;
+  a.max_rows = table_rows(c.layout, c.max_pages);
+  a.arena = static_cast<const unsigned char*>(c.arena);
+  a.bt = c.block_table;
+  a.bt_stride = c.bt_stride;
+  a.max_pages = c.max_pages;
+  a.seq_lens = c.seq_lens;
+  a.scale_log2 = c.scale * kLog2e;
+  a.base2 = c.lse_base == DCP_LSE_BASE_2;
+  a.lse = c.lse;
+  a.old_lens = c.old_lens;
+  a.decay = c.decay;
+  a.weights = c.weights;
+  a.w_stride = c.w_stride;
+  a.status = c.status;
+  CUtensorMap tq, tkv;
+  if (!make_tmap(&tq, c.q, (uint64_t)c.B * a.R, (uint32_t)a.Rg / 2)) return DCP_ERR_CUDA;
+  if (kQ4)
+    tkv = tq;  // its rows are copied as they are
+  else if (!make_tmap(&tkv, c.arena, (uint64_t)a.n_held * a.pool_rows, (uint32_t)a.box_rows))
+    return DCP_ERR_CUDA;
+  if (!kernel.ensure_smem(smem)) return DCP_ERR_CUDA;
+  weigh_kernel<kQ4><<<2 * a.npairs, kQ4 ? kThreadsQ4 : kThreads, smem, as_stream(c.stream)>>>(tq, tkv, a);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" int32_t dcp_mla_key_weights(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
+                                       int32_t B, int32_t q_len, int32_t H, const void* arena, int64_t pool_pages,
+                                       const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                                       const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
+                                       const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
+                                       int32_t* status, void* stream) {
+  return weigh<false>(WeighCall{layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
+                                max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, status,
+                                stream});
+}
+
+extern "C" int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                                          const void* q, int32_t B, int32_t q_len, int32_t H, const void* arena,
+                                          int64_t pool_pages, const int32_t* block_table, int64_t bt_stride,
+                                          int64_t max_pages, const int64_t* seq_lens, float scale, int32_t lse_base,
+                                          const float* lse, const int64_t* old_lens, float decay, float* weights,
+                                          int64_t w_stride, int32_t* status, void* stream) {
+  return weigh<true>(WeighCall{layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
+                               max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, status,
+                               stream});
+}

@@ -28,6 +28,13 @@
  * and, before any of them, the tables they read
  *  12. dcp_block_tables        block tables, free pages, positions and slots of a
  *                              step from the requests' lengths
+ * and, in front of append and absorb_q,
+ *  13. dcp_q_norm_rope         RMS norm of each head's query, its position dims rotated
+ *      dcp_kv_norm_rope_append (_q4)  the same for the latent rows, into the shards' pools
+ * and, to shorten a cache by what its rows weigh,
+ *  14. dcp_mla_key_weights (_q4)  the attention weight of every cached row, accumulated
+ *  15. dcp_evict_select        the rows each shard keeps of each request
+ *  16. dcp_kv_compact (_q4)    kept rows moved to the front of their shard, in place
  *
  * On one GPU the N context shards are N compact paged pools in one HBM
  * allocation (the "arena"), so the cross-rank steps (query all-gather,
@@ -108,6 +115,8 @@ enum {
 
 enum { DCP_LSE_BASE_E = 0, DCP_LSE_BASE_2 = 1 };
 enum { DCP_F32 = 0, DCP_BF16 = 1 };
+/* Which position dims rotate together: (2i, 2i + 1), or (i, i + 32). */
+enum { DCP_ROPE_PAIRS = 0, DCP_ROPE_HALVES = 1 };
 
 /* Library version (major * 10000 + minor * 100 + patch). */
 int32_t dcp_version(void);
@@ -663,6 +672,187 @@ int32_t dcp_block_tables(const dcp_layout_t* layout, int32_t B, int64_t* seq_len
                          int64_t* free_state, int64_t pool_pages, int64_t T, int64_t* pos, int32_t* req,
                          int32_t* owner, int64_t* row, int64_t* slot, int64_t* cu_tokens, int32_t* status,
                          void* stream);
+
+/*
+ * Norm and rotation, in front of the cache and the absorption product.
+ *
+ * Sources: "MLA 的 Decode Context Parallelism", section 2 (a cached row is the
+ * normalised latent c_K and the rotated k_R, a query head its content part and the
+ * rotated q_R); "Decode Context Parallelism" (zdszero), section "decode 路径：以
+ * Kimi K3 的 MLA 为例" (a model may leave the position dims unrotated).
+ *
+ *   norm      y_d = x_d * rsqrt(mean_d x_d^2 + eps) * gamma_d, over the dims that
+ *             gamma has; gamma NULL: no norm.  gamma is f32 or bf16 (gamma_dtype),
+ *             16-byte aligned.  eps is finite and not negative
+ *   rotation  pair i of the 64 position dims, dims (2i, 2i + 1) with DCP_ROPE_PAIRS
+ *             or (i, i + 32) with DCP_ROPE_HALVES, turns by position * inv_freq[i]:
+ *             (a, b) -> (a cos - b sin, a sin + b cos).  inv_freq f32[32], finite, in
+ *             radians a position; NULL: no rotation.  The angle is taken modulo a turn
+ *             in 64 bits: off by at most 2^-52 of itself + 2^-23, whatever the position
+ * Both are computed in f32 and rounded to bf16 once, at the end (the 4-bit append
+ * quantises that bf16 row).
+ */
+
+/*
+ * dcp_q_norm_rope — per-head RMS norm of the queries and rotation of their position
+ * dims: the q_nope and q_pe that dcp_absorb_q takes (both with stride 192).
+ *
+ *   q        bf16, row (t, h) at element (t * H + h) * q_stride; 192 elements read:
+ *            128 content dims, then 64 position dims.  q_stride >= 192, a multiple of 8
+ *   pos      int64[T]: rotation position of each token.  -1: padding, the token's rows
+ *            are left as they are; any other negative one is flagged (BAD_POSITION)
+ *            and left too.  Needed without a rotation as well
+ *   gamma    [192] or NULL: the norm is over all 192 dims, before the rotation
+ *   out      bf16 [T, H, 192]; may be q itself if q_stride is 192, must not overlap
+ *            it otherwise
+ *   status   device word (may be NULL)
+ * q and out are 16-byte aligned.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID on T < 0,
+ * H < 1, a bad stride, gamma_dtype, eps or rope_style, or a null / misaligned pointer.
+ */
+int32_t dcp_q_norm_rope(int64_t T, int32_t H, const void* q, int64_t q_stride, const int64_t* pos,
+                        const void* gamma, int32_t gamma_dtype, float eps, const float* inv_freq,
+                        int32_t rope_style, void* out, int32_t* status, void* stream);
+
+/*
+ * dcp_kv_norm_rope_append — dcp_kv_append of rows that are still a projection's output.
+ *
+ *   kv        bf16, row t at element t * kv_stride; 576 elements read: 512 latent dims
+ *             (normed, gamma [512]), then 64 position dims (rotated).  kv_stride >= 576,
+ *             a multiple of 8 (the last columns of a joint projection pass their base)
+ *   rope_pos  int64[T] rotation positions, or NULL: pos.  They differ once a request has
+ *             been shortened (dcp_kv_compact): its next token goes to row pos of what is
+ *             left, and still turns by its place in the text.  Not looked at for padding
+ *   the rest, the placement and the device status are dcp_kv_append's
+ * A (pos, req) pair must appear once at most.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID
+ * as dcp_kv_append and dcp_q_norm_rope.
+ */
+int32_t dcp_kv_norm_rope_append(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* kv,
+                                int64_t kv_stride, const void* gamma, int32_t gamma_dtype, float eps,
+                                const float* inv_freq, int32_t rope_style, const int64_t* rope_pos,
+                                const int64_t* pos, const int32_t* req, int64_t T, const int32_t* block_table,
+                                int32_t B, int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages,
+                                int32_t* status, void* stream);
+
+/* The same into a 4-bit cache: the bf16 row of dcp_kv_norm_rope_append, quantised as
+ * dcp_kv_append_q4 does (bit for bit what the two calls give). */
+int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* kv,
+                                   int64_t kv_stride, const void* gamma, int32_t gamma_dtype, float eps,
+                                   const float* inv_freq, int32_t rope_style, const int64_t* rope_pos,
+                                   const int64_t* pos, const int32_t* req, int64_t T, const int32_t* block_table,
+                                   int32_t B, int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages,
+                                   int32_t* status, void* stream);
+
+/*
+ * Eviction by attention weight.
+ *
+ * A step's queries give every cached row a weight, dcp_mla_key_weights adds them up over
+ * steps, dcp_evict_select picks the rows that stay, dcp_kv_compact moves them to the front
+ * and dcp_block_tables (from the old lengths to the new ones) gives the freed pages back.
+ * Every shard keeps count_r(new length) of its OWN rows ("PCP / DCP：计算、KV 布局与块
+ * 轮转", section 6, local_len): no row changes shard, so a group of GPUs needs no exchange,
+ * and what is left is laid out as any request of that length.  Afterwards a position is a
+ * place in the shortened cache; the rows keep the rotation of their place in the text.
+ */
+
+/*
+ * dcp_mla_key_weights — attention weight of every cached row, summed over a call's queries.
+ *
+ * Source: "MLA 的 Decode Context Parallelism", section 2 (the scores); the weights are
+ * those of the merged softmax, so they sum to one over all shards for every query row.
+ *
+ * For held shard r, request b and local row i < count_r(S_b), whose position is p and
+ * whose latent row is k:
+ *   new     = sum over (t, h) with p <= S_b - q_len + t of
+ *             exp(scale * q[b,t,h] . k - lse[b,t,h])      (lse in base e; base 2: exp2(.. * log2 e - lse))
+ *   weights[r - shard_begin][b][i] = (p < old_lens[b] ? decay * weights : 0) + new
+ *   q, arena, block_table, seq_lens, scale, lse_base: as for dcp_mla_decode_partial, with
+ *              the rows of the call's own tokens in the cache
+ *   lse        f32[B, q_len, H]: the merged lse of those queries (dcp_lse_merge).  A row of
+ *              -inf (it saw nothing) adds nothing
+ *   old_lens   int64[B] or NULL: rows at positions below it have a weight to add to, those
+ *              from it on (new since the last call) start from 0.  NULL: every row starts
+ *              from 0
+ *   decay      factor on the weights there are, finite and not negative; with 0 they are
+ *              not read
+ *   weights    f32[shard_end - shard_begin, B, w_stride], w_stride >= max_pages * P; entries
+ *              from count_r(S_b) on are left as they are
+ * A request with S_b < q_len is flagged (BAD_LENGTH) and left as it is; a row on a page
+ * outside the pool (BAD_PAGE_ID) is left as it is; a request longer than its table is
+ * flagged (BAD_PAGE_ID) and worked on as far as the table goes.  A NaN in a cached row
+ * makes that row's weight NaN; a NaN in a query row or its lse that of every row it sees.  What lies
+ * behind a request's last row does not matter, NaN included.
+ * Precision: products bf16 by bf16 added in f32; exponents, weights and sums in f32.  The
+ * order of the sums is fixed: equal calls give equal bits.
+ * Sizes and errors as dcp_mla_decode_partial (page sizes, H, q_len * H <= 65536), without
+ * a workspace; DCP_ERR_INVALID also on w_stride < max_pages * P or a bad decay.  Device
+ * status DCP_STATUS_TIMEOUT / INTERNAL: the weights are invalid.
+ */
+int32_t dcp_mla_key_weights(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
+                            int32_t B, int32_t q_len, int32_t H, const void* arena, int64_t pool_pages,
+                            const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                            const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
+                            const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
+                            int32_t* status, void* stream);
+
+/* The same over a 4-bit cache (k is the row the cache holds). */
+int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
+                               int32_t B, int32_t q_len, int32_t H, const void* arena, int64_t pool_pages,
+                               const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
+                               const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
+                               const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
+                               int32_t* status, void* stream);
+
+/*
+ * dcp_evict_select — the rows that stay when requests go from seq_lens to new_lens.
+ *
+ * For held shard r and request b, n = count_r(seq_lens[b]) rows become
+ * m = count_r(new_lens[b]).  Rows at positions below `sinks` come first, in order; then
+ * those among the last `recent` positions, the latest first; then the others, the heaviest
+ * first (a NaN is heavier than any number; among equal weights the lowest row).  The first
+ * m of that sequence stay.
+ *   seq_lens, new_lens  int64[B] (device), 0 <= new_lens[b] <= seq_lens[b]
+ *   sinks, recent       positions, >= 0
+ *   weights             f32[shard_end - shard_begin, B, w_stride] (dcp_mla_key_weights)
+ *   kept  (out)         int32[shard_end - shard_begin, B, kept_stride]: the rows that
+ *                       stay, ascending, in entries [0, m); the others are left as they are
+ * A request with new_lens outside [0, seq_lens], or a unit with n > w_stride or
+ * m > kept_stride, is flagged (BAD_LENGTH) and its entries [0, min(m, kept_stride)) become -1,
+ * which dcp_kv_compact skips.  Errors: DCP_ERR_INVALID for a bad layout or shard range,
+ * B < 1, sinks or recent < 0, a stride < 1 or a null pointer.
+ */
+int32_t dcp_evict_select(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, int32_t B,
+                         const int64_t* seq_lens, const int64_t* new_lens, int64_t sinks, int64_t recent,
+                         const float* weights, int64_t w_stride, int32_t* kept, int64_t kept_stride,
+                         int32_t* status, void* stream);
+
+/*
+ * dcp_kv_compact — row i of every held shard and request becomes its row kept[i], in place,
+ * for i < count_r(new_lens[b]); with `weights`, weight i becomes weight kept[i] too.
+ *
+ *   kept       int32[shard_end - shard_begin, B, kept_stride], kept[i] >= i (repeats
+ *              allowed); rows are those from before the call.  -1: row i stays as it is;
+ *              another entry below i is flagged (BAD_POSITION) and its row left
+ *   new_lens   int64[B] (device)
+ *   block_table, arena, pool_pages: as for dcp_kv_append.  The table still holds the pages
+ *              of the old length.  No page may belong to two requests of the call
+ *   weights    f32[shard_end - shard_begin, B, w_stride] or NULL
+ * Rows from count_r(new_lens[b]) on are left as they are.  A row past the table or past
+ * w_stride (BAD_PAGE_INDEX), or with a page outside the pool on either side (BAD_PAGE_ID),
+ * is left as it is; a unit with a negative new length, or more rows than kept_stride, is
+ * flagged (BAD_LENGTH) and left.  kept_stride == 0 is a no-op.  Errors: DCP_ERR_INVALID for
+ * a bad layout or shard range, B < 1, max_pages outside [1, bt_stride], pool_pages < 1,
+ * kept_stride < 0, weights with w_stride < 1, a null pointer, or arena not 16-byte aligned.
+ */
+int32_t dcp_kv_compact(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const int32_t* kept,
+                       int64_t kept_stride, int32_t B, const int64_t* new_lens, const int32_t* block_table,
+                       int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages, float* weights,
+                       int64_t w_stride, int32_t* status, void* stream);
+
+/* The same on a 4-bit cache. */
+int32_t dcp_kv_compact_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const int32_t* kept,
+                          int64_t kept_stride, int32_t B, const int64_t* new_lens, const int32_t* block_table,
+                          int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages, float* weights,
+                          int64_t w_stride, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

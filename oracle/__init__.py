@@ -36,6 +36,8 @@ Modules
 ``attention``   per-shard partial (o_r, lse_r), LSE merge, unsharded attention.
 ``bruteforce``  pure-Python loop versions for tiny inputs (pins for the above).
 ``absorb``      the query-side and output-side absorption products (identities 1, 2).
+``norm_rope``   RMS norm and rotation of the position dims.
+``evict``       attention weight of cached rows, the rows that stay and their move.
 ``exchange``    the cross-rank exchange of the partials: the all-to-all by head slice
                 (and its wire format) and the AllGather + ReduceScatter merge.
 
@@ -43,4 +45,4 @@ Every function here is pinned by a ``-m "not gpu"`` test against the pages'
 worked examples, closed forms, invariants or brute force.  None is unpinned.
 """
 
-from . import layout, attention, bruteforce, absorb, exchange  # noqa: F401
+from . import layout, attention, bruteforce, absorb, exchange, norm_rope, evict  # noqa: F401

@@ -1,0 +1,97 @@
+"""What the norm/rotation, key-weight and eviction calls refuse, before anything is launched (no GPU)."""
+
+import ctypes
+
+import pytest
+import torch
+
+import context_sharded_mla_gb300 as dcp
+
+INVALID, UNSUPPORTED = -1, -2
+P = ctypes.c_void_p
+GOOD, BAD, HUGE = dcp.Layout(4, 1, 16), dcp.Layout(4, 3, 16), 2 ** 62
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from context_sharded_mla_gb300 import _build
+    _build.build()
+    return dcp.load_library()
+
+
+def call(fn, defaults, **kw):
+    lay = kw.pop("lay", GOOD)
+    assert not set(kw) - set(defaults)
+    return fn(ctypes.byref(lay) if lay else None, *dict(defaults, **kw).values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(H=0), dict(q=None), dict(q=P(24)), dict(qs=191), dict(qs=196), dict(pos=None), dict(g=P(24)),
+    dict(gd=2), dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(style=2), dict(out=None), dict(out=P(40))])
+def test_q_norm_rope(lib, kw):
+    base = dict(T=1, H=2, q=P(16), qs=192, pos=P(16), g=P(16), gd=1, eps=1e-6, f=P(16), style=0, out=P(32), status=None,
+                stream=None)
+    assert lib.dcp_q_norm_rope(*dict(base, **kw).values()) == INVALID
+    assert lib.dcp_q_norm_rope(*dict(base, T=0, q=None, out=None).values()) == 0
+    assert lib.dcp_q_norm_rope(*dict(base, T=HUGE).values()) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lay=None), dict(lay=BAD), dict(sb=-1), dict(se=5), dict(sb=2, se=2), dict(kv=None), dict(kv=P(24)), dict(ks=575),
+    dict(ks=580), dict(g=P(24)), dict(gd=7), dict(eps=-0.5), dict(eps=NAN), dict(style=-1), dict(pos=None),
+    dict(req=None), dict(T=-1), dict(bt=None), dict(B=0), dict(mp=0), dict(mp=2), dict(ar=None), dict(ar=P(40)),
+    dict(pp=0)])
+def test_norm_rope_append(lib, kw):
+    base = dict(sb=0, se=4, kv=P(16), ks=576, g=P(16), gd=0, eps=0.0, f=P(16), style=1, rp=None, pos=P(16), req=P(16), T=1,
+                bt=P(16), B=1, st=1, mp=1, ar=P(32), pp=1, status=P(16), stream=None)
+    for fn in (lib.dcp_kv_norm_rope_append, lib.dcp_kv_norm_rope_append_q4):
+        assert call(fn, base, **kw) == INVALID
+        assert call(fn, base, T=0, kv=None) == 0
+        assert call(fn, base, T=HUGE) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(lay=None), INVALID), (dict(lay=BAD), INVALID), (dict(se=5), INVALID), (dict(q=None), INVALID),
+    (dict(q=P(264)), INVALID), (dict(B=0), INVALID), (dict(ql=0), INVALID), (dict(H=65537), INVALID),
+    (dict(ql=512, H=129), INVALID), (dict(ar=None), INVALID), (dict(ar=P(264)), INVALID), (dict(pp=0), INVALID),
+    (dict(bt=None), INVALID), (dict(mp=2), INVALID), (dict(sl=None), INVALID), (dict(sc=0.0), INVALID),
+    (dict(sc=INF), INVALID), (dict(sc=NAN), INVALID), (dict(base=7), INVALID), (dict(lse=None), INVALID),
+    (dict(decay=-0.1), INVALID), (dict(decay=NAN), INVALID), (dict(decay=INF), INVALID), (dict(w=None), INVALID),
+    (dict(ws=15), INVALID), (dict(ws=-16), INVALID), (dict(lay=dcp.Layout(4, 1, 12)), UNSUPPORTED),
+    (dict(lay=dcp.Layout(4, 1, 4)), UNSUPPORTED), (dict(pp=2 ** 27), UNSUPPORTED),
+    (dict(B=2 ** 15, st=2 ** 22, mp=2 ** 22, ws=2 ** 40), UNSUPPORTED)])
+def test_key_weights(lib, kw, rc):
+    base = dict(sb=0, se=4, q=P(256), B=1, ql=1, H=16, ar=P(256), pp=1, bt=P(256), st=1, mp=1, sl=P(256), sc=0.1, base=0,
+                lse=P(256), old=None, decay=1.0, w=P(256), ws=16, status=P(256), stream=None)
+    for fn in (lib.dcp_mla_key_weights, lib.dcp_mla_key_weights_q4):
+        assert call(fn, base, **kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(lay=BAD), INVALID), (dict(se=5), INVALID), (dict(B=0), INVALID), (dict(sl=None), INVALID),
+    (dict(nl=None), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(w=None), INVALID),
+    (dict(ws=0), INVALID), (dict(k=None), INVALID), (dict(ks=0), INVALID), (dict(ws=2 ** 31), UNSUPPORTED),
+    (dict(B=2 ** 30), UNSUPPORTED)])
+def test_select(lib, kw, rc):
+    base = dict(sb=0, se=4, B=1, sl=P(16), nl=P(16), sinks=0, recent=0, w=P(16), ws=16, k=P(16), ks=16, status=P(16),
+                stream=None)
+    assert call(lib.dcp_evict_select, base, **kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(lay=BAD), INVALID), (dict(sb=3, se=3), INVALID), (dict(k=None), INVALID), (dict(ks=-1), INVALID),
+    (dict(B=0), INVALID), (dict(nl=None), INVALID), (dict(bt=None), INVALID), (dict(mp=0), INVALID),
+    (dict(mp=2), INVALID), (dict(ar=None), INVALID), (dict(ar=P(40)), INVALID), (dict(pp=0), INVALID),
+    (dict(ws=0), INVALID), (dict(ks=2 ** 31), UNSUPPORTED), (dict(ks=0, k=None), 0)])
+def test_compact(lib, kw, rc):
+    base = dict(sb=0, se=4, k=P(16), ks=4, B=1, nl=P(16), bt=P(16), st=1, mp=1, ar=P(32), pp=1, w=P(16), ws=4,
+                status=P(16), stream=None)
+    for fn in (lib.dcp_kv_compact, lib.dcp_kv_compact_q4):
+        assert call(fn, base, **kw) == rc
+
+
+def test_the_binding_wants_cuda_tensors_of_the_right_shape(lib):
+    q = torch.zeros(2, 3, 192, dtype=torch.bfloat16)
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        dcp.dcp_q_norm_rope(q, torch.zeros(2, dtype=torch.int64), q)
