@@ -80,12 +80,12 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 __device__ __forceinline__ void expect_tx_cluster(uint32_t bar_cluster, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
                "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 __device__ __forceinline__ void mma_pair_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -435,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         }
       } else {
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = warp_wait_cluster(&bars[kEmpty + st], ph ^ 1, abort_s, lane);
+          ok = warp_wait(&bars[kEmpty + st], ph ^ 1, abort_s, lane);
           if (!ok) break;
           const uint32_t full = lead + 8 * (kFull + st);
           if (lane == 0) expect_tx_cluster(full, __popc(who) * a.box_rows * 128);
@@ -456,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       const uint32_t uses = kQ4 ? tiles : tiles * kChunks;
       for (uint32_t s = 0; s < (uint32_t)a.stages && s < uses; ++s) {
         const uint32_t n = (uses - 1 - s) / a.stages;  // its last use
-        if (!warp_wait_cluster(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s, lane)) break;
+        if (!warp_wait(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s, lane)) break;
       }
     }
   } else if (warp == kQueryWarp && any) {
@@ -468,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       if (w.first()) {
         const int32_t y = w.b * a.R + w.g * a.Rg + rank * (a.Rg / 2);
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = warp_wait_cluster(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+          ok = warp_wait(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
           if (ok && lane == 0) {
             expect_tx_cluster(lead + 8 * (kQFull + c), q_chunk);
             tma_load_2d_pair(smem_u32(smem) + sl.q + c * q_chunk, &tmap_q, lead + 8 * (kQFull + c), c * kChunkDims, y);
@@ -478,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       }
       more = w.next(a, rank);
     }
-    for (int c = 0; c < kChunks && ok; ++c) ok = warp_wait_cluster(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+    for (int c = 0; c < kChunks && ok; ++c) ok = warp_wait(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
   } else if (warp == kMmaWarp && any && rank == 0) {
     // ------------------------------------------------------------------ products (the leader's alone)
     if (lane == 0) {
@@ -490,10 +490,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       while (more && ok) {
         const bool first = w.first(), last = w.last();
         const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
-        ok = mbar_wait_cluster(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
+        ok = mbar_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
         for (int c = 0; c < kChunks && ok; ++c) {
-          if (first) ok = mbar_wait_cluster(&bars[kQFull + c], qph, abort_s);
-          ok = ok && mbar_wait_cluster(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
+          if (first) ok = mbar_wait(&bars[kQFull + c], qph, abort_s);
+          ok = ok && mbar_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
           if (!ok) break;
           tc_fence_after();
           const uint64_t qd = qdesc + c * (q_chunk >> 4);
