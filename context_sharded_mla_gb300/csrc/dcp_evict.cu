@@ -5,14 +5,13 @@
 // 轮转", section 6: local_len), so that no row leaves its shard and the layout's count
 // rule holds for what is left; kept rows stay in order.
 //
-// select_kernel: one cluster of CTAs for a (request, shard) unit.  The k-th largest
-// weight of the rows that compete is found digit by digit, 8 bits of an order-preserving
-// integer at a time: histograms in shared memory, one copy a lane, so that the lanes of a
-// warp never meet in a bank however alike their weights are (weights of one
-// magnitude share their first digit); the CTAs add theirs up through distributed shared
-// memory.  Rows are then written in order: counts a warp, prefix sums, ballots.  Only
-// whole numbers are added, so the result depends on no order.  It reads the weights six
-// times, five of them from L1 or L2.
+// select_kernel: one cluster of CTAs for a (request, shard) unit, each thread holding its
+// rows' weights in registers as integers of the same order.  The k-th largest of the rows
+// that compete is found digit by digit, 8 bits at a time: histograms in shared memory, one
+// copy a lane, so that the lanes of a warp never meet in a bank however alike their
+// weights are (weights of one magnitude share their first digit); the CTAs add theirs up
+// through distributed shared memory.  Rows are then written in order: ballots, one block
+// scan of their counts.  Only whole numbers are added, so the result depends on no order.
 //
 // compact_kernel: row i <- row kept[i] >= i.  Writing row i is safe once the rows up to
 // i have been read: a later row j > i reads kept[j] >= j.  So a cluster walks a unit in
@@ -68,111 +67,224 @@ __device__ __forceinline__ int warp_sum(int v) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
-  __shared__ uint32_t hist[kBins * 32];
-  __shared__ uint32_t total[kDigits][kBins];  // this CTA's counts of each digit's bins, read by the cluster
-  __shared__ uint32_t all[kBins];
-  __shared__ uint32_t pick_s[2];              // chosen bin, rows still wanted of it
-  __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
-  __shared__ uint32_t cta_n[2];               // rows above and at the limit
-  const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
-  const int64_t u = blockIdx.x / nranks;
-  const int rs = (int)(u / a.B), b = (int)(u % a.B);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t S = a.seq_lens[b], M = a.new_lens[b];
-  const int64_t r = a.shard_begin + rs;
-  const int64_t m = M > 0 ? count_of(r, M, a.L) : 0;
-  const int64_t n = S > 0 ? count_of(r, S, a.L) : 0;
-  int32_t* kept = a.kept + u * a.kept_stride;
-  if (M < 0 || M > S || n > a.w_stride || m > a.kept_stride) {  // refused: the whole cluster leaves
+// A unit's parts: rows [0, lo) are sinks, [hi, n) recent ones, those between compete for `want` places.
+struct Unit {
+  int32_t lo, hi, ns;
+  uint32_t want;
+};
+
+// Sets u up and writes its sinks and recent rows; false (for the whole cluster) where no row competes, or the unit is
+// refused.
+__device__ bool select_begin(const SelectArgs& a, int64_t unit, uint32_t rank, uint32_t nranks, Unit* u) {
+  const int rs = (int)(unit / a.B), b = (int)(unit % a.B), tid = threadIdx.x;
+  const int64_t S = a.seq_lens[b], M = a.new_lens[b], r = a.shard_begin + rs;
+  const int64_t m = M > 0 ? count_of(r, M, a.L) : 0, n = S > 0 ? count_of(r, S, a.L) : 0;
+  int32_t* kept = a.kept + unit * a.kept_stride;
+  if (M < 0 || M > S || n > a.w_stride || m > a.kept_stride) {
     if (tid == 0 && rank == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
     const int64_t e = m < a.kept_stride ? m : a.kept_stride;
     for (int64_t i = rank * kSelThreads + tid; i < e; i += nranks * kSelThreads) kept[i] = -1;
-    return;
+    return false;
   }
-  // rows [0, lo) are sinks, [hi, n) recent ones, those between compete
   const int64_t lo = count_of(r, a.sinks < S ? a.sinks : S, a.L);
   const int64_t zr = count_of(r, S > a.recent ? S - a.recent : 0, a.L);
-  const int64_t hi = zr > lo ? zr : lo;
-  const int64_t ns = lo < m ? lo : m;
-  const int64_t nr = m - ns < n - hi ? m - ns : n - hi;
-  const int64_t len = hi - lo;
-  uint32_t want = (uint32_t)(m - ns - nr);  // of the rows between; rows of a unit fit 31 bits (w_stride)
+  const int64_t hi = zr > lo ? zr : lo, ns = lo < m ? lo : m, nr = m - ns < n - hi ? m - ns : n - hi;
+  u->lo = (int32_t)lo;  // rows of a unit fit 31 bits (w_stride)
+  u->hi = (int32_t)hi;
+  u->ns = (int32_t)ns;
+  u->want = (uint32_t)(m - ns - nr);
   if (rank == 0)
     for (int64_t i = tid; i < ns; i += kSelThreads) kept[i] = (int32_t)i;
   if (rank == nranks - 1)
     for (int64_t i = tid; i < nr; i += kSelThreads) kept[m - nr + i] = (int32_t)(n - nr + i);
-  if (want == 0) return;  // uniform over the cluster
+  return u->want != 0;
+}
 
-  // this CTA's rows, and this warp's of them
-  const int64_t per = ((len + nranks - 1) / nranks + 31) / 32 * 32;
-  const int32_t c0 = (int32_t)(rank * per < len ? rank * per : len);
-  const int32_t c1 = (int32_t)(c0 + per < len ? c0 + per : len);
-  const float* w = a.weights + u * a.w_stride + lo;
-  uint32_t prefix = 0;
+struct SelectSmem {
+  uint32_t hist[kBins * 32];         // a copy a lane
+  uint32_t total[kDigits][kBins];    // this CTA's counts of each digit's bins, read by the cluster
+  uint32_t all[kBins];
+  uint32_t pick[3];                  // chosen bin, rows still wanted of it, rows in it
+  uint32_t cta_n[2];                 // rows above and at the limit
+};
+
+// After a digit's histogram: the bin that holds the want-th largest of the cluster's candidates.
+__device__ void choose_bin(SelectSmem& sm, int d, uint32_t want, uint32_t nranks) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  __syncthreads();
+  {
+    const int bin = tid >> 1;
+    uint32_t s = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += sm.hist[bin * 32 + 16 * (tid & 1) + ((k + (tid >> 1)) & 15)];
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    if (!(tid & 1)) sm.total[d][bin] = s;
+  }
+  if (nranks > 1) {
+    cluster_sync();
+    if (tid < kBins) {
+      uint32_t s = 0;
+      for (uint32_t c = 0; c < nranks; ++c) s += ld_cluster_u32(mapa_shared(smem_u32(&sm.total[d][tid]), c));
+      sm.all[tid] = s;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {  // counts from the top, 8 bins a lane
+    const uint32_t* all = nranks > 1 ? sm.all : sm.total[d];
+    uint32_t c[8], s = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += c[k] = all[255 - 8 * lane - k];
+    uint32_t incl = s;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
+    uint32_t before = incl - s;
+    if (before < want && want <= incl) {  // exactly one lane
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (before < want && want <= before + c[k]) {
+          sm.pick[0] = 255 - 8 * lane - k;
+          sm.pick[1] = want - before;
+          sm.pick[2] = c[k];
+        }
+        before += c[k];
+      }
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void clear_hist(SelectSmem& sm) {
+  for (int i = threadIdx.x; i < kBins * 32 / 4; i += kSelThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
+// Units of at most kPer * 512 rows a CTA: every thread holds its kPer keys in registers (rows tid, tid + 512, ..; 0,
+// which is no weight's key, where there is none), so that the weights are read once.
+template <int kPer>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
+  __shared__ __align__(16) SelectSmem sm;
+  __shared__ uint32_t at_s[kPer * kSelWarps];  // rows at (<< 16) and above the limit, then their prefix sums
+  __shared__ uint32_t warp_s[kSelWarps];
+  const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
+  const int64_t unit = blockIdx.x / nranks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Unit u;
+  if (!select_begin(a, unit, rank, nranks, &u)) return;
+  const int32_t len = u.hi - u.lo, per = (len + nranks - 1) / nranks;
+  const int32_t c0 = min((int32_t)rank * per, len), c1 = min(c0 + per, len);
+  const float* w = a.weights + unit * a.w_stride + u.lo;
+  uint32_t key[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int32_t i = c0 + k * kSelThreads + tid;
+    key[k] = i < c1 ? order_key(__ldg(w + i)) : 0u;
+  }
+  uint32_t limit = 0, want = u.want;
 #pragma unroll 1
   for (int d = 0; d < kDigits; ++d) {
     const int shift = 24 - 8 * d;
-    for (int i = tid; i < kBins * 32; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
     const uint32_t mask = d ? 0xFFFFFFFFu << (shift + 8) : 0u;
-#pragma unroll 4
+    clear_hist(sm);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (key[k] != 0 && (key[k] & mask) == limit) atomicAdd(&sm.hist[((key[k] >> shift) & 255u) * 32 + lane], 1u);
+    choose_bin(sm, d, want, nranks);
+    limit |= sm.pick[0] << shift;
+    want = sm.pick[1];
+    if (want == sm.pick[2]) {  // the whole bin stays: every key from `limit` on (no weight's key is 0)
+      limit = limit ? limit - 1 : 0;
+      want = 0;
+      break;
+    }
+  }
+  // keys above the limit stay, and the first `want` of those at it, in row order: k, then warp, then lane
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
+    if (lane == 0) at_s[k * kSelWarps + warp] = __popc(bg) | __popc(be) << 16;
+  }
+  __syncthreads();
+  {  // exclusive prefix sums (at most 16384 rows: the halves do not meet)
+    const uint32_t mine = tid < kPer * kSelWarps ? at_s[tid] : 0;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 31) warp_s[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+    for (int i = 0; i < kSelWarps; ++i) {
+      if (i < warp) before += warp_s[i];
+      total += warp_s[i];
+    }
+    if (tid < kPer * kSelWarps) at_s[tid] = before + incl - mine;
+    if (tid == 0) {
+      sm.cta_n[0] = total & 0xFFFFu;
+      sm.cta_n[1] = total >> 16;
+    }
+  }
+  uint32_t gt0 = 0, eq0 = 0;  // rows of the CTAs before
+  if (nranks > 1) {
+    cluster_sync();
+    for (uint32_t c = 0; c < rank; ++c) {
+      gt0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[0]), c));
+      eq0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[1]), c));
+    }
+  }
+  __syncthreads();
+  int32_t* kept = a.kept + unit * a.kept_stride + u.ns;
+  const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
+    const uint32_t at = at_s[k * kSelWarps + warp];
+    const uint32_t eq = eq0 + (at >> 16) + __popc(be & below);
+    if (key[k] > limit || (key[k] == limit && eq < want))
+      kept[gt0 + (at & 0xFFFFu) + __popc(bg & below) + min(eq, want)] = u.lo + c0 + k * kSelThreads + tid;
+  }
+  if (nranks > 1) cluster_sync();  // no CTA leaves while its counts are read
+}
+
+// Longer units: the weights are read six times, mostly from L2.
+__global__ void __launch_bounds__(kSelThreads) select_long_kernel(SelectArgs a) {
+  __shared__ __align__(16) SelectSmem sm;
+  __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
+  const int64_t unit = blockIdx.x / nranks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Unit u;
+  if (!select_begin(a, unit, rank, nranks, &u)) return;
+  const int64_t len = u.hi - u.lo, per = ((len + nranks - 1) / nranks + 31) / 32 * 32;
+  const int32_t c0 = (int32_t)(rank * per < len ? rank * per : len), c1 = (int32_t)(c0 + per < len ? c0 + per : len);
+  const float* w = a.weights + unit * a.w_stride + u.lo;
+  uint32_t limit = 0, want = u.want;
+#pragma unroll 1
+  for (int d = 0; d < kDigits; ++d) {
+    const int shift = 24 - 8 * d;
+    const uint32_t mask = d ? 0xFFFFFFFFu << (shift + 8) : 0u;
+    clear_hist(sm);
+#pragma unroll 8
     for (int32_t i = c0 + tid; i < c1; i += kSelThreads) {
       const uint32_t k = order_key(w[i]);
-      if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * 32 + lane], 1u);
+      if ((k & mask) == limit) atomicAdd(&sm.hist[((k >> shift) & 255u) * 32 + lane], 1u);
     }
-    __syncthreads();
-    {
-      const int bin = tid >> 1;
-      uint32_t s = 0;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) s += hist[bin * 32 + 16 * (tid & 1) + ((k + (tid >> 1)) & 15)];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      if (!(tid & 1)) total[d][bin] = s;
-    }
-    if (nranks > 1) cluster_sync(); else __syncthreads();
-    if (tid < kBins) {
-      uint32_t s = 0;
-      for (uint32_t c = 0; c < nranks; ++c)
-        s += nranks > 1 ? ld_cluster_u32(mapa_shared(smem_u32(&total[d][tid]), c)) : total[d][tid];
-      all[tid] = s;
-    }
-    __syncthreads();
-    if (warp == 0) {  // the bin that holds the want-th largest: counts from the top, 8 bins a lane
-      uint32_t c[8], s = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s += c[k] = all[255 - 8 * lane - k];
-      uint32_t incl = s;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, x);
-        if (lane >= x) incl += y;
-      }
-      uint32_t before = incl - s;
-      if (before < want && want <= incl) {  // exactly one lane
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (before < want && want <= before + c[k]) {
-            pick_s[0] = 255 - 8 * lane - k;
-            pick_s[1] = want - before;
-          }
-          before += c[k];
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= pick_s[0] << shift;
-    want = pick_s[1];
+    choose_bin(sm, d, want, nranks);
+    limit |= sm.pick[0] << shift;
+    want = sm.pick[1];
   }
-  // rows above the limit `prefix` stay, and the first `want` of those at it
   const int32_t perw = ((c1 - c0 + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int32_t w0 = min(c0 + warp * perw, c1), w1 = min(w0 + perw, c1);
   int gt = 0, eq = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int32_t i = w0 + lane; i < w1; i += 32) {
     const uint32_t k = order_key(w[i]);
-    gt += k > prefix;
-    eq += k == prefix;
+    gt += k > limit;
+    eq += k == limit;
   }
   gt = warp_sum(gt);
   eq = warp_sum(eq);
@@ -187,29 +299,31 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
       sg += warp_gt[i];
       se += warp_eq[i];
     }
-    cta_n[0] = sg;
-    cta_n[1] = se;
+    sm.cta_n[0] = sg;
+    sm.cta_n[1] = se;
   }
   uint32_t gt0 = 0, eq0 = 0;  // rows above and at the limit before this warp's
   if (nranks > 1) {
     cluster_sync();
     for (uint32_t c = 0; c < rank; ++c) {
-      gt0 += ld_cluster_u32(mapa_shared(smem_u32(&cta_n[0]), c));
-      eq0 += ld_cluster_u32(mapa_shared(smem_u32(&cta_n[1]), c));
+      gt0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[0]), c));
+      eq0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[1]), c));
     }
   }
   for (int i = 0; i < warp; ++i) {
     gt0 += warp_gt[i];
     eq0 += warp_eq[i];
   }
+  int32_t* kept = a.kept + unit * a.kept_stride + u.ns;
   const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
   for (int32_t i = w0; i < w1; i += 32) {
     const bool in = i + lane < w1;
     const uint32_t k = in ? order_key(w[i + lane]) : 0u;
-    const uint32_t bg = __ballot_sync(0xffffffffu, in && k > prefix), be = __ballot_sync(0xffffffffu, in && k == prefix);
+    const uint32_t bg = __ballot_sync(0xffffffffu, in && k > limit), be = __ballot_sync(0xffffffffu, in && k == limit);
     const uint32_t at_eq = eq0 + __popc(be & below);
-    if (in && (k > prefix || (k == prefix && at_eq < want)))
-      kept[ns + gt0 + __popc(bg & below) + (at_eq < want ? at_eq : want)] = (int32_t)(lo + i + lane);
+    if (in && (k > limit || (k == limit && at_eq < want)))
+      kept[gt0 + __popc(bg & below) + min(at_eq, want)] = u.lo + i + lane;
     gt0 += __popc(bg);
     eq0 += __popc(be);
   }
@@ -294,6 +408,9 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
   float* wts = a.weights ? a.weights + u * a.w_stride : nullptr;
   unsigned char* pool = a.arena + rs * a.pool_pages * a.L.P * kRowBytes;
   const int32_t P = (int32_t)a.L.P;
+  const int32_t shift = (P & (P - 1)) ? -1 : 31 - __clz(P);  // page sizes are mostly powers of two
+  auto page_at = [&](int32_t row) -> int32_t { return shift >= 0 ? row >> shift : row / P; };
+  auto in_page = [&](int32_t row) -> int32_t { return shift >= 0 ? row & (P - 1) : row % P; };
   const int32_t step = (int32_t)nranks * R::kRows;
   const int32_t nwin = (int32_t)(((int64_t)m + step - 1) / step);
 
@@ -313,11 +430,11 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
       if (k < -1 || (k >= 0 && k < i)) flag(a.status, DCP_STATUS_BAD_POSITION);
       return Pages{-1, 0, 0};  // none, or in its place already
     }
-    if (k / P >= a.max_pages || (wts && k >= a.w_stride)) {
+    if (page_at(k) >= a.max_pages || (wts && k >= a.w_stride)) {
       flag(a.status, DCP_STATUS_BAD_PAGE_INDEX);
       return Pages{-1, 0, 0};
     }
-    return Pages{k, __ldg(bt + k / P), __ldg(bt + (int32_t)i / P)};
+    return Pages{k, __ldg(bt + page_at(k)), __ldg(bt + page_at((int32_t)i))};
   };
   // window x into its slot; returns where this lane's row goes (null: nowhere)
   auto load = [&](int32_t x, const Pages& pg) -> unsigned char* {
@@ -332,12 +449,12 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
     if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(who) * kRowBytes);
     __syncwarp();
     if (live) {
-      bulk_load(ring + s * R::kSlotBytes + lane * kRowBytes, pool + ((int64_t)pg.src * P + pg.from % P) * kRowBytes,
+      bulk_load(ring + s * R::kSlotBytes + lane * kRowBytes, pool + ((int64_t)pg.src * P + in_page(pg.from)) * kRowBytes,
                 kRowBytes, &full[s]);
       if (wts) copy4_async(smem_u32(&w_s[s][lane]), wts + pg.from);
     }
     copies_arrive(&full[s]);
-    return live ? pool + ((int64_t)pg.dst * P + i % P) * kRowBytes : nullptr;
+    return live ? pool + ((int64_t)pg.dst * P + in_page(i)) * kRowBytes : nullptr;
   };
 
   constexpr int kAhead = R::kWindows - 2;  // windows loaded ahead of the one written
@@ -356,27 +473,32 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
   };
 #pragma unroll
   for (int x = 0; x < kAhead; ++x) dst[x] = x < nwin ? feed(x) : nullptr;
+  // The barrier that says "window x has been read by all" is arrived at a window early, so that it completes behind
+  // the store and the copies of the window before.  It orders no memory: the rows have landed when a CTA arrives.
   bool ok = true;
+  auto read_one = [&](int s, int32_t x) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(x / R::kWindows) & 1u, abort_s));
+    if (nranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // after a lost wait too
+  };
+  read_one(0, 0);
   for (int32_t x0 = 0; x0 < nwin; x0 += R::kWindows) {
 #pragma unroll
     for (int s = 0; s < R::kWindows; ++s) {
       const int32_t x = x0 + s;
       if (x >= nwin) break;
-      if (ok) {
-        bool here = mbar_wait(&full[s], (uint32_t)(x / R::kWindows) & 1u, abort_s);
-        ok = __all_sync(0xffffffffu, here);
-      }
-      if (nranks > 1) cluster_sync();  // after a wait that ran out too: the others count on it
-      if (ok) {
+      const bool had = ok;
+      if (nranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (x + 1 < nwin) read_one((s + 1) % R::kWindows, x + 1);
+      if (had) {
         if (dst[s]) {
           bulk_store(dst[s], smem_u32(ring) + s * R::kSlotBytes + lane * kRowBytes, kRowBytes);
           if (wts) wts[row_at(x)] = w_s[s][lane];
         }
         bulk_commit();
-        if (x + kAhead < nwin) {
-          bulk_wait_read<2>();  // window x - 2 has left the slot that is filled next
-          dst[(s + kAhead) % R::kWindows] = feed(x + kAhead);
-        }
+      }
+      if (ok && x + kAhead < nwin) {
+        bulk_wait_read<2>();  // window x - 2 has left the slot that is filled next
+        dst[(s + kAhead) % R::kWindows] = feed(x + kAhead);
       }
     }
   }
@@ -455,7 +577,12 @@ extern "C" int32_t dcp_evict_select(const dcp_layout_t* layout, int32_t shard_be
   const SelectArgs a{to_layout(layout), shard_begin, shard_end - shard_begin, B, seq_lens, new_lens, sinks, recent,
                      weights, w_stride, kept, kept_stride, status};
   const int64_t units = (int64_t)B * a.n_held;
-  return launch_clusters(select_kernel, units, cluster_of(units, w_stride, 2048, 608), kSelThreads, 0, stream, a);
+  // CTAs a unit while they leave SMs idle, then as many as hold its rows in registers
+  unsigned c = cluster_of(units, w_stride, 2048, 304);
+  while (c < 8 && w_stride > (int64_t)c * 32 * kSelThreads) c *= 2;
+  const int64_t per = (w_stride + c * kSelThreads - 1) / (c * kSelThreads);
+  const auto kernel = per <= 4 ? select_kernel<4> : per <= 16 ? select_kernel<16> : per <= 32 ? select_kernel<32> : select_long_kernel;
+  return launch_clusters(kernel, units, c, kSelThreads, 0, stream, a);
 }
 
 extern "C" int32_t dcp_kv_compact(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,

@@ -57,16 +57,19 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return u;
 }
 
-// Norm weights of 8 dims, f32 or bf16.
-__device__ __forceinline__ void gamma8(const void* gamma, int bf16, int at, float (&g)[8]) {
-  if (bf16) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gamma) + at)), g);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(gamma) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
-    g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
-  }
+// Norm weights (f32 or bf16) into shared memory, in f32.
+__device__ __forceinline__ void load_gamma(const void* gamma, int bf16, int dims, float* g) {
+  if (gamma)
+    for (int i = threadIdx.x; i < dims; i += blockDim.x)
+      g[i] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(gamma)[i]) : static_cast<const float*>(gamma)[i];
+  __syncthreads();
+}
+
+// 8 normed values: x * inv * gamma.
+__device__ __forceinline__ void scale8(float (&v)[8], float inv, const float* g) {
+  const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
+  v[0] = v[0] * inv * a.x; v[1] = v[1] * inv * a.y; v[2] = v[2] * inv * a.z; v[3] = v[3] * inv * a.w;
+  v[4] = v[4] * inv * b.x; v[5] = v[5] * inv * b.y; v[6] = v[6] * inv * b.z; v[7] = v[7] * inv * b.w;
 }
 
 __device__ __forceinline__ float square8(const float (&v)[8], float sum) {
@@ -77,18 +80,26 @@ __device__ __forceinline__ float square8(const float (&v)[8], float sum) {
 
 // ---------------------------------------------------------------- queries
 constexpr int kQThreads = 256;
-constexpr int kQAhead = 2;  // warp steps (of 4 heads) whose loads are in flight before their stores
+#ifndef QAHEAD
+#define QAHEAD 2
+#define QMIN 4
+#define RAHEAD 4
+#define RMIN 3
+#endif
+constexpr int kQAhead = QAHEAD;  // warp steps (of 4 heads) whose loads are in flight before their stores
 
 // Warp task: token task / parts, its heads [part * per, part * per + per).
 template <bool kHalves>
-__global__ void __launch_bounds__(kQThreads) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
+__global__ void __launch_bounds__(kQThreads, QMIN) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
                                                                 const __nv_bfloat16* q, int64_t stride,
                                                                 const int64_t* __restrict__ pos, const void* gamma,
                                                                 int gamma_bf16, float eps,
                                                                 const float* __restrict__ inv_freq,
                                                                 __nv_bfloat16* out, int32_t* status) {
+  __shared__ __align__(16) float gamma_s[kQDims];
   const int64_t task = blockIdx.x * (int64_t)(kQThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = task / parts;
+  const int64_t t = parts == 1 ? task : (int64_t)((uint64_t)task / (uint32_t)parts);
+  load_gamma(gamma, gamma_bf16, kQDims, gamma_s);
   if (t >= T) return;
   const int lane = threadIdx.x & 31, l = lane & 7;  // lane of its row: dims 64 j + [8 l, 8 l + 8), j < 3
   const int64_t p = __ldg(pos + t);
@@ -96,7 +107,7 @@ __global__ void __launch_bounds__(kQThreads) q_norm_rope_kernel(int64_t T, int32
     if (p != -1 && lane == 0) flag(status, DCP_STATUS_BAD_POSITION);
     return;
   }
-  const int h0 = (int)(task % parts) * per, h1 = min(h0 + per, H);
+  const int h0 = (int)(task - t * parts) * per, h1 = min(h0 + per, H);
   // the first step's loads go out before anything else is worked out
   uint4 x[kQAhead][3];
   auto load = [&](int a, int h) {
@@ -110,10 +121,6 @@ __global__ void __launch_bounds__(kQThreads) q_norm_rope_kernel(int64_t T, int32
   const int hl = h0 + (lane >> 3);
 #pragma unroll
   for (int a = 0; a < kQAhead; ++a) load(a, hl + 4 * a);
-  float g[3][8];
-  if (gamma)
-#pragma unroll
-    for (int j = 0; j < 3; ++j) gamma8(gamma, gamma_bf16, 64 * j + 8 * l, g[j]);
   // this lane's angles: pairs (2 i, 2 i + 1) lie in one lane, halves (i, i + 32) in lanes l and l ^ 4
   constexpr int kTurns = kHalves ? 8 : 4;
   Turn turn[kTurns];
@@ -133,9 +140,7 @@ __global__ void __launch_bounds__(kQThreads) q_norm_rope_kernel(int64_t T, int32
         for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const float r = rsqrtf(sum * (1.f / kQDims) + eps);
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * r * g[j][k];
+        for (int j = 0; j < 3; ++j) scale8(v[j], r, gamma_s + 64 * j + 8 * l);
       }
       if (inv_freq) {
         if (kHalves) {
@@ -176,17 +181,19 @@ struct RowArgs {
   const int64_t* rope_pos;
 };
 
-constexpr int kRowAhead = 4;  // tokens whose loads are in flight before their stores
+constexpr int kRowAhead = RAHEAD;  // tokens whose loads are in flight before their stores
 
 template <bool kQ4>
-__global__ void __launch_bounds__(256) norm_rope_store_kernel(Layout L, int32_t shard_begin, int32_t shard_end,
+__global__ void __launch_bounds__(256, RMIN) norm_rope_store_kernel(Layout L, int32_t shard_begin, int32_t shard_end,
                                                               RowArgs in, const int64_t* __restrict__ pos,
                                                               const int32_t* __restrict__ req, int64_t T, int per_warp,
                                                               Table tab, unsigned char* __restrict__ arena,
                                                               int32_t* status) {
+  __shared__ __align__(16) float gamma_s[kDv];
   const int64_t t0 = (blockIdx.x * (int64_t)(blockDim.x / 32) + (threadIdx.x >> 5)) * per_warp;
   const int lane = threadIdx.x & 31;
   const int n = (int)min((int64_t)per_warp, T - t0);
+  load_gamma(in.gamma, in.gamma_bf16, kDv, gamma_s);
   if (n <= 0) return;
   Spot spot{-1, -1, 0};
   int64_t angle_pos = 0, to = -1;  // lane: of token t0 + lane
@@ -196,11 +203,6 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(Layout L, int32_t 
     spot = find_spot(p, __ldg(req + t0 + lane), L, tab, shard_begin, shard_end, status);
   }
   const uint64_t step = in.inv_freq ? turn_step(__ldg(in.inv_freq + lane)) : 0;  // lane: pair `lane`
-  float g[2][8];
-  if (in.gamma) {
-    gamma8(in.gamma, in.gamma_bf16, 8 * lane, g[0]);
-    gamma8(in.gamma, in.gamma_bf16, 256 + 8 * lane, g[1]);
-  }
   for (int i = 0; i < n; i += kRowAhead) {
     uint4 x[kRowAhead][2];
     uint32_t rope[kRowAhead];  // this lane's pair: dims 2 l, 2 l + 1 or l, l + 32
@@ -233,10 +235,8 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(Layout L, int32_t 
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const float inv = rsqrtf(sum * (1.f / kDv) + in.eps);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * inv * g[j][k];
+        scale8(v[0], inv, gamma_s + 8 * lane);
+        scale8(v[1], inv, gamma_s + 256 + 8 * lane);
         x[e][0] = pack8(v[0]);
         x[e][1] = pack8(v[1]);
       }

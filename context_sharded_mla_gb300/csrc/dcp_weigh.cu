@@ -39,13 +39,21 @@ constexpr int kMaxStages = 12;
 constexpr int kBlock = 4;                  // pair-tiles of a block when there is more than one row group
 constexpr int kRawTile = kKeys * kQ4RowBytes;
 constexpr int kMaxRaw = 3;
+// The tensor core cuts its running sum off toward zero at each of the 36 steps of a score instead of rounding it: half
+// a last place of the sum so far, a relative loss between 0 and 36 * 2^-24 that averages 16 * 2^-25 over the scores that
+// carry the weights (measured: weights 1.5e-6 low without this, 1e-7 off with it).
+constexpr double kTruncation = 0x1p-21;
 constexpr int kASlots = 8;                 // 32-column operand slots in TMEM (4-bit cache)
 constexpr int kACol = 256;
 constexpr uint32_t kAllCols = 512;
 
-// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8-15 dequantise
+// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8 on dequantise, in sets of four
+#ifndef SETS
+#define SETS 3
+#endif
+constexpr int kDequantSets = SETS;
 constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kDequantWarp = 8;
-constexpr int kThreads = 256, kThreadsQ4 = 512;
+constexpr int kThreads = 256, kThreadsQ4 = kThreads + 128 * kDequantSets;
 
 struct WeighArgs {
   Layout L;
@@ -275,8 +283,16 @@ __device__ __forceinline__ int32_t pool_row(const WeighArgs& a, int32_t rs, int3
   return (int32_t)(rs * a.pool_rows + page * a.L.P + rho % (int32_t)a.L.P);
 }
 
-// One 64-dim chunk of a 4-bit row: 8 words of codes and 4 scales -> 32 bf16 pairs.
-__device__ __forceinline__ void dequant_chunk(uint32_t row_s, int c, uint32_t (&v)[32]) {
+// One 64-dim chunk of a 4-bit row as it lies in shared memory: 8 words of codes and 4 scales, or 32 bf16 pairs.
+__device__ __forceinline__ void load_chunk(uint32_t row_s, int c, uint32_t (&w)[9]) {
+  if (c == kChunks - 1) return;
+  const uint4 lo = ld_shared_v4(row_s + 32 * c), hi = ld_shared_v4(row_s + 32 * c + 16);
+  w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+  w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+  w[8] = ld_shared_u32(row_s + kQ4ScaleOff + 4 * c);
+}
+// Its 32 bf16 pairs.
+__device__ __forceinline__ void dequant_chunk(uint32_t row_s, int c, const uint32_t (&w)[9], uint32_t (&v)[32]) {
   if (c == kChunks - 1) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -285,13 +301,10 @@ __device__ __forceinline__ void dequant_chunk(uint32_t row_s, int c, uint32_t (&
     }
     return;
   }
-  const uint4 lo = ld_shared_v4(row_s + 32 * c), hi = ld_shared_v4(row_s + 32 * c + 16);
-  const uint32_t four = ld_shared_u32(row_s + kQ4ScaleOff + 4 * c);
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t s2[2], off2[2];
-    q4_scales(half ? four >> 16 : four & 0xFFFFu, s2, off2);
+    q4_scales(half ? w[8] >> 16 : w[8] & 0xFFFFu, s2, off2);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t p[4];
@@ -343,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&bars[kRFull + i], 1);
-      mbar_init(&bars[kRFree + i], 8);
+      mbar_init(&bars[kRFree + i], 4 * kDequantSets);
     }
     fence_barrier_init();
   }
@@ -612,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     }
   } else if (kQ4 && warp >= kDequantWarp && any) {
     // ------------------------------------------------------------------ 4-bit rows -> operands in TMEM
-    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of every second chunk.
+    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of every kDequantSets-th chunk.
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
     uint32_t rb = 0, rph = 0, n = 0;  // raw tile and its parity; chunks so far
@@ -622,13 +635,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       ok = warp_wait(&bars[kRFull + rb], rph, abort_s, lane);
       const uint32_t row_s = smem_u32(smem) + sl.ring + rb * kRawTile + (quarter * 32 + lane) * kQ4RowBytes;
       for (int c = 0; c < kChunks && ok; ++c, ++n) {
-        if ((n & 1) != (uint32_t)set) continue;
+        if (n % kDequantSets != (uint32_t)set) continue;
         const uint32_t slot = n % kASlots;
+        uint32_t raw[9];
+        if (have) load_chunk(row_s, c, raw);
         ok = warp_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s, lane);
         if (!ok) break;
         if (have) {
           uint32_t v[32];
-          dequant_chunk(row_s, c, v);
+          dequant_chunk(row_s, c, raw, v);
           tc_fence_after();
           tmem_st32(lane_addr + 32 * slot, v);
           tmem_st_wait();
@@ -729,7 +744,7 @@ int32_t weigh(const WeighCall& c) {
   a.bt_stride = c.bt_stride;
   a.max_pages = c.max_pages;
   a.seq_lens = c.seq_lens;
-  a.scale_log2 = c.scale * kLog2e;
+  a.scale_log2 = (float)((double)c.scale * 1.4426950408889634 * (1.0 + kTruncation));
   a.base2 = c.lse_base == DCP_LSE_BASE_2;
   a.lse = c.lse;
   a.old_lens = c.old_lens;

@@ -204,3 +204,11 @@ def test_compact_beyond_four_gigabytes_on_another_stream():
     want = rows.clone()
     want[:200] = rows[k[0, 0].long()]
     assert int(status.item()) == 0 and torch.equal(arena[0, at], want)
+
+
+@pytest.mark.parametrize("value", [float("-inf"), -3e38, float("nan"), 0.0])
+@pytest.mark.parametrize("keep", [1, 700, 999, 1000])
+def test_select_of_equal_weights(value, keep):
+    w = np.full((1, 1, 1000), value, np.float32)
+    kept, status = run_select(w, [1000], [keep], 1, 1, 8, 0, 1, 0, 0)
+    assert status == 0 and kept[0, 0, :keep].tolist() == list(range(keep))
