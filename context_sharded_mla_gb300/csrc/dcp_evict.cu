@@ -73,12 +73,21 @@ struct Unit {
   uint32_t want;
 };
 
+// Rows of shard r below position x (32-bit division where it does: a 64-bit one is some hundred instructions).
+__device__ __forceinline__ int64_t rows_below(int64_t r, int64_t x, const Layout& L) {
+  const int64_t blk = L.N * L.I;
+  const int64_t k = ((x | blk) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)blk) : x / blk;
+  int64_t rem = x - k * blk - r * L.I;
+  rem = rem < 0 ? 0 : (rem > L.I ? L.I : rem);
+  return k * L.I + rem;
+}
+
 // Sets u up and writes its sinks and recent rows; false (for the whole cluster) where no row competes, or the unit is
 // refused.
 __device__ bool select_begin(const SelectArgs& a, int64_t unit, uint32_t rank, uint32_t nranks, Unit* u) {
   const int rs = (int)(unit / a.B), b = (int)(unit % a.B), tid = threadIdx.x;
   const int64_t S = a.seq_lens[b], M = a.new_lens[b], r = a.shard_begin + rs;
-  const int64_t m = M > 0 ? count_of(r, M, a.L) : 0, n = S > 0 ? count_of(r, S, a.L) : 0;
+  const int64_t m = M > 0 ? rows_below(r, M, a.L) : 0, n = S > 0 ? rows_below(r, S, a.L) : 0;
   int32_t* kept = a.kept + unit * a.kept_stride;
   if (M < 0 || M > S || n > a.w_stride || m > a.kept_stride) {
     if (tid == 0 && rank == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
@@ -86,8 +95,8 @@ __device__ bool select_begin(const SelectArgs& a, int64_t unit, uint32_t rank, u
     for (int64_t i = rank * kSelThreads + tid; i < e; i += nranks * kSelThreads) kept[i] = -1;
     return false;
   }
-  const int64_t lo = count_of(r, a.sinks < S ? a.sinks : S, a.L);
-  const int64_t zr = count_of(r, S > a.recent ? S - a.recent : 0, a.L);
+  const int64_t lo = rows_below(r, a.sinks < S ? a.sinks : S, a.L);
+  const int64_t zr = rows_below(r, S > a.recent ? S - a.recent : 0, a.L);
   const int64_t hi = zr > lo ? zr : lo, ns = lo < m ? lo : m, nr = m - ns < n - hi ? m - ns : n - hi;
   u->lo = (int32_t)lo;  // rows of a unit fit 31 bits (w_stride)
   u->hi = (int32_t)hi;
@@ -161,36 +170,44 @@ __device__ __forceinline__ void clear_hist(SelectSmem& sm) {
   __syncthreads();
 }
 
-// Units of at most kPer * 512 rows a CTA: every thread holds its kPer keys in registers (rows tid, tid + 512, ..; 0,
-// which is no weight's key, where there is none), so that the weights are read once.
+// Units of at most kPer * 512 rows a CTA: every thread holds its kPer keys in registers (warp w has rows
+// [32 kPer w, 32 kPer (w + 1)) of the CTA's, lane by lane; key 0, which is no weight's, where there is none), so that
+// the weights are read once.
 template <int kPer>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   __shared__ __align__(16) SelectSmem sm;
-  __shared__ uint32_t at_s[kPer * kSelWarps];  // rows at (<< 16) and above the limit, then their prefix sums
-  __shared__ uint32_t warp_s[kSelWarps];
+  __shared__ uint32_t warp_s[kSelWarps];  // rows at (<< 16) and above the limit (at most 16384: the halves do not meet)
   const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
   const int64_t unit = blockIdx.x / nranks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Unit u;
   if (!select_begin(a, unit, rank, nranks, &u)) return;
   const int32_t len = u.hi - u.lo, per = (len + nranks - 1) / nranks;
-  const int32_t c0 = min((int32_t)rank * per, len), c1 = min(c0 + per, len);
+  const int32_t c1 = min((int32_t)(rank + 1) * per, len);
+  const int32_t i0 = min((int32_t)rank * per, len) + warp * (32 * kPer) + lane;
   const float* w = a.weights + unit * a.w_stride + u.lo;
   uint32_t key[kPer];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int32_t i = c0 + k * kSelThreads + tid;
-    key[k] = i < c1 ? order_key(__ldg(w + i)) : 0u;
-  }
+  for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? __float_as_uint(__ldg(w + i0 + 32 * k)) : 0u;
+  clear_hist(sm);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? order_key(__uint_as_float(key[k])) : 0u;
   uint32_t limit = 0, want = u.want;
+  uint32_t* hist = sm.hist + lane;
 #pragma unroll 1
   for (int d = 0; d < kDigits; ++d) {
     const int shift = 24 - 8 * d;
-    const uint32_t mask = d ? 0xFFFFFFFFu << (shift + 8) : 0u;
-    clear_hist(sm);
+    if (d == 0) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (key[k] != 0 && (key[k] & mask) == limit) atomicAdd(&sm.hist[((key[k] >> shift) & 255u) * 32 + lane], 1u);
+      for (int k = 0; k < kPer; ++k)
+        if (key[k] != 0) atomicAdd(hist + (key[k] >> 24) * 32, 1u);
+    } else {
+      clear_hist(sm);
+      const uint32_t lead = limit >> (shift + 8);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)  // few are left after the first digit
+        if (key[k] >> (shift + 8) == lead && key[k] != 0) atomicAdd(hist + ((key[k] >> shift) & 255u) * 32, 1u);
+    }
     choose_bin(sm, d, want, nranks);
     limit |= sm.pick[0] << shift;
     want = sm.pick[1];
@@ -200,52 +217,51 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
       break;
     }
   }
-  // keys above the limit stay, and the first `want` of those at it, in row order: k, then warp, then lane
+  // keys above the limit stay, and the first `want` of those at it
+  int n = 0;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
-    if (lane == 0) at_s[k * kSelWarps + warp] = __popc(bg) | __popc(be) << 16;
-  }
+  for (int k = 0; k < kPer; ++k) n += (key[k] > limit) + (key[k] == limit && want ? 1 << 16 : 0);
+  n = warp_sum(n);
+  if (lane == 0) warp_s[warp] = n;
   __syncthreads();
-  {  // exclusive prefix sums (at most 16384 rows: the halves do not meet)
-    const uint32_t mine = tid < kPer * kSelWarps ? at_s[tid] : 0;
-    uint32_t incl = mine;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
-      if (lane >= s) incl += y;
-    }
-    if (lane == 31) warp_s[warp] = incl;
-    __syncthreads();
-    uint32_t before = 0, total = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-      if (i < warp) before += warp_s[i];
-      total += warp_s[i];
-    }
-    if (tid < kPer * kSelWarps) at_s[tid] = before + incl - mine;
+  uint32_t gt = 0, eq = 0, total = 0;  // rows before this warp's
+  for (int i = 0; i < kSelWarps; ++i) {
+    const uint32_t c = warp_s[i];
+    if (i < warp) gt += c;
+    total += c;
+  }
+  eq = gt >> 16;
+  gt &= 0xFFFFu;
+  if (nranks > 1) {
     if (tid == 0) {
       sm.cta_n[0] = total & 0xFFFFu;
       sm.cta_n[1] = total >> 16;
     }
-  }
-  uint32_t gt0 = 0, eq0 = 0;  // rows of the CTAs before
-  if (nranks > 1) {
     cluster_sync();
     for (uint32_t c = 0; c < rank; ++c) {
-      gt0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[0]), c));
-      eq0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[1]), c));
+      gt += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[0]), c));
+      eq += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[1]), c));
     }
   }
-  __syncthreads();
   int32_t* kept = a.kept + unit * a.kept_stride + u.ns;
   const uint32_t below = (1u << lane) - 1;
+  if (want == 0) {  // no tie to cut
+    kept += gt;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
-    const uint32_t at = at_s[k * kSelWarps + warp];
-    const uint32_t eq = eq0 + (at >> 16) + __popc(be & below);
-    if (key[k] > limit || (key[k] == limit && eq < want))
-      kept[gt0 + (at & 0xFFFFu) + __popc(bg & below) + min(eq, want)] = u.lo + c0 + k * kSelThreads + tid;
+    for (int k = 0; k < kPer; ++k) {
+      const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit);
+      if (key[k] > limit) kept[__popc(bg & below)] = u.lo + i0 + 32 * k;
+      kept += __popc(bg);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
+      const uint32_t e = eq + __popc(be & below);
+      if (key[k] > limit || (key[k] == limit && e < want)) kept[gt + __popc(bg & below) + min(e, want)] = u.lo + i0 + 32 * k;
+      gt += __popc(bg);
+      eq += __popc(be);
+    }
   }
   if (nranks > 1) cluster_sync();  // no CTA leaves while its counts are read
 }
@@ -390,7 +406,7 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
   const int64_t u = blockIdx.x / nranks;
   const int rs = (int)(u / a.B), b = (int)(u % a.B), lane = threadIdx.x;
   const int64_t M = a.new_lens[b];
-  const int64_t m64 = M > 0 ? count_of(a.shard_begin + rs, M, a.L) : 0;
+  const int64_t m64 = M > 0 ? rows_below(a.shard_begin + rs, M, a.L) : 0;
   if (M < 0 || m64 > a.kept_stride) {  // uniform over the cluster
     if (lane == 0 && rank == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
     return;

@@ -80,92 +80,99 @@ __device__ __forceinline__ float square8(const float (&v)[8], float sum) {
 
 // ---------------------------------------------------------------- queries
 constexpr int kQThreads = 256;
-#ifndef QAHEAD
-#define QAHEAD 2
+#ifndef QMIN
 #define QMIN 4
-#define RAHEAD 4
-#define RMIN 3
+#define RAHEAD 2
+#define RMIN 4
 #endif
-constexpr int kQAhead = QAHEAD;  // warp steps (of 4 heads) whose loads are in flight before their stores
 
-// Warp task: token task / parts, its heads [part * per, part * per + per).
+// Warp task: token task / parts, its heads [part * per, part * per + per).  The next step's row is on its way while
+// this one's is worked on; sines lie in shared memory (an angle is computed once a warp, by lane `pair`).
 template <bool kHalves>
 __global__ void __launch_bounds__(kQThreads, QMIN) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
-                                                                const __nv_bfloat16* q, int64_t stride,
-                                                                const int64_t* __restrict__ pos, const void* gamma,
-                                                                int gamma_bf16, float eps,
-                                                                const float* __restrict__ inv_freq,
-                                                                __nv_bfloat16* out, int32_t* status) {
+                                                                   const __nv_bfloat16* q, int64_t stride,
+                                                                   const int64_t* __restrict__ pos, const void* gamma,
+                                                                   int gamma_bf16, float eps,
+                                                                   const float* __restrict__ inv_freq,
+                                                                   __nv_bfloat16* out, int32_t* status) {
   __shared__ __align__(16) float gamma_s[kQDims];
+  __shared__ __align__(16) float2 turn_s[kQThreads / 32][kRope / 2];
   const int64_t task = blockIdx.x * (int64_t)(kQThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = parts == 1 ? task : (int64_t)((uint64_t)task / (uint32_t)parts);
-  load_gamma(gamma, gamma_bf16, kQDims, gamma_s);
-  if (t >= T) return;
   const int lane = threadIdx.x & 31, l = lane & 7;  // lane of its row: dims 64 j + [8 l, 8 l + 8), j < 3
-  const int64_t p = __ldg(pos + t);
+  const int h0 = (int)(task - t * parts) * per, h1 = min(h0 + per, H);
+  const __nv_bfloat16* src = q + (t * H + h0 + (lane >> 3)) * stride + 8 * l;
+  uint4 x[3];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      x[j] = h < h1 ? *reinterpret_cast<const uint4*>(src + 64 * j) : make_uint4(0, 0, 0, 0);
+    src += 4 * stride;
+  };
+  int h = h0 + (lane >> 3);
+  int64_t p = -1;
+  if (t < T) {
+    p = __ldg(pos + t);
+    load(h);
+  }
+  if (inv_freq && t < T) {
+    const Turn turn = turn_of(turn_step(__ldg(inv_freq + lane)), p);
+    turn_s[threadIdx.x >> 5][lane] = make_float2(turn.s, turn.c);
+  }
+  load_gamma(gamma, gamma_bf16, kQDims, gamma_s);
   if (p < 0) {
-    if (p != -1 && lane == 0) flag(status, DCP_STATUS_BAD_POSITION);
+    if (t < T && p != -1 && lane == 0) flag(status, DCP_STATUS_BAD_POSITION);
     return;
   }
-  const int h0 = (int)(task - t * parts) * per, h1 = min(h0 + per, H);
-  // the first step's loads go out before anything else is worked out
-  uint4 x[kQAhead][3];
-  auto load = [&](int a, int h) {
+  // pairs (2 i, 2 i + 1) lie in one lane, halves (i, i + 32) in lanes l and l ^ 4
+  const float4* turns = reinterpret_cast<const float4*>(turn_s[threadIdx.x >> 5] + (kHalves ? 8 * (l & 3) : 4 * l));
+  __nv_bfloat16* dst = out + (t * H + h) * (int64_t)kQDims + 8 * l;
+  for (; h - (lane >> 3) < h1; h += 4) {
+    uint4 y[3] = {x[0], x[1], x[2]};
+    load(h + 4);
+    float r = 1.f, v[8];
+    if (gamma) {
+      float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 3; ++j) x[a][j] = make_uint4(0, 0, 0, 0);
-    if (h >= h1) return;
-    const uint4* src = reinterpret_cast<const uint4*>(q + (t * H + h) * stride) + l;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) x[a][j] = src[8 * j];
-  };
-  const int hl = h0 + (lane >> 3);
-#pragma unroll
-  for (int a = 0; a < kQAhead; ++a) load(a, hl + 4 * a);
-  // this lane's angles: pairs (2 i, 2 i + 1) lie in one lane, halves (i, i + 32) in lanes l and l ^ 4
-  constexpr int kTurns = kHalves ? 8 : 4;
-  Turn turn[kTurns];
-  if (inv_freq)
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k)
-      turn[k] = turn_of(turn_step(__ldg(inv_freq + (kHalves ? 8 * (l & 3) : 4 * l) + k)), p);
-  for (int h = hl; h - (lane >> 3) < h1; h += 4 * kQAhead) {
-#pragma unroll
-    for (int a = 0; a < kQAhead; ++a) {
-      float v[3][8];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) unpack8(x[a][j], v[j]);
-      if (gamma) {
-        float sum = square8(v[2], square8(v[1], square8(v[0], 0.f)));
-#pragma unroll
-        for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        const float r = rsqrtf(sum * (1.f / kQDims) + eps);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) scale8(v[j], r, gamma_s + 64 * j + 8 * l);
+      for (int j = 0; j < 3; ++j) {
+        unpack8(y[j], v);
+        sum = square8(v, sum);
       }
-      if (inv_freq) {
-        if (kHalves) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float o = __shfl_xor_sync(0xffffffffu, v[2][k], 4);
-            v[2][k] = fmaf(v[2][k], turn[k].c, l < 4 ? -o * turn[k].s : o * turn[k].s);
-          }
+      for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      r = rsqrtf(sum * (1.f / kQDims) + eps);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        unpack8(y[j], v);
+        scale8(v, r, gamma_s + 64 * j + 8 * l);
+        y[j] = pack8(v);
+      }
+    }
+    unpack8(y[2], v);
+    if (gamma) scale8(v, r, gamma_s + 128 + 8 * l);
+    if (inv_freq) {
+#pragma unroll
+      for (int k = 0; k < (kHalves ? 4 : 2); ++k) {
+        const float4 sc = turns[k];  // sine, cosine of two angles
+        if (kHalves) {
+          const float a = __shfl_xor_sync(0xffffffffu, v[2 * k], 4), b = __shfl_xor_sync(0xffffffffu, v[2 * k + 1], 4);
+          v[2 * k] = fmaf(v[2 * k], sc.y, l < 4 ? -a * sc.x : a * sc.x);
+          v[2 * k + 1] = fmaf(v[2 * k + 1], sc.w, l < 4 ? -b * sc.z : b * sc.z);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float u = v[2][2 * k], w = v[2][2 * k + 1];
-            v[2][2 * k] = fmaf(u, turn[k].c, -w * turn[k].s);
-            v[2][2 * k + 1] = fmaf(u, turn[k].s, w * turn[k].c);
+          for (int e = 0; e < 2; ++e) {
+            const float s = e ? sc.z : sc.x, c = e ? sc.w : sc.y, a = v[4 * k + 2 * e], b = v[4 * k + 2 * e + 1];
+            v[4 * k + 2 * e] = fmaf(a, c, -b * s);
+            v[4 * k + 2 * e + 1] = fmaf(a, s, b * c);
           }
         }
       }
-      const int hh = h + 4 * a;
-      if (hh < h1) {
-        uint4* dst = reinterpret_cast<uint4*>(out + (t * H + hh) * (int64_t)kQDims) + l;
-#pragma unroll
-        for (int j = 0; j < 3; ++j) dst[8 * j] = pack8(v[j]);
-      }
-      load(a, hh + 4 * kQAhead);
     }
+    y[2] = pack8(v);
+    if (h < h1)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(dst + 64 * j) = y[j];
+    dst += 4 * kQDims;
   }
 }
 
@@ -228,17 +235,21 @@ __global__ void __launch_bounds__(256, RMIN) norm_rope_store_kernel(Layout L, in
     for (int e = 0; e < kRowAhead; ++e) {
       const int64_t r = __shfl_sync(0xffffffffu, to, i + e), ap = __shfl_sync(0xffffffffu, angle_pos, i + e);
       if (in.gamma) {
-        float v[2][8];
-        unpack8(x[e][0], v[0]);
-        unpack8(x[e][1], v[1]);
-        float sum = square8(v[1], square8(v[0], 0.f));
+        float v[8], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          unpack8(x[e][j], v);
+          sum = square8(v, sum);
+        }
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const float inv = rsqrtf(sum * (1.f / kDv) + in.eps);
-        scale8(v[0], inv, gamma_s + 8 * lane);
-        scale8(v[1], inv, gamma_s + 256 + 8 * lane);
-        x[e][0] = pack8(v[0]);
-        x[e][1] = pack8(v[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          unpack8(x[e][j], v);
+          scale8(v, inv, gamma_s + 256 * j + 8 * lane);
+          x[e][j] = pack8(v);
+        }
       }
       if (in.inv_freq) {
         const Turn t = turn_of(step, ap);

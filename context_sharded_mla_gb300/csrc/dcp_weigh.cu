@@ -425,6 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     // A lane a copy; the next tile's page ids are on their way while this one's copies go out.
     if (lane == 0) prefetch_tmap(&tmap_kv);
     int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
+    const int32_t box = 4 * lane / a.box_rows, in_box = 4 * lane - box * a.box_rows;  // this lane's four rows of a tile
     uint32_t st = 0, ph = 0;
     bool ok = true, more = true;
     uint32_t tiles = 0;
@@ -439,9 +440,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull + st], __popc(who) * a.box_rows * kQ4RowBytes);
         __syncwarp();
-        if (y >= 0)
-          bulk_load(smem + sl.ring + st * kRawTile + lane * a.box_rows * kQ4RowBytes, a.arena + (int64_t)y * kQ4RowBytes,
-                    a.box_rows * kQ4RowBytes, &bars[kRFull + st]);
+        const int32_t yl = __shfl_sync(0xffffffffu, y, box);
+        if (yl >= 0)
+          bulk_load(smem + sl.ring + st * kRawTile + 4 * lane * kQ4RowBytes, a.arena + (int64_t)(yl + in_box) * kQ4RowBytes,
+                    4 * kQ4RowBytes, &bars[kRFull + st]);
         if (++st == (uint32_t)a.stages) {
           st = 0;
           ph ^= 1;
@@ -494,44 +496,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     for (int c = 0; c < kChunks && ok; ++c) ok = warp_wait(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
   } else if (warp == kMmaWarp && any && rank == 0) {
     // ------------------------------------------------------------------ products (the leader's alone)
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(2 * kKeys, a.Rg, 0, 0);
-      const uint64_t kdesc = sw128_desc(smem_u32(smem) + sl.ring, 16, 1024);
-      const uint64_t qdesc = sw128_desc(smem_u32(smem) + sl.q, 16, 1024);
-      uint32_t st = 0, ph = 0, qph = 0, j = 0;
-      bool ok = true, more = true;
-      while (more && ok) {
-        const bool first = w.first(), last = w.last();
-        const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
-        ok = mbar_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
-        for (int c = 0; c < kChunks && ok; ++c) {
-          if (first) ok = mbar_wait(&bars[kQFull + c], qph, abort_s);
-          ok = ok && mbar_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t qd = qdesc + c * (q_chunk >> 4);
+    // The whole warp walks and waits, one lane issues: the operands' descriptors are then uniform values.  (With one
+    // lane in a loop of its own each product's came through vector registers, 760 cycles a chunk in all.)
+    const bool one = elect_one();
+    const uint32_t idesc = idesc_bf16_f32(2 * kKeys, a.Rg, 0, 0);
+    const uint64_t kdesc = sw128_desc(smem_u32(smem) + sl.ring, 16, 1024);
+    const uint64_t qdesc = sw128_desc(smem_u32(smem) + sl.q, 16, 1024);
+    const uint32_t slots = kQ4 ? kASlots : a.stages;
+    uint32_t st = 0, ph = 0, qph = 0, j = 0;
+    bool ok = true, more = true;
+    while (more && ok) {
+      const bool first = w.first(), last = w.last();
+      const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
+      ok = warp_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s, lane);
+      for (int c = 0; c < kChunks && ok; ++c) {
+        if (first) ok = warp_wait(&bars[kQFull + c], qph, abort_s, lane);
+        ok = ok && warp_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s, lane);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = qdesc + c * (q_chunk >> 4), kd = kdesc + st * (kStageBytes >> 4);
+        const uint32_t kt = tmem + kACol + 32 * st;
+        if (one) {
 #pragma unroll
           for (int k = 0; k < kChunkDims / 16; ++k) {
             if (kQ4)
-              mma_pair_ts(d, tmem + kACol + 32 * st + 8 * k, qd + 2 * k, idesc, (c | k) != 0);
+              mma_pair_ts(d, kt + 8 * k, qd + 2 * k, idesc, (c | k) != 0);
             else
-              mma_pair_ss(d, kdesc + st * (kStageBytes >> 4) + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
+              mma_pair_ss(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
           }
           commit_pair(&bars[(kQ4 ? kAEmpty : kEmpty) + st]);
           if (last) commit_pair(&bars[kQEmpty + c]);
-          if (++st == (uint32_t)(kQ4 ? kASlots : a.stages)) {
-            st = 0;
-            ph ^= 1;
-          }
+          if (c == kChunks - 1) commit_pair(&bars[kSFull + buf]);
         }
-        if (!ok) break;
-        commit_pair(&bars[kSFull + buf]);
-        if (first) qph ^= 1;
-        ++j;
-        more = w.next(a, rank);
+        __syncwarp();
+        if (++st == slots) {
+          st = 0;
+          ph ^= 1;
+        }
       }
+      if (!ok) break;
+      if (first) qph ^= 1;
+      ++j;
+      more = w.next(a, rank);
     }
-    __syncwarp();
   } else if (warp < 4 && any) {
     // ------------------------------------------------------------------ sums: a thread a key
     const float c = a.scale_log2;
