@@ -194,17 +194,21 @@ struct Walk {
   int32_t b, left;           // request; pair-tiles left, this block's included
   int32_t pt, npt;           // block's first pair-tile, pair-tiles of the request
   int32_t nblk, g, i;        // pair-tiles of the block, row group, pair-tile within the block
-  int32_t rs0, t0, rs, t;    // this CTA's tile: shard and tile of it, at the block's start and now (rs == n_held: none)
+  int32_t rs, t, rows, nt;   // this CTA's tile: shard (n_held: none), tile of it; the shard's rows and tiles
+  int32_t rs0, t0, rows0, nt0;  // the same at the block's start
   Shape sh;
   int64_t S_next;            // the next request's length, already loaded
 
+  __device__ void shard(const WeighArgs& a, int32_t r) {
+    rs = r;
+    rows = r < a.n_held ? sh.rows(a, r) : 0;
+    nt = (rows + kKeys - 1) / kKeys;
+  }
   __device__ void advance(const WeighArgs& a, int32_t by) {
     t += by;
-    while (rs < a.n_held) {
-      const int32_t n = sh.tiles(a, rs);
-      if (t < n) break;
-      t -= n;
-      ++rs;
+    while (t >= nt && rs < a.n_held) {
+      t -= nt;
+      shard(a, rs + 1);
     }
   }
   __device__ void block(const WeighArgs& a) {
@@ -213,23 +217,23 @@ struct Walk {
     g = i = 0;
     rs0 = rs;
     t0 = t;
+    rows0 = rows;
+    nt0 = nt;
   }
   __device__ void request(const WeighArgs& a, int64_t S) {
     sh.set(a, S);
     npt = sh.pair_tiles(a);
     S_next = b + 1 < a.B ? __ldg(a.seq_lens + b + 1) : 0;
   }
-  __device__ bool start(const WeighArgs& a, int32_t b_, int32_t pt_, int32_t n, int rank) {
+  __device__ void start(const WeighArgs& a, int32_t b_, int32_t pt_, int32_t n, int rank) {
     left = n;
-    if (n <= 0) return false;
     b = b_;
     pt = pt_;
     request(a, __ldg(a.seq_lens + b));
-    rs = 0;
     t = 0;
+    shard(a, 0);
     advance(a, 2 * pt + rank);
     block(a);
-    return true;
   }
   __device__ bool next(const WeighArgs& a, int rank) {
     if (++i < nblk) {
@@ -240,6 +244,8 @@ struct Walk {
     if (++g < a.ngroups) {
       rs = rs0;
       t = t0;
+      rows = rows0;
+      nt = nt0;
       return true;
     }
     left -= nblk;
@@ -253,8 +259,8 @@ struct Walk {
         request(a, S_next);
       } while (npt == 0);
       pt = 0;
-      rs = 0;
       t = 0;
+      shard(a, 0);
       advance(a, rank);
     }
     block(a);
@@ -268,7 +274,7 @@ struct Walk {
 __device__ __forceinline__ int32_t box_row(const WeighArgs& a, const Walk& w, int box) {
   if (w.rs >= a.n_held || box >= a.nbox) return -1;
   const int32_t rho = w.t * kKeys + box * a.box_rows;
-  return rho < w.sh.rows(a, w.rs) ? rho : -1;
+  return rho < w.rows ? rho : -1;
 }
 __device__ __forceinline__ int32_t page_of(const WeighArgs& a, const Walk& w, int32_t rho) {
   return rho < 0 ? -1 : __ldg(a.bt + (int64_t)w.b * a.bt_stride + rho / (int32_t)a.L.P);
@@ -417,7 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   const uint32_t tmem = *tmem_base_s;
   const uint32_t lead = mapa_shared(smem_u32(bars), 0);  // the leader's barriers
   Walk w;
-  const bool any = w.start(a, start_s[0], start_s[1], start_s[2], rank);
+  const bool any = start_s[2] > 0;
+  if (any && (!kQ4 || warp < kDequantWarp)) w.start(a, start_s[0], start_s[1], start_s[2], rank);
   const uint32_t q_chunk = (uint32_t)a.Rg / 2 * 128;
 
   if (warp == kKeyWarp && any) {
@@ -559,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       // this thread's key
       const int32_t row = w.t * kKeys + warp * 32 + lane;
       const bool done = w.g == a.ngroups - 1;
-      bool live = w.rs < a.n_held && row < w.sh.rows(a, w.rs);
+      const bool live = row < w.rows;
       int32_t page = 0, col0 = 0;
       float old = 0.f;
       float* wp = nullptr;
@@ -632,30 +639,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     }
   } else if (kQ4 && warp >= kDequantWarp && any) {
     // ------------------------------------------------------------------ 4-bit rows -> operands in TMEM
-    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of every kDequantSets-th chunk.
+    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of chunks s, s + kDequantSets, ..  Every pair-tile of the run is met
+    // once a row group; a CTA without a tile in the last of a request turns over what its slot holds, for nobody.
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
-    uint32_t rb = 0, rph = 0, n = 0;  // raw tile and its parity; chunks so far
-    bool ok = true, more = true;
-    while (more && ok) {
-      const bool have = w.rs < a.n_held;  // a CTA may have no tile in the last pair-tile of a request
+    const uint32_t tiles = (uint32_t)start_s[2] * a.ngroups;
+    uint32_t rb = 0, rph = 0;  // raw tile and its parity
+    bool ok = true;
+    for (uint32_t j = 0; j < tiles && ok; ++j) {
       ok = warp_wait(&bars[kRFull + rb], rph, abort_s, lane);
       const uint32_t row_s = smem_u32(smem) + sl.ring + rb * kRawTile + (quarter * 32 + lane) * kQ4RowBytes;
-      for (int c = 0; c < kChunks && ok; ++c, ++n) {
-        if (n % kDequantSets != (uint32_t)set) continue;
-        const uint32_t slot = n % kASlots;
-        uint32_t raw[9];
-        if (have) load_chunk(row_s, c, raw);
+#pragma unroll 1
+      for (int c = set; c < kChunks && ok; c += kDequantSets) {
+        const uint32_t n = j * kChunks + c, slot = n % kASlots;
+        uint32_t raw[9], v[32];
+        load_chunk(row_s, c, raw);
         ok = warp_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s, lane);
         if (!ok) break;
-        if (have) {
-          uint32_t v[32];
-          dequant_chunk(row_s, c, raw, v);
-          tc_fence_after();
-          tmem_st32(lane_addr + 32 * slot, v);
-          tmem_st_wait();
-          tc_fence_before();
-        }
+        dequant_chunk(row_s, c, raw, v);
+        tc_fence_after();
+        tmem_st32(lane_addr + 32 * slot, v);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(lead + 8 * (kAFull + slot));
       }
@@ -665,9 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         rb = 0;
         rph ^= 1;
       }
-      more = w.next(a, rank);
     }
     // the operand slots' last releases land before the CTA may leave
+    const uint32_t n = tiles * kChunks;
     for (uint32_t s = 0; s < kASlots && s < n && ok; ++s) {
       const uint32_t uses = (n - 1 - s) / kASlots;
       ok = warp_wait(&bars[kAEmpty + s], uses & 1, abort_s, lane);
