@@ -19,6 +19,7 @@
 // windows ahead), and writes it when every CTA of the cluster has its part of it.
 // Memory-bound: 2 * 1152 (or 416) bytes a row; a warp issues everything.
 #include "dcp_internal.cuh"
+
 #include "sm100_ptx.cuh"
 
 using namespace dcp;
@@ -43,10 +44,8 @@ struct SelectArgs {
 
 // Unsigned integers in the order of the weights; a NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float w) {
-  const uint32_t u = __float_as_uint(w);
-  if (w != w) return 0xFFFFFFFFu;
-  if (w == 0.f) return 0x80000000u;
-  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  const uint32_t u = __float_as_uint(__fadd_rn(w, 0.f));  // -0 becomes 0, a NaN 0x7fffffff
+  return w != w ? 0xFFFFFFFFu : u ^ (0x80000000u | (uint32_t)((int32_t)u >> 31));
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -109,25 +108,36 @@ __device__ bool select_begin(const SelectArgs& a, int64_t unit, uint32_t rank, u
   return u->want != 0;
 }
 
+constexpr int kCopies = 16;                 // of a histogram of 256 bins: lanes l and l + 16 share one
+constexpr int kTopBits = 12, kTopBins = 1 << kTopBits;  // first digit of the keys in registers: one copy of 4096 bins
+constexpr int kFewKeys = 2048;              // candidates that get a list of their own
 struct SelectSmem {
-  uint32_t hist[kBins * 32];         // a copy a lane
+  uint32_t hist[kBins * kCopies];    // or [kTopBins]
   uint32_t total[kDigits][kBins];    // this CTA's counts of each digit's bins, read by the cluster
   uint32_t all[kBins];
   uint32_t pick[3];                  // chosen bin, rows still wanted of it, rows in it
   uint32_t cta_n[2];                 // rows above and at the limit
 };
+static_assert(kTopBins == kBins * kCopies, "one buffer for both");
+
+__device__ __forceinline__ void clear_hist(SelectSmem& sm) {
+  for (int i = threadIdx.x; i < kTopBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
+__device__ __forceinline__ void count_digit(SelectSmem& sm, uint32_t digit) {
+  atomicAdd(&sm.hist[digit * kCopies + (threadIdx.x & (kCopies - 1))], 1u);
+}
 
 // After a digit's histogram: the bin that holds the want-th largest of the cluster's candidates.
 __device__ void choose_bin(SelectSmem& sm, int d, uint32_t want, uint32_t nranks) {
   const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();
-  {
-    const int bin = tid >> 1;
+  if (tid < kBins) {
     uint32_t s = 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += sm.hist[bin * 32 + 16 * (tid & 1) + ((k + (tid >> 1)) & 15)];
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    if (!(tid & 1)) sm.total[d][bin] = s;
+    for (int k = 0; k < kCopies; ++k) s += sm.hist[tid * kCopies + ((k + tid) & (kCopies - 1))];
+    sm.total[d][tid] = s;
   }
   if (nranks > 1) {
     cluster_sync();
@@ -165,17 +175,59 @@ __device__ void choose_bin(SelectSmem& sm, int d, uint32_t want, uint32_t nranks
   __syncthreads();
 }
 
-__device__ __forceinline__ void clear_hist(SelectSmem& sm) {
-  for (int i = threadIdx.x; i < kBins * 32 / 4; i += kSelThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0, 0, 0, 0);
+// The same for the first digit of the keys in registers, 4096 bins: 8 a thread, from the top.
+__device__ void choose_top(SelectSmem& sm, uint32_t* warp_s, uint32_t want, uint32_t nranks) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (nranks > 1) cluster_sync(); else __syncthreads();
+  uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s = 0;  // bins from 4088 - 8 tid on, lowest first
+  const uint32_t at = smem_u32(sm.hist + (kTopBins - 8 - 8 * tid));
+  for (uint32_t r = 0; r < nranks; ++r) {
+    const uint32_t from = nranks > 1 ? mapa_shared(at, r) : at;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t x[4];
+      asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                   : "r"(from + 16 * k)
+                   : "memory");
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[4 * k + e] += x[e];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += c[k];
+  uint32_t incl = s;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, x);
+    if (lane >= x) incl += y;
+  }
+  if (lane == 31) warp_s[warp] = incl;
+  if (nranks > 1) cluster_sync(); else __syncthreads();  // and every count has been read
+  uint32_t before = incl - s;
+  for (int i = 0; i < warp; ++i) before += warp_s[i];
+  if (before < want && want <= before + s) {  // exactly one thread
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+      if (before < want && want <= before + c[k]) {
+        sm.pick[0] = kTopBins - 8 - 8 * tid + k;
+        sm.pick[1] = want - before;
+        sm.pick[2] = c[k];
+      }
+      before += c[k];
+    }
+  }
   __syncthreads();
 }
 
 // Units of at most kPer * 512 rows a CTA: every thread holds its kPer keys in registers (warp w has rows
-// [32 kPer w, 32 kPer (w + 1)) of the CTA's, lane by lane; key 0, which is no weight's, where there is none), so that
-// the weights are read once.
+// [32 kPer w, 32 kPer (w + 1)) of the CTA's, lane by lane; key 0, which is no weight's and lies below all, where there
+// is none), so that the weights are read once.  Few keys share a first digit of 12 bits: those of the chosen bin go to
+// a list, and the other digits are looked for there.
 template <int kPer>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   __shared__ __align__(16) SelectSmem sm;
+  __shared__ uint32_t few[kFewKeys];
   __shared__ uint32_t warp_s[kSelWarps];  // rows at (<< 16) and above the limit (at most 16384: the halves do not meet)
   const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
   const int64_t unit = blockIdx.x / nranks;
@@ -185,53 +237,82 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   const int32_t len = u.hi - u.lo, per = (len + nranks - 1) / nranks;
   const int32_t c1 = min((int32_t)(rank + 1) * per, len);
   const int32_t i0 = min((int32_t)rank * per, len) + warp * (32 * kPer) + lane;
-  const float* w = a.weights + unit * a.w_stride + u.lo;
+  const float* w = a.weights + unit * a.w_stride + u.lo + i0;
   uint32_t key[kPer];
+  const bool whole = i0 - lane + 32 * kPer <= c1;  // uniform over the warp
+  if (whole) {
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? __float_as_uint(__ldg(w + i0 + 32 * k)) : 0u;
+    for (int k = 0; k < kPer; ++k) key[k] = __float_as_uint(__ldg(w + 32 * k));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? __float_as_uint(__ldg(w + 32 * k)) : 0u;
+  }
   clear_hist(sm);
+  if (tid == 0) sm.cta_n[0] = 0;
+  if (whole) {
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? order_key(__uint_as_float(key[k])) : 0u;
-  uint32_t limit = 0, want = u.want;
-  uint32_t* hist = sm.hist + lane;
-#pragma unroll 1
-  for (int d = 0; d < kDigits; ++d) {
-    const int shift = 24 - 8 * d;
-    if (d == 0) {
+    for (int k = 0; k < kPer; ++k) key[k] = order_key(__uint_as_float(key[k]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) key[k] = i0 + 32 * k < c1 ? order_key(__uint_as_float(key[k])) : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) atomicAdd(&sm.hist[key[k] >> (32 - kTopBits)], 1u);
+  uint32_t want = u.want;
+  choose_top(sm, warp_s, want, nranks);
+  uint32_t limit = sm.pick[0] << (32 - kTopBits);
+  want = sm.pick[1];
+  if (want < sm.pick[2]) {
+    const bool listed = nranks == 1 && sm.pick[2] <= kFewKeys;
+    const uint32_t n = sm.pick[2];
+    if (listed) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
-        if (key[k] != 0) atomicAdd(hist + (key[k] >> 24) * 32, 1u);
-    } else {
+        if (key[k] >> (32 - kTopBits) == limit >> (32 - kTopBits)) few[atomicAdd(&sm.cta_n[0], 1u)] = key[k];
+    }
+#pragma unroll 1
+    for (int d = 0; d < 3; ++d) {  // 8, 8 and 4 bits
+      const int shift = d == 0 ? 12 : d == 1 ? 4 : 0, above = shift + (d == 2 ? 4 : 8);
+      const uint32_t bins = (1u << (above - shift)) - 1;
       clear_hist(sm);
-      const uint32_t lead = limit >> (shift + 8);
+      if (listed) {
+        for (uint32_t i = tid; i < n; i += kSelThreads) {
+          const uint32_t x = few[i];
+          if ((x ^ limit) >> above == 0) count_digit(sm, x >> shift & bins);
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)  // few are left after the first digit
-        if (key[k] >> (shift + 8) == lead && key[k] != 0) atomicAdd(hist + ((key[k] >> shift) & 255u) * 32, 1u);
+        for (int k = 0; k < kPer; ++k)
+          if ((key[k] ^ limit) >> above == 0) count_digit(sm, key[k] >> shift & bins);
+      }
+      choose_bin(sm, d, want, nranks);
+      limit |= sm.pick[0] << shift;
+      want = sm.pick[1];
+      if (want == sm.pick[2]) break;
     }
-    choose_bin(sm, d, want, nranks);
-    limit |= sm.pick[0] << shift;
-    want = sm.pick[1];
-    if (want == sm.pick[2]) {  // the whole bin stays: every key from `limit` on (no weight's key is 0)
-      limit = limit ? limit - 1 : 0;
-      want = 0;
-      break;
-    }
+  }
+  if (want == sm.pick[2]) {  // the whole bin stays: every key from `limit` on
+    limit = limit ? limit - 1 : 0;
+    want = 0;
   }
   // keys above the limit stay, and the first `want` of those at it
-  int n = 0;
+  uint32_t gt = 0, eq = 0;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) n += (key[k] > limit) + (key[k] == limit && want ? 1 << 16 : 0);
-  n = warp_sum(n);
-  if (lane == 0) warp_s[warp] = n;
+  for (int k = 0; k < kPer; ++k) gt += __popc(__ballot_sync(0xffffffffu, key[k] > limit));
+  if (want)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) eq += __popc(__ballot_sync(0xffffffffu, key[k] == limit));
+  __syncthreads();  // warp_s has been read
+  if (lane == 0) warp_s[warp] = gt | eq << 16;
   __syncthreads();
-  uint32_t gt = 0, eq = 0, total = 0;  // rows before this warp's
+  uint32_t before = 0, total = 0;
   for (int i = 0; i < kSelWarps; ++i) {
     const uint32_t c = warp_s[i];
-    if (i < warp) gt += c;
+    if (i < warp) before += c;
     total += c;
   }
-  eq = gt >> 16;
-  gt &= 0xFFFFu;
+  gt = before & 0xFFFFu;
+  eq = before >> 16;
   if (nranks > 1) {
     if (tid == 0) {
       sm.cta_n[0] = total & 0xFFFFu;
@@ -245,12 +326,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
   }
   int32_t* kept = a.kept + unit * a.kept_stride + u.ns;
   const uint32_t below = (1u << lane) - 1;
+  const int32_t row = u.lo + i0;
   if (want == 0) {  // no tie to cut
     kept += gt;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit);
-      if (key[k] > limit) kept[__popc(bg & below)] = u.lo + i0 + 32 * k;
+      if (key[k] > limit) kept[__popc(bg & below)] = row + 32 * k;
       kept += __popc(bg);
     }
   } else {
@@ -258,7 +340,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
     for (int k = 0; k < kPer; ++k) {
       const uint32_t bg = __ballot_sync(0xffffffffu, key[k] > limit), be = __ballot_sync(0xffffffffu, key[k] == limit);
       const uint32_t e = eq + __popc(be & below);
-      if (key[k] > limit || (key[k] == limit && e < want)) kept[gt + __popc(bg & below) + min(e, want)] = u.lo + i0 + 32 * k;
+      if (key[k] > limit || (key[k] == limit && e < want)) kept[gt + __popc(bg & below) + min(e, want)] = row + 32 * k;
       gt += __popc(bg);
       eq += __popc(be);
     }
@@ -287,7 +369,7 @@ __global__ void __launch_bounds__(kSelThreads) select_long_kernel(SelectArgs a) 
 #pragma unroll 8
     for (int32_t i = c0 + tid; i < c1; i += kSelThreads) {
       const uint32_t k = order_key(w[i]);
-      if ((k & mask) == limit) atomicAdd(&sm.hist[((k >> shift) & 255u) * 32 + lane], 1u);
+      if ((k & mask) == limit) count_digit(sm, (k >> shift) & 255u);
     }
     choose_bin(sm, d, want, nranks);
     limit |= sm.pick[0] << shift;
@@ -362,13 +444,13 @@ struct CompactArgs {
   int32_t* status;
 };
 
-// Rows a window and windows a ring: about 108 KB a CTA, two CTAs an SM.
-template <int kRowBytes>
+// kWarps warps a CTA, each with a ring of kWindows windows of kRows rows (a lane each).
+template <int kRowBytes, int kWarps_, int kRows_, int kWindows_>
 struct Ring {
-  static constexpr int kRows = kRowBytes > 1024 ? 16 : 32;
-  static constexpr int kWindows = kRowBytes > 1024 ? 6 : 8;
-  static constexpr int kSlotBytes = kRows * kRowBytes;
-  static constexpr int kSmem = kWindows * kSlotBytes;
+  static constexpr int kBytes = kRowBytes, kWarps = kWarps_, kRows = kRows_, kWindows = kWindows_;
+  static constexpr int kSlotBytes = kRows * kRowBytes, kRingBytes = kWindows * kSlotBytes;
+  static constexpr int kSmem = kWarps * kRingBytes;
+  static_assert(kRows <= 32 && kWindows >= 4, "a lane a row; two windows in flight beside the two being stored");
 };
 
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
@@ -392,33 +474,37 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int kRowBytes>
-__global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
-  using R = Ring<kRowBytes>;
-  extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ uint64_t full[R::kWindows];
-  __shared__ float w_s[R::kWindows][R::kRows];
+template <class R>
+__global__ void __launch_bounds__(32 * R::kWarps) compact_kernel(CompactArgs a) {
+  constexpr int kRowBytes = R::kBytes;
+  extern __shared__ __align__(128) unsigned char rings[];
+  __shared__ uint64_t fulls[R::kWarps][R::kWindows];
+  __shared__ float w_all[R::kWarps][R::kWindows][R::kRows];
   __shared__ int abort_w;
   volatile int* abort_s = &abort_w;
-  const uint32_t rank = cluster_ctarank();
-  uint32_t nranks;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nranks));
+  uint32_t nranks = cluster_nctarank();
   const int64_t u = blockIdx.x / nranks;
-  const int rs = (int)(u / a.B), b = (int)(u % a.B), lane = threadIdx.x;
+  const int rs = (int)(u / a.B), b = (int)(u % a.B), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t M = a.new_lens[b];
   const int64_t m64 = M > 0 ? rows_below(a.shard_begin + rs, M, a.L) : 0;
   if (M < 0 || m64 > a.kept_stride) {  // uniform over the cluster
-    if (lane == 0 && rank == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
+    if (threadIdx.x == 0 && cluster_ctarank() == 0) flag(a.status, DCP_STATUS_BAD_LENGTH);
     return;
   }
   const int32_t m = (int32_t)m64;
   if (m == 0) return;
+  // a window of the unit is one of every warp of the cluster
+  const uint32_t rank = cluster_ctarank() * R::kWarps + warp;
+  nranks *= R::kWarps;
+  unsigned char* ring = rings + warp * R::kRingBytes;
+  uint64_t* full = fulls[warp];
+  float (*w_s)[R::kRows] = w_all[warp];
+  if (threadIdx.x == 0) *abort_s = 0;
   if (lane == 0) {
-    *abort_s = 0;
     for (int i = 0; i < R::kWindows; ++i) mbar_init(&full[i], 33);  // the byte count, and every lane's weight
     fence_barrier_init();
   }
-  __syncwarp();
+  __syncthreads();
   const int32_t* kept = a.kept + u * a.kept_stride;
   const int32_t* bt = a.bt + (int64_t)b * a.bt_stride;
   float* wts = a.weights ? a.weights + u * a.w_stride : nullptr;
@@ -494,6 +580,7 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
   bool ok = true;
   auto read_one = [&](int s, int32_t x) {
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(x / R::kWindows) & 1u, abort_s));
+    __syncwarp();
     if (nranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // after a lost wait too
   };
   read_one(0, 0);
@@ -527,8 +614,6 @@ __global__ void __launch_bounds__(32) compact_kernel(CompactArgs a) {
   }
 }
 
-SmemLimit g_compact_bf16, g_compact_q4;
-
 bool shards_ok(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, int32_t B) {
   return layout_ok(layout) && shard_begin >= 0 && shard_end <= layout->n_shards && shard_begin < shard_end && B >= 1;
 }
@@ -558,11 +643,23 @@ int32_t launch_clusters(Kernel kernel, int64_t units, unsigned c, int threads, s
   return launch_status();
 }
 
-template <int kRowBytes>
-int32_t compact(SmemLimit& limit, const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
-                const int32_t* kept, int64_t kept_stride, int32_t B, const int64_t* new_lens,
-                const int32_t* block_table, int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages,
-                float* weights, int64_t w_stride, int32_t* status, void* stream) {
+template <class R>
+int32_t launch_compact(int64_t units, unsigned c, void* stream, const CompactArgs& a) {
+  static SmemLimit limit;
+  if (!limit.ensure(reinterpret_cast<const void*>(&compact_kernel<R>), R::kSmem)) return DCP_ERR_CUDA;
+  return launch_clusters(compact_kernel<R>, units, c, 32 * R::kWarps, R::kSmem, stream, a);
+}
+
+// A bulk copy's operands are uniform ones: a warp issues its lanes' copies one after the other, some 75 ns each, so
+// eight warps an SM are wanted.  One warp a CTA, eight CTAs an SM, where the units are enough for that with up to 8 CTAs
+// each; else eight warps a CTA.  524288 rows kept, in us, 8 CTAs an SM / 8 warps a CTA: 128 units 195 / 204 (4-bit 236 /
+// 242), 64 units 292 / 205; 262144 rows of 16 units 539 / 184 (385 / 172).  Four warps an SM, in windows of twice the
+// rows: 203 (249); one warp an SM in windows of 32 rows: 305 (471).
+template <class Many, class Few>
+int32_t compact(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const int32_t* kept,
+                int64_t kept_stride, int32_t B, const int64_t* new_lens, const int32_t* block_table,
+                int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages, float* weights,
+                int64_t w_stride, int32_t* status, void* stream) {
   if (!shards_ok(layout, shard_begin, shard_end, B) || kept_stride < 0 || max_pages < 1 || bt_stride < max_pages ||
       pool_pages < 1 || (weights && w_stride < 1))
     return DCP_ERR_INVALID;
@@ -570,14 +667,13 @@ int32_t compact(SmemLimit& limit, const dcp_layout_t* layout, int32_t shard_begi
     return DCP_ERR_INVALID;
   if (kept_stride == 0) return DCP_OK;
   if (kept_stride > INT32_MAX - 1024) return DCP_ERR_UNSUPPORTED;  // kept entries are 32-bit rows
-  using R = Ring<kRowBytes>;
-  if (!limit.ensure(reinterpret_cast<const void*>(&compact_kernel<kRowBytes>), R::kSmem)) return DCP_ERR_CUDA;
   const CompactArgs a{to_layout(layout), shard_begin, shard_end - shard_begin, B, kept, kept_stride, new_lens,
                       block_table, bt_stride, max_pages, static_cast<unsigned char*>(arena), pool_pages, weights,
                       w_stride, status};
   const int64_t units = (int64_t)B * a.n_held;
-  return launch_clusters(compact_kernel<kRowBytes>, units, cluster_of(units, kept_stride, 2 * R::kRows, 304), 32, R::kSmem,
-                         stream, a);
+  if (units * 8 >= 1024)
+    return launch_compact<Many>(units, cluster_of(units, kept_stride, 2 * Many::kRows, 1216), stream, a);
+  return launch_compact<Few>(units, cluster_of(units, kept_stride, 2 * Few::kRows * Few::kWarps, 152), stream, a);
 }
 
 }  // namespace
@@ -606,7 +702,7 @@ extern "C" int32_t dcp_kv_compact(const dcp_layout_t* layout, int32_t shard_begi
                                   const int32_t* block_table, int64_t bt_stride, int64_t max_pages, void* arena,
                                   int64_t pool_pages, float* weights, int64_t w_stride, int32_t* status,
                                   void* stream) {
-  return compact<kDk * 2>(g_compact_bf16, layout, shard_begin, shard_end, kept, kept_stride, B, new_lens, block_table,
+  return compact<Ring<kDk * 2, 1, 4, 6>, Ring<kDk * 2, 8, 4, 6>>(layout, shard_begin, shard_end, kept, kept_stride, B, new_lens, block_table,
                           bt_stride, max_pages, arena, pool_pages, weights, w_stride, status, stream);
 }
 
@@ -615,6 +711,6 @@ extern "C" int32_t dcp_kv_compact_q4(const dcp_layout_t* layout, int32_t shard_b
                                      const int32_t* block_table, int64_t bt_stride, int64_t max_pages, void* arena,
                                      int64_t pool_pages, float* weights, int64_t w_stride, int32_t* status,
                                      void* stream) {
-  return compact<kQ4RowBytes>(g_compact_q4, layout, shard_begin, shard_end, kept, kept_stride, B, new_lens, block_table,
+  return compact<Ring<kQ4RowBytes, 1, 8, 8>, Ring<kQ4RowBytes, 8, 8, 8>>(layout, shard_begin, shard_end, kept, kept_stride, B, new_lens, block_table,
                               bt_stride, max_pages, arena, pool_pages, weights, w_stride, status, stream);
 }

@@ -7,8 +7,8 @@
 // and one rounding to bf16 at the end.
 //
 // Angles.  A position times a frequency in f32 is off by 0.03 rad at 10^6, and f64 is
-// slow on this card (2 operations a clock and SM).  So each lane turns its frequency
-// into a step of 2^-64 turns once, in f64, and a position's angle is one wrapping 64-bit
+// slow on this card (2 operations a clock and SM).  So a block turns the frequencies
+// into steps of 2^-64 turns once, in f64, and a position's angle is one wrapping 64-bit
 // product: the fraction of a turn to 2^-64 * position.  The step itself is off by
 // 1.5 * 2^-53 of its value, 2e-10 rad at 10^6 rad.
 //
@@ -57,11 +57,14 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return u;
 }
 
-// Norm weights (f32 or bf16) into shared memory, in f32.
-__device__ __forceinline__ void load_gamma(const void* gamma, int bf16, int dims, float* g) {
+// What a block's tokens share, in shared memory: norm weights (f32 or bf16) in f32, and the frequencies' steps (f64 runs
+// at 2 operations a clock and SM: once a block, not once a warp).
+__device__ __forceinline__ void load_shared(const void* gamma, int bf16, int dims, float* g, const float* inv_freq,
+                                            uint64_t* steps) {
   if (gamma)
     for (int i = threadIdx.x; i < dims; i += blockDim.x)
       g[i] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(gamma)[i]) : static_cast<const float*>(gamma)[i];
+  if (inv_freq && threadIdx.x < kRope / 2) steps[threadIdx.x] = turn_step(__ldg(inv_freq + threadIdx.x));
   __syncthreads();
 }
 
@@ -80,22 +83,18 @@ __device__ __forceinline__ float square8(const float (&v)[8], float sum) {
 
 // ---------------------------------------------------------------- queries
 constexpr int kQThreads = 256;
-#ifndef QMIN
-#define QMIN 4
-#define RAHEAD 2
-#define RMIN 4
-#endif
 
 // Warp task: token task / parts, its heads [part * per, part * per + per).  The next step's row is on its way while
 // this one's is worked on; sines lie in shared memory (an angle is computed once a warp, by lane `pair`).
 template <bool kHalves>
-__global__ void __launch_bounds__(kQThreads, QMIN) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
+__global__ void __launch_bounds__(kQThreads, 4) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
                                                                    const __nv_bfloat16* q, int64_t stride,
                                                                    const int64_t* __restrict__ pos, const void* gamma,
                                                                    int gamma_bf16, float eps,
                                                                    const float* __restrict__ inv_freq,
                                                                    __nv_bfloat16* out, int32_t* status) {
   __shared__ __align__(16) float gamma_s[kQDims];
+  __shared__ uint64_t steps_s[kRope / 2];
   __shared__ __align__(16) float2 turn_s[kQThreads / 32][kRope / 2];
   const int64_t task = blockIdx.x * (int64_t)(kQThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = parts == 1 ? task : (int64_t)((uint64_t)task / (uint32_t)parts);
@@ -115,14 +114,15 @@ __global__ void __launch_bounds__(kQThreads, QMIN) q_norm_rope_kernel(int64_t T,
     p = __ldg(pos + t);
     load(h);
   }
-  if (inv_freq && t < T) {
-    const Turn turn = turn_of(turn_step(__ldg(inv_freq + lane)), p);
-    turn_s[threadIdx.x >> 5][lane] = make_float2(turn.s, turn.c);
-  }
-  load_gamma(gamma, gamma_bf16, kQDims, gamma_s);
+  load_shared(gamma, gamma_bf16, kQDims, gamma_s, inv_freq, steps_s);
   if (p < 0) {
     if (t < T && p != -1 && lane == 0) flag(status, DCP_STATUS_BAD_POSITION);
     return;
+  }
+  if (inv_freq) {
+    const Turn turn = turn_of(steps_s[lane], p);
+    turn_s[threadIdx.x >> 5][lane] = make_float2(turn.s, turn.c);
+    __syncwarp();
   }
   // pairs (2 i, 2 i + 1) lie in one lane, halves (i, i + 32) in lanes l and l ^ 4
   const float4* turns = reinterpret_cast<const float4*>(turn_s[threadIdx.x >> 5] + (kHalves ? 8 * (l & 3) : 4 * l));
@@ -188,19 +188,22 @@ struct RowArgs {
   const int64_t* rope_pos;
 };
 
-constexpr int kRowAhead = RAHEAD;  // tokens whose loads are in flight before their stores
+// Tokens whose loads are in flight before their stores: 32768 tokens take 14.9 us with 2 and four blocks an SM, 16.1 with
+// 4 and two blocks, 18.4 with 3 and three; 16.0 with 1 and five.
+constexpr int kRowAhead = 2;
 
 template <bool kQ4>
-__global__ void __launch_bounds__(256, RMIN) norm_rope_store_kernel(Layout L, int32_t shard_begin, int32_t shard_end,
+__global__ void __launch_bounds__(256, 4) norm_rope_store_kernel(Layout L, int32_t shard_begin, int32_t shard_end,
                                                               RowArgs in, const int64_t* __restrict__ pos,
                                                               const int32_t* __restrict__ req, int64_t T, int per_warp,
                                                               Table tab, unsigned char* __restrict__ arena,
                                                               int32_t* status) {
   __shared__ __align__(16) float gamma_s[kDv];
+  __shared__ uint64_t steps_s[kRope / 2];
   const int64_t t0 = (blockIdx.x * (int64_t)(blockDim.x / 32) + (threadIdx.x >> 5)) * per_warp;
   const int lane = threadIdx.x & 31;
   const int n = (int)min((int64_t)per_warp, T - t0);
-  load_gamma(in.gamma, in.gamma_bf16, kDv, gamma_s);
+  load_shared(in.gamma, in.gamma_bf16, kDv, gamma_s, in.inv_freq, steps_s);
   if (n <= 0) return;
   Spot spot{-1, -1, 0};
   int64_t angle_pos = 0, to = -1;  // lane: of token t0 + lane
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(256, RMIN) norm_rope_store_kernel(Layout L, in
     angle_pos = in.rope_pos ? __ldg(in.rope_pos + t0 + lane) : p;
     spot = find_spot(p, __ldg(req + t0 + lane), L, tab, shard_begin, shard_end, status);
   }
-  const uint64_t step = in.inv_freq ? turn_step(__ldg(in.inv_freq + lane)) : 0;  // lane: pair `lane`
+  const uint64_t step = in.inv_freq ? steps_s[lane] : 0;  // lane: pair `lane`
   for (int i = 0; i < n; i += kRowAhead) {
     uint4 x[kRowAhead][2];
     uint32_t rope[kRowAhead];  // this lane's pair: dims 2 l, 2 l + 1 or l, l + 32

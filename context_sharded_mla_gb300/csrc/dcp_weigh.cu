@@ -43,13 +43,16 @@ constexpr int kMaxRaw = 3;
 // a last place of the sum so far, a relative loss between 0 and 36 * 2^-24 that averages 16 * 2^-25 over the scores that
 // carry the weights (measured: weights 1.5e-6 low without this, 1e-7 off with it).
 constexpr double kTruncation = 0x1p-21;
-constexpr int kASlots = 8;                 // 32-column operand slots in TMEM (4-bit cache)
+// 4-bit: operand slots of 128 dims (64 columns) in TMEM.  A slot of 64 dims costs its wait, its commit and its
+// products' issue more than the products take at 128 rows.
+constexpr int kASlots = 4;
+constexpr int kAParts = 5;                 // slots a tile fills: 4 of codes, one of the 64 position dims
 constexpr int kACol = 256;
 constexpr uint32_t kAllCols = 512;
 
 // Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8 on dequantise, in sets of four
 #ifndef SETS
-#define SETS 3
+#define SETS 2
 #endif
 constexpr int kDequantSets = SETS;
 constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kDequantWarp = 8;
@@ -291,7 +294,7 @@ __device__ __forceinline__ int32_t pool_row(const WeighArgs& a, int32_t rs, int3
 
 // One 64-dim chunk of a 4-bit row as it lies in shared memory: 8 words of codes and 4 scales, or 32 bf16 pairs.
 __device__ __forceinline__ void load_chunk(uint32_t row_s, int c, uint32_t (&w)[9]) {
-  if (c == kChunks - 1) return;
+  if (c >= kChunks - 1) return;
   const uint4 lo = ld_shared_v4(row_s + 32 * c), hi = ld_shared_v4(row_s + 32 * c + 16);
   w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
   w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
@@ -432,7 +435,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     // A lane a copy; the next tile's page ids are on their way while this one's copies go out.
     if (lane == 0) prefetch_tmap(&tmap_kv);
     int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
-    const int32_t box = 4 * lane / a.box_rows, in_box = 4 * lane - box * a.box_rows;  // this lane's four rows of a tile
     uint32_t st = 0, ph = 0;
     bool ok = true, more = true;
     uint32_t tiles = 0;
@@ -447,10 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull + st], __popc(who) * a.box_rows * kQ4RowBytes);
         __syncwarp();
-        const int32_t yl = __shfl_sync(0xffffffffu, y, box);
-        if (yl >= 0)
-          bulk_load(smem + sl.ring + st * kRawTile + 4 * lane * kQ4RowBytes, a.arena + (int64_t)(yl + in_box) * kQ4RowBytes,
-                    4 * kQ4RowBytes, &bars[kRFull + st]);
+        if (y >= 0)
+          bulk_load(smem + sl.ring + st * kRawTile + lane * a.box_rows * kQ4RowBytes, a.arena + (int64_t)y * kQ4RowBytes,
+                    a.box_rows * kQ4RowBytes, &bars[kRFull + st]);
         if (++st == (uint32_t)a.stages) {
           st = 0;
           ph ^= 1;
@@ -516,13 +517,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       const bool first = w.first(), last = w.last();
       const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
       ok = warp_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s, lane);
-      for (int c = 0; c < kChunks && ok; ++c) {
-        if (first) ok = warp_wait(&bars[kQFull + c], qph, abort_s, lane);
+      for (int c = 0; c < (kQ4 ? kAParts : kChunks) && ok; ++c) {
+        const int q0 = kQ4 ? 2 * c : c, nq = kQ4 && c < kAParts - 1 ? 2 : 1;  // query chunks of this step
+        if (first)
+          for (int i = 0; i < nq; ++i) ok = ok && warp_wait(&bars[kQFull + q0 + i], qph, abort_s, lane);
         ok = ok && warp_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s, lane);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t qd = qdesc + c * (q_chunk >> 4), kd = kdesc + st * (kStageBytes >> 4);
-        const uint32_t kt = tmem + kACol + 32 * st;
+        const uint64_t qd = qdesc + q0 * (q_chunk >> 4), kd = kdesc + st * (kStageBytes >> 4);
+        const uint32_t kt = tmem + kACol + 64 * st;
         if (one) {
 #pragma unroll
           for (int k = 0; k < kChunkDims / 16; ++k) {
@@ -531,9 +534,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
             else
               mma_pair_ss(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
           }
+          if (kQ4 && nq == 2) {
+#pragma unroll
+            for (int k = 0; k < kChunkDims / 16; ++k) mma_pair_ts(d, kt + 32 + 8 * k, qd + (q_chunk >> 4) + 2 * k, idesc, 1);
+          }
           commit_pair(&bars[(kQ4 ? kAEmpty : kEmpty) + st]);
-          if (last) commit_pair(&bars[kQEmpty + c]);
-          if (c == kChunks - 1) commit_pair(&bars[kSFull + buf]);
+          if (last)
+            for (int i = 0; i < nq; ++i) commit_pair(&bars[kQEmpty + q0 + i]);
+          if (q0 == kChunks - 1) commit_pair(&bars[kSFull + buf]);
         }
         __syncwarp();
         if (++st == slots) {
@@ -639,7 +647,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     }
   } else if (kQ4 && warp >= kDequantWarp && any) {
     // ------------------------------------------------------------------ 4-bit rows -> operands in TMEM
-    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of chunks s, s + kDequantSets, ..  Every pair-tile of the run is met
+    // Warp 8 + 4 s + k: keys [32 k, 32 k + 32) of every kDequantSets-th slot.  Every pair-tile of the run is met
     // once a row group; a CTA without a tile in the last of a request turns over what its slot holds, for nobody.
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
@@ -649,16 +657,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     for (uint32_t j = 0; j < tiles && ok; ++j) {
       ok = warp_wait(&bars[kRFull + rb], rph, abort_s, lane);
       const uint32_t row_s = smem_u32(smem) + sl.ring + rb * kRawTile + (quarter * 32 + lane) * kQ4RowBytes;
-#pragma unroll 1
-      for (int c = set; c < kChunks && ok; c += kDequantSets) {
-        const uint32_t n = j * kChunks + c, slot = n % kASlots;
-        uint32_t raw[9], v[32];
-        load_chunk(row_s, c, raw);
+      for (int part = 0; part < kAParts && ok; ++part) {
+        const uint32_t n = j * kAParts + part, slot = n % kASlots;
+        if (n % kDequantSets != (uint32_t)set) continue;
+        uint32_t raw[9];
+        load_chunk(row_s, 2 * part, raw);
         ok = warp_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s, lane);
         if (!ok) break;
-        dequant_chunk(row_s, c, raw, v);
         tc_fence_after();
-        tmem_st32(lane_addr + 32 * slot, v);
+#pragma unroll 1
+        for (int h = 0; h < (part < kAParts - 1 ? 2 : 1); ++h) {
+          uint32_t v[32];
+          dequant_chunk(row_s, 2 * part + h, raw, v);
+          if (h == 0) load_chunk(row_s, 2 * part + 1, raw);
+          tmem_st32(lane_addr + 64 * slot + 32 * h, v);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -672,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       }
     }
     // the operand slots' last releases land before the CTA may leave
-    const uint32_t n = tiles * kChunks;
+    const uint32_t n = tiles * kAParts;
     for (uint32_t s = 0; s < kASlots && s < n && ok; ++s) {
       const uint32_t uses = (n - 1 - s) / kASlots;
       ok = warp_wait(&bars[kAEmpty + s], uses & 1, abort_s, lane);
