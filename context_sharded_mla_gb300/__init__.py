@@ -618,12 +618,14 @@ def dcp_block_tables(layout, seq_lens, new_lens, block_table, max_pages, free_pa
     _check("dcp_block_tables", rc)
 
 
-def _strided(t, name, width, dev):
-    """(address, row stride in elements) of a bf16 view [..., width] on the current device with equally strided rows."""
-    stride = _rows(t, name, width)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
-    return t.data_ptr(), stride
+def _strided(t, name, shape, dev):
+    """(address, row stride in elements) of a bf16 view of this shape on the current device with equally strided rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape:
+        return t.data_ptr(), shape[-1] if t.is_contiguous() else _rows(t, name, shape[-1])
+    _rows(t, name, shape[-1])
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
 
 
 def _gamma(gamma, width, dev):
@@ -642,9 +644,7 @@ def dcp_q_norm_rope(q, pos, out, gamma=None, eps=1e-6, inv_freq=None, rope_style
     if not isinstance(out, torch.Tensor) or out.dim() != 3:
         raise ValueError("out must be [T, H, 192]")
     T, H, _ = out.shape
-    at_q, stride = _strided(q, "q", 192, dev)
-    if q.shape != out.shape:
-        raise ValueError(f"q must have out's shape {tuple(out.shape)}, got {tuple(q.shape)}")
+    at_q, stride = _strided(q, "q", (T, H, 192), dev)
     at_gamma, code = _gamma(gamma, 192, dev)
     rc = load_library().dcp_q_norm_rope(
         T, H, at_q, stride, _at(pos, "pos", torch.int64, (T,), dev), at_gamma, code, eps,
@@ -659,9 +659,7 @@ def _norm_rope_append(name, width, dtype, layout, shard_begin, shard_end, kv, po
     dev = torch.cuda.current_device()
     T = pos.numel()
     B, stride = _table(block_table, "block_table")
-    at_kv, kv_stride = _strided(kv, "kv", 576, dev)
-    if kv.shape != (T, 576):
-        raise ValueError(f"kv must have shape {(T, 576)}, got {tuple(kv.shape)}")
+    at_kv, kv_stride = _strided(kv, "kv", (T, 576), dev)
     at_gamma, code = _gamma(gamma, 512, dev)
     rc = getattr(load_library(), name)(
         layout, shard_begin, shard_end, at_kv, kv_stride, at_gamma, code, eps,

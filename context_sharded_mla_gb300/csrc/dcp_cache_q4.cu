@@ -25,11 +25,82 @@
 // dims go through as 4 bytes a lane.  Memory-bound for long lists: 1152 + 416 bytes a
 // token either way; 262143 rows in 72 us written (5.7 TB/s) and 76 us read (5.4 TB/s).
 // A list of a few rows is two or three memory latencies, 2.7 us in a captured graph.
-#include "dcp_rows.cuh"
+#include "dcp_norm_rope.cuh"
 
 using namespace dcp;
 
 namespace {
+
+// Largest magnitude of 8 bf16 values; a NaN among them gives NaN.
+__device__ __forceinline__ __nv_bfloat16 top8(const uint4& x) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+  const __nv_bfloat162 a = __hmax2_nan(__habs2(h[0]), __habs2(h[1])), b = __hmax2_nan(__habs2(h[2]), __habs2(h[3]));
+  const __nv_bfloat162 c = __hmax2_nan(a, b);
+  return __hmax_nan(c.x, c.y);
+}
+
+// A / 7 to 12 significant bits (an infinity stays one; a NaN's bits could wrap).
+__device__ __forceinline__ float seventh(float top) {
+  const float q = __uint_as_float((__float_as_uint(top * (1.f / 7.f)) + 0x800u) & 0xFFFFF000u);
+  return top != top ? top : q;
+}
+
+__device__ __forceinline__ float reciprocal(float s) {  // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Quotients from here on are clamped before they are rounded.  x / s is at most 7.46875 or
+// at least 7.5 (8 significant bits over 4), so the limit is one between the two that a
+// reciprocal one ulp off cannot cross.  (7.5 itself is crossed: it would become code 8, in
+// the next dim's bits.)
+constexpr float kClampFrom = 7.499f;
+
+// The word of codes of 8 bf16 values under scale s, whose group's largest magnitude is
+// `top`.  A sum with kSnap ends at a multiple of 2^-11, one with kInt at a whole number
+// that its low mantissa bits hold as code + 8.
+__device__ __forceinline__ uint32_t codes8(const uint4& x, float s, float top) {
+  constexpr float kSnap = 1.5f * 4096.f, kInt = 1.5f * 8388608.f + 8.f;
+  if (!(s > 0.f)) return 0x88888888u;  // scale 0 or NaN: every code 0
+  const float inv = reciprocal(s);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+  // only a scale that was clamped, or is one of the few smallest, leaves |x / s| above 7.5
+  const bool clamp = !(top * inv < kClampFrom);
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 f = __bfloat1622float2(h[k]);
+    if (clamp) {
+      f.x = fminf(fmaxf(f.x, -7.f * s), 7.f * s);
+      f.y = fminf(fmaxf(f.y, -7.f * s), 7.f * s);
+    }
+    const uint32_t a = __float_as_uint(__fadd_rn(__fmaf_rn(f.x, inv, kSnap), kInt - kSnap));
+    const uint32_t b = __float_as_uint(__fadd_rn(__fmaf_rn(f.y, inv, kSnap), kInt - kSnap));
+    w |= __byte_perm(a, b, 0x5410) << (4 * k);
+  }
+  return w;
+}
+
+// A 4-bit row's first 512 dims, from the normed bf16 ones (dcp_norm_rope.cuh): lane l has a
+// word of codes of each half, its groups are its own 8 dims and its neighbour's.
+struct Q4Row {
+  static constexpr int kBytes = kQ4RowBytes, kRopeAt = kQ4RopeOff;
+  uint32_t w0, w1, scales;
+  __device__ explicit Q4Row(const uint4 (&x)[2]) {
+    const __nv_bfloat162 mine = __nv_bfloat162(top8(x[0]), top8(x[1]));
+    const float2 top = __bfloat1622float2(__hmax2_nan(mine, __shfl_xor_sync(0xffffffffu, mine, 1)));
+    scales = __nv_cvt_float2_to_fp8x2(make_float2(seventh(top.x), seventh(top.y)), __NV_SATFINITE, __NV_E4M3);
+    const float2 s = q4_scales_f32(scales);
+    w0 = codes8(x[0], s.x, top.x);
+    w1 = codes8(x[1], s.y, top.y);
+  }
+  __device__ void store(unsigned char* row, int lane) const {
+    reinterpret_cast<uint32_t*>(row)[lane] = w0;
+    reinterpret_cast<uint32_t*>(row)[32 + lane] = w1;
+    row[kQ4ScaleOff + 16 * (lane & 1) + (lane >> 1)] = (unsigned char)(lane & 1 ? scales >> 8 : scales);
+  }
+};
 
 // The source row of a moved token, or -1: row t of kv_new, or the prefill pool's
 // row of its position.
@@ -218,4 +289,16 @@ extern "C" int32_t dcp_kv_read_q4(const dcp_layout_t* layout, int32_t shard_begi
       to_layout(layout), shard_begin, shard_end, static_cast<const unsigned char*>(arena), pos, req, T, per_warp,
       Table{block_table, B, bt_stride, max_pages, pool_pages}, static_cast<unsigned char*>(kv), status);
   return launch_status();
+}
+
+extern "C" int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
+                                              const void* kv, int64_t kv_stride, const void* gamma,
+                                              int32_t gamma_dtype, float eps, const float* inv_freq,
+                                              int32_t rope_style, const int64_t* rope_pos, const int64_t* pos,
+                                              const int32_t* req, int64_t T, const int32_t* block_table, int32_t B,
+                                              int64_t bt_stride, int64_t max_pages, void* arena, int64_t pool_pages,
+                                              int32_t* status, void* stream) {
+  return norm_rope_append<Q4Row>(layout, shard_begin, shard_end, kv, kv_stride, gamma, gamma_dtype, eps, inv_freq,
+                                rope_style, rope_pos, pos, req, T, block_table, B, bt_stride, max_pages, arena,
+                                pool_pages, status, stream);
 }

@@ -1,6 +1,5 @@
 // dcp_rows.cuh — what the kernels that write or read cache rows share: where a token
-// goes, the 4-bit codes of its values (row format and quantiser: dcp_internal.cuh and
-// dcp_cache_q4.cu), and how a token list is spread over warps.
+// goes, and how a token list is spread over warps.
 #pragma once
 
 #include "dcp_internal.cuh"
@@ -64,57 +63,6 @@ __device__ __forceinline__ int64_t row_of(const Spot& s, const Layout& L, const 
     return -1;
   }
   return s.pool + s.page * L.P + s.in_page;
-}
-
-// Largest magnitude of 8 bf16 values; a NaN among them gives NaN.
-__device__ __forceinline__ __nv_bfloat16 top8(const uint4& x) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
-  const __nv_bfloat162 a = __hmax2_nan(__habs2(h[0]), __habs2(h[1])), b = __hmax2_nan(__habs2(h[2]), __habs2(h[3]));
-  const __nv_bfloat162 c = __hmax2_nan(a, b);
-  return __hmax_nan(c.x, c.y);
-}
-
-// A / 7 to 12 significant bits (an infinity stays one; a NaN's bits could wrap).
-__device__ __forceinline__ float seventh(float top) {
-  const float q = __uint_as_float((__float_as_uint(top * (1.f / 7.f)) + 0x800u) & 0xFFFFF000u);
-  return top != top ? top : q;
-}
-
-__device__ __forceinline__ float reciprocal(float s) {  // within 1 ulp
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return r;
-}
-
-// Quotients from here on are clamped before they are rounded.  x / s is at most 7.46875 or
-// at least 7.5 (8 significant bits over 4), so the limit is one between the two that a
-// reciprocal one ulp off cannot cross.  (7.5 itself is crossed: it would become code 8, in
-// the next dim's bits.)
-constexpr float kClampFrom = 7.499f;
-
-// The word of codes of 8 bf16 values under scale s, whose group's largest magnitude is
-// `top`.  A sum with kSnap ends at a multiple of 2^-11, one with kInt at a whole number
-// that its low mantissa bits hold as code + 8.
-__device__ __forceinline__ uint32_t codes8(const uint4& x, float s, float top) {
-  constexpr float kSnap = 1.5f * 4096.f, kInt = 1.5f * 8388608.f + 8.f;
-  if (!(s > 0.f)) return 0x88888888u;  // scale 0 or NaN: every code 0
-  const float inv = reciprocal(s);
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
-  // only a scale that was clamped, or is one of the few smallest, leaves |x / s| above 7.5
-  const bool clamp = !(top * inv < kClampFrom);
-  uint32_t w = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float2 f = __bfloat1622float2(h[k]);
-    if (clamp) {
-      f.x = fminf(fmaxf(f.x, -7.f * s), 7.f * s);
-      f.y = fminf(fmaxf(f.y, -7.f * s), 7.f * s);
-    }
-    const uint32_t a = __float_as_uint(__fadd_rn(__fmaf_rn(f.x, inv, kSnap), kInt - kSnap));
-    const uint32_t b = __float_as_uint(__fadd_rn(__fmaf_rn(f.y, inv, kSnap), kInt - kSnap));
-    w |= __byte_perm(a, b, 0x5410) << (4 * k);
-  }
-  return w;
 }
 
 constexpr int kThreads = 256;  // 8 warps

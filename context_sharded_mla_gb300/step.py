@@ -19,26 +19,35 @@ the same calls, on the quantising append and the 4-bit partial.
 pages on the device and moves them from step to step in one call, which also
 lists the new tokens' positions and slots.  Ranks that are given the same lengths
 build the same tables, so a group of them exchanges none.
+
+With ``evict=True`` a decoder also accumulates the attention weight of its cached rows
+(``weigh``, after a decode) and drops the light ones (``evict``, before the tables
+shrink); ``append_normed`` takes latent rows as the projection leaves them.
 """
 
 from __future__ import annotations
 
 import torch
 
-from . import (DCP_LSE_BASE_2, DCP_LSE_BASE_E, Q4_ROW_BYTES, Layout, dcp_block_tables, dcp_kv_append,
-               dcp_kv_append_q4, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
-               dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4)
+from . import (DCP_LSE_BASE_2, DCP_LSE_BASE_E, DCP_ROPE_PAIRS, Q4_ROW_BYTES, Layout, dcp_block_tables, dcp_evict_select,
+               dcp_kv_append, dcp_kv_append_q4, dcp_kv_compact, dcp_kv_compact_q4, dcp_kv_norm_rope_append,
+               dcp_kv_norm_rope_append_q4, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
+               dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4, dcp_mla_key_weights,
+               dcp_mla_key_weights_q4)
 
 _CACHES = {"bf16": (576, torch.bfloat16, dcp_kv_append, dcp_mla_decode_partial, dcp_mla_decode_workspace_size),
            "q4": (Q4_ROW_BYTES, torch.uint8, dcp_kv_append_q4, dcp_mla_decode_partial_q4,
                   dcp_mla_decode_workspace_size_q4)}
+_NORMED = {"bf16": dcp_kv_norm_rope_append, "q4": dcp_kv_norm_rope_append_q4}
+_WEIGH = {"bf16": dcp_mla_key_weights, "q4": dcp_mla_key_weights_q4}
+_COMPACT = {"bf16": dcp_kv_compact, "q4": dcp_kv_compact_q4}
 
 
 class ShardedMlaDecoder:
     def __init__(self, layout: Layout, B: int, q_len: int, H: int, pool_pages: int, max_pages: int,
                  scale: float, lse_base: int = DCP_LSE_BASE_E, out_dtype=torch.bfloat16,
                  part_dtype=torch.float32, shard_begin: int = 0, shard_end: int | None = None,
-                 device="cuda", cache: str = "bf16"):
+                 device="cuda", cache: str = "bf16", evict: bool = False):
         if cache not in _CACHES:
             raise ValueError(f"unknown cache format {cache!r} (bf16 or q4)")
         width, dtype, self._append, self._partial, workspace_size = _CACHES[cache]
@@ -60,6 +69,12 @@ class ShardedMlaDecoder:
         ws = workspace_size(layout, self.shard_begin, self.shard_end, B, q_len, H)
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        if evict:
+            rows = max_pages * layout.page_size
+            self.weights = torch.zeros(n, B, rows, dtype=torch.float32, device=dev)
+            self.kept = torch.full((n, B, rows), -1, dtype=torch.int32, device=dev)
+            # requests' positions below it have a weight (set an entry to 0 when its slot gets another request)
+            self.weighed = torch.zeros(B, dtype=torch.int64, device=dev)
 
     def append(self, kv_new, pos, req, block_table, stream=None):
         """Place T new latent rows (kv_new [T, 576] bf16 at positions pos of requests req):
@@ -68,6 +83,38 @@ class ShardedMlaDecoder:
             return
         self._append(self.layout, self.shard_begin, self.shard_end, kv_new, pos, req, block_table,
                      self.max_pages, self.arena, self.pool_pages, self.status, stream)
+
+    def append_normed(self, kv, pos, req, block_table, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS,
+                      rope_pos=None, stream=None):
+        """append of rows kv [T, 576] that are still a projection's output: latent dims RMS-normed, position dims
+        rotated by rope_pos (None: pos; they differ once a request has been shortened)."""
+        if kv.shape[0] == 0:
+            return
+        _NORMED[self.cache](self.layout, self.shard_begin, self.shard_end, kv, pos, req, block_table, self.max_pages,
+                            self.arena, self.pool_pages, self.status, gamma=gamma, eps=eps, inv_freq=inv_freq,
+                            rope_style=rope_style, rope_pos=rope_pos, stream=stream)
+
+    def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None):
+        """After a decode of q: what weight every cached row got from it is added to decay times what it had."""
+        _WEIGH[self.cache](self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
+                           self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
+                           old_lens=self.weighed, decay=decay, stream=stream)
+        with torch.cuda.stream(stream):
+            self.weighed.copy_(seq_lens)
+        return self.weights
+
+    def evict(self, block_table, seq_lens, new_lens, sinks=0, recent=0, stream=None):
+        """Every shard keeps its share of new_lens positions of each request: the first `sinks`, the last `recent` and
+        the heaviest, moved to the front.  The tables, which still hold the old lengths, shrink afterwards
+        (BlockTables.update(new_lens)).  Returns kept: the rows that stayed."""
+        dcp_evict_select(self.layout, self.shard_begin, self.shard_end, seq_lens, new_lens, sinks, recent, self.weights,
+                         self.kept, self.status, stream)
+        _COMPACT[self.cache](self.layout, self.shard_begin, self.shard_end, self.kept, new_lens, block_table,
+                             self.max_pages, self.arena, self.pool_pages, self.status, weights=self.weights,
+                             stream=stream)
+        with torch.cuda.stream(stream):
+            torch.minimum(self.weighed, new_lens, out=self.weighed)
+        return self.kept
 
     def partial(self, q, block_table, seq_lens, stream=None):
         self._partial(self.layout, self.shard_begin, self.shard_end, q, self.arena,

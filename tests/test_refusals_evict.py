@@ -91,7 +91,30 @@ def test_compact(lib, kw, rc):
         assert call(fn, base, **kw) == rc
 
 
-def test_the_binding_wants_cuda_tensors_of_the_right_shape(lib):
-    q = torch.zeros(2, 3, 192, dtype=torch.bfloat16)
-    with pytest.raises((ValueError, RuntimeError, AssertionError)):
-        dcp.dcp_q_norm_rope(q, torch.zeros(2, dtype=torch.int64), q)
+def test_tensors_that_cannot_be_used(lib, monkeypatch):
+    """The Python entry points name the argument."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    z = lambda *s, d=torch.int64: torch.zeros(*s, dtype=d)   # noqa: E731
+    i32, u8, bf, f32 = torch.int32, torch.uint8, torch.bfloat16, torch.float32
+    arena, bt, st = z(4, 16, 576, d=bf), z(1, 1, d=i32), z(1, d=i32)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        dcp.dcp_q_norm_rope(z(2, 3, 192, d=bf), z(2), z(2, 3, 192, d=bf))
+    with pytest.raises(ValueError, match="out must be"):
+        dcp.dcp_q_norm_rope(z(2, 3, 192, d=bf), z(2), z(2, 576, d=bf))
+    with pytest.raises(ValueError, match="kv must be a CUDA tensor"):
+        dcp.dcp_kv_norm_rope_append(GOOD, 0, 4, z(2, 576, d=bf), z(2), z(2, d=i32), bt, 1, arena, 1, st)
+    with pytest.raises(ValueError, match="block_table must be"):
+        dcp.dcp_kv_norm_rope_append_q4(GOOD, 0, 4, z(2, 576, d=bf), z(2), z(2, d=i32), z(1, d=i32), 1, arena, 1, st)
+    lse, w = z(1, 1, 16, d=f32), z(4, 1, 16, d=f32)
+    with pytest.raises(ValueError, match="q must be"):
+        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w, st)
+    with pytest.raises(ValueError, match="one row per request"):
+        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(2, 1, 16, 576, d=bf), arena, 1, bt, 1, z(2), 0.1, 0, lse, w, st)
+    with pytest.raises(ValueError, match="weights must be"):
+        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w[:3], st)
+    with pytest.raises(ValueError, match="seq_lens must be a CUDA tensor"):
+        dcp.dcp_evict_select(GOOD, 0, 4, z(1), z(1), 0, 0, w, z(4, 1, 4, d=i32), st)
+    with pytest.raises(ValueError, match="kept must be"):
+        dcp.dcp_kv_compact(GOOD, 0, 4, z(4, 2, 4, d=i32), z(1), bt, 1, arena, 1, st)
+    with pytest.raises(ValueError, match="kept must be a CUDA tensor"):
+        dcp.dcp_kv_compact_q4(GOOD, 0, 4, z(4, 1, 4, d=i32), z(1), bt, 1, z(4, 16, 416, d=u8), 1, st)
