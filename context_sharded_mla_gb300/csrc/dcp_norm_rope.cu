@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kQThreads, 4) q_norm_rope_kernel(int64_t T, in
 extern "C" int32_t dcp_q_norm_rope(int64_t T, int32_t H, const void* q, int64_t q_stride, const int64_t* pos,
                                    const void* gamma, int32_t gamma_dtype, float eps, const float* inv_freq,
                                    int32_t rope_style, void* out, int32_t* status, void* stream) {
-  if (T < 0 || H < 1 || q_stride < kQDims || q_stride % 8 || !norm_args_ok(gamma, gamma_dtype, eps, rope_style))
+  if (T < 0 || H < 1 || H > 65535 || q_stride < kQDims || q_stride % 8 || !norm_args_ok(gamma, gamma_dtype, eps, rope_style))
     return DCP_ERR_INVALID;
   if (T == 0) return DCP_OK;
   if (!q || !pos || !out || misaligned(q, out)) return DCP_ERR_INVALID;

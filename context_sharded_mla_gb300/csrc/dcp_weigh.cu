@@ -130,6 +130,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
+// warp_wait for waits that are long as a rule: the warp sleeps in the barrier, up to kSuspendNs at a time, instead of
+// asking again and again (the other warps want the issue slots).  Bounded as mbar_wait is.
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, volatile int* abort_s) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kSuspendNs))) return true;
+    if (__any_sync(0xffffffffu, *abort_s)) return false;
+    if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
+      *abort_s = 1;
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- barriers and shared memory
 enum : int {
   kFull = 0,                            // key chunk in both CTAs (bf16; counted at the leader)
@@ -292,28 +307,25 @@ __device__ __forceinline__ int32_t pool_row(const WeighArgs& a, int32_t rs, int3
   return (int32_t)(rs * a.pool_rows + page * a.L.P + rho % (int32_t)a.L.P);
 }
 
-// One 64-dim chunk of a 4-bit row as it lies in shared memory: 8 words of codes and 4 scales, or 32 bf16 pairs.
-__device__ __forceinline__ void load_chunk(uint32_t row_s, int c, uint32_t (&w)[9]) {
-  if (c >= kChunks - 1) return;
-  const uint4 lo = ld_shared_v4(row_s + 32 * c), hi = ld_shared_v4(row_s + 32 * c + 16);
-  w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-  w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
-  w[8] = ld_shared_u32(row_s + kQ4ScaleOff + 4 * c);
-}
-// Its 32 bf16 pairs.
-__device__ __forceinline__ void dequant_chunk(uint32_t row_s, int c, const uint32_t (&w)[9], uint32_t (&v)[32]) {
-  if (c == kChunks - 1) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint4 x = ld_shared_v4(row_s + kQ4RopeOff + 16 * k);
-      v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
-    }
-    return;
+// 4-bit rows lie 416 bytes apart: 16-byte loads of eight neighbouring lanes meet two to a bank.  Lanes 4 to 7 of each
+// eight take every other piece first, which they do not meet, and swap.
+struct Swap {
+  bool odd;
+  __device__ explicit Swap(int lane) : odd((lane & 4) != 0) {}
+  // 32 bytes at `at`, in order
+  __device__ __forceinline__ void load(uint32_t at, uint32_t* w) const {
+    const uint32_t d = odd ? 16u : 0u;
+    const uint4 x = ld_shared_v4(at + d), y = ld_shared_v4(at + 16 - d);
+    w[0] = odd ? y.x : x.x; w[1] = odd ? y.y : x.y; w[2] = odd ? y.z : x.z; w[3] = odd ? y.w : x.w;
+    w[4] = odd ? x.x : y.x; w[5] = odd ? x.y : y.y; w[6] = odd ? x.z : y.z; w[7] = odd ? x.w : y.w;
   }
+};
+// Four scales (64 dims) and 8 words of codes -> 32 bf16 pairs.
+__device__ __forceinline__ void dequant_chunk(const uint32_t (&w)[8], uint32_t four, uint32_t (&v)[32]) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t s2[2], off2[2];
-    q4_scales(half ? w[8] >> 16 : w[8] & 0xFFFFu, s2, off2);
+    q4_scales(half ? four >> 16 : four & 0xFFFFu, s2, off2);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t p[4];
@@ -445,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       page = page_of(a, w, rho);
       const uint32_t who = __ballot_sync(0xffffffffu, y >= 0);
       if (kQ4) {
-        ok = warp_wait(&bars[kRFree + st], ph ^ 1, abort_s, lane);
+        ok = sleep_wait(&bars[kRFree + st], ph ^ 1, abort_s);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull + st], __popc(who) * a.box_rows * kQ4RowBytes);
         __syncwarp();
@@ -458,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         }
       } else {
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = warp_wait(&bars[kEmpty + st], ph ^ 1, abort_s, lane);
+          ok = sleep_wait(&bars[kEmpty + st], ph ^ 1, abort_s);
           if (!ok) break;
           const uint32_t full = lead + 8 * (kFull + st);
           if (lane == 0) expect_tx_cluster(full, __popc(who) * a.box_rows * 128);
@@ -479,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       const uint32_t uses = kQ4 ? tiles : tiles * kChunks;
       for (uint32_t s = 0; s < (uint32_t)a.stages && s < uses; ++s) {
         const uint32_t n = (uses - 1 - s) / a.stages;  // its last use
-        if (!warp_wait(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s, lane)) break;
+        if (!sleep_wait(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s)) break;
       }
     }
   } else if (warp == kQueryWarp && any) {
@@ -491,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       if (w.first()) {
         const int32_t y = w.b * a.R + w.g * a.Rg + rank * (a.Rg / 2);
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = warp_wait(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+          ok = sleep_wait(&bars[kQEmpty + c], ph ^ 1, abort_s);
           if (ok && lane == 0) {
             expect_tx_cluster(lead + 8 * (kQFull + c), q_chunk);
             tma_load_2d_pair(smem_u32(smem) + sl.q + c * q_chunk, &tmap_q, lead + 8 * (kQFull + c), c * kChunkDims, y);
@@ -501,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       }
       more = w.next(a, rank);
     }
-    for (int c = 0; c < kChunks && ok; ++c) ok = warp_wait(&bars[kQEmpty + c], ph ^ 1, abort_s, lane);
+    for (int c = 0; c < kChunks && ok; ++c) ok = sleep_wait(&bars[kQEmpty + c], ph ^ 1, abort_s);
   } else if (warp == kMmaWarp && any && rank == 0) {
     // ------------------------------------------------------------------ products (the leader's alone)
     // The whole warp walks and waits, one lane issues: the operands' descriptors are then uniform values.  (With one
@@ -516,12 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     while (more && ok) {
       const bool first = w.first(), last = w.last();
       const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
-      ok = warp_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s, lane);
+      ok = sleep_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
       for (int c = 0; c < (kQ4 ? kAParts : kChunks) && ok; ++c) {
         const int q0 = kQ4 ? 2 * c : c, nq = kQ4 && c < kAParts - 1 ? 2 : 1;  // query chunks of this step
         if (first)
-          for (int i = 0; i < nq; ++i) ok = ok && warp_wait(&bars[kQFull + q0 + i], qph, abort_s, lane);
-        ok = ok && warp_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s, lane);
+          for (int i = 0; i < nq; ++i) ok = ok && sleep_wait(&bars[kQFull + q0 + i], qph, abort_s);
+        ok = ok && sleep_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
         if (!ok) break;
         tc_fence_after();
         const uint64_t qd = qdesc + q0 * (q_chunk >> 4), kd = kdesc + st * (kStageBytes >> 4);
@@ -556,53 +568,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     }
   } else if (warp < 4 && any) {
     // ------------------------------------------------------------------ sums: a thread a key
+    // What a tile wants from global memory (its key's page and old weight) is loaded while the tile before is summed.
     const float c = a.scale_log2;
     const uint64_t c2 = f2_pack(__float_as_uint(c), __float_as_uint(c));
+    struct Key {
+      float* wp;          // its weight, null: not written
+      float old;
+      int32_t page, col0; // first column of the group that sees it
+      int32_t ncols, i;   // columns of the group, pair-tile of the block
+      int64_t lse_at;     // the group's first row, -1: as before
+      bool add;           // to the groups' sum so far
+    };
+    const bool keeps = a.old_lens && a.decay != 0.f;
+    int32_t old_b = -1;
+    int64_t old_len = 0;
+    auto look = [&]() -> Key {
+      Key k;
+      k.ncols = min(a.Rg, a.R - w.g * a.Rg);
+      k.i = w.i;
+      k.lse_at = w.first() ? (int64_t)w.b * a.R + w.g * a.Rg : -1;
+      k.add = w.g > 0;
+      k.wp = nullptr;
+      k.old = 0.f;
+      k.page = k.col0 = 0;
+      if (keeps && w.b != old_b) {
+        old_b = w.b;
+        old_len = __ldg(a.old_lens + w.b);
+      }
+      const int32_t row = w.t * kKeys + warp * 32 + lane;
+      if (row < w.rows) {
+        const int32_t I = (int32_t)a.L.I, blk = I == 1 ? row : row / I;
+        const int64_t p = ((int64_t)blk * a.L.N + a.shard_begin + w.rs) * I + (row - blk * I);
+        const int64_t hidden = p - (w.sh.S - a.q_len);  // query tokens [0, hidden) come before this key
+        if (hidden > 0) {
+          const int64_t x = hidden * a.H - (int64_t)w.g * a.Rg;
+          k.col0 = (int32_t)(x < 0 ? 0 : (x > a.Rg ? a.Rg : x));
+        }
+        if (w.g == a.ngroups - 1) {
+          k.page = __ldg(a.bt + (int64_t)w.b * a.bt_stride + row / (int32_t)a.L.P);
+          k.wp = a.weights + ((int64_t)w.rs * a.B + w.b) * a.w_stride + row;
+          if (keeps && p < old_len) k.old = *k.wp;
+        }
+      }
+      return k;
+    };
     bool ok = true, more = true;
     uint32_t j = 0;
+    Key key = look();
     while (more && ok) {
-      const int32_t ncols = min(a.Rg, a.R - w.g * a.Rg);
-      if (w.first()) {
+      if (key.lse_at >= 0) {
         __syncwarp();  // the columns' lse of the group before have been used
-        for (int k = lane; k < ncols; k += 32) {
-          const float l = __ldg(a.lse + (int64_t)w.b * a.R + w.g * a.Rg + k);
+        for (int k = lane; k < key.ncols; k += 32) {
+          const float l = __ldg(a.lse + key.lse_at + k);
           // a row that saw nothing adds 2^-inf
           lse_s[k] = l == -INFINITY ? -INFINITY : -(a.base2 ? l : l * kLog2e);
         }
         __syncwarp();
       }
-      // this thread's key
-      const int32_t row = w.t * kKeys + warp * 32 + lane;
-      const bool done = w.g == a.ngroups - 1;
-      const bool live = row < w.rows;
-      int32_t page = 0, col0 = 0;
-      float old = 0.f;
-      float* wp = nullptr;
-      if (live) {
-        const int32_t I = (int32_t)a.L.I, k = row / I;
-        const int64_t p = ((int64_t)k * a.L.N + a.shard_begin + w.rs) * I + (row - k * I);
-        const int64_t hidden = p - (w.sh.S - a.q_len);  // query tokens [0, hidden) come before this key
-        if (hidden > 0) {
-          const int64_t x = hidden * a.H - (int64_t)w.g * a.Rg;
-          col0 = (int32_t)(x < 0 ? 0 : (x > a.Rg ? a.Rg : x));
-        }
-        if (done) {
-          page = __ldg(a.bt + (int64_t)w.b * a.bt_stride + row / (int32_t)a.L.P);
-          wp = a.weights + ((int64_t)w.rs * a.B + w.b) * a.w_stride + row;
-          if (a.old_lens && a.decay != 0.f && p < __ldg(a.old_lens + w.b)) old = a.decay * *wp;
-        }
-      }
+      const Key now = key;
+      more = w.next(a, rank);
+      if (more) key = look();
       const uint32_t buf = j & 1;
-      ok = warp_wait(&bars[kSFull + buf], (j >> 1) & 1, abort_s, lane);
+      ok = sleep_wait(&bars[kSFull + buf], (j >> 1) & 1, abort_s);
       if (!ok) break;
       tc_fence_after();
       const uint32_t s_addr = tmem + ((uint32_t)(warp * 32) << 16) + (kQ4 ? 128 : 256) * buf;
-      const bool masked = __any_sync(0xffffffffu, col0 > 0);
+      const bool masked = __any_sync(0xffffffffu, now.col0 > 0);
       uint64_t sum[2] = {0, 0};
-      for (int k0 = 0; k0 < ncols; k0 += 32) {
+      for (int k0 = 0; k0 < now.ncols; k0 += 32) {
         uint32_t r[32];
         tmem_ld32_sync(s_addr + k0, r);
-        if (!masked && k0 + 32 <= ncols) {
+        if (!masked && k0 + 32 <= now.ncols) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float4 l = *reinterpret_cast<const float4*>(lse_s + k0 + 4 * k);
@@ -623,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int col = k0 + k + h;
-              const bool in = col >= col0 && col < ncols;
+              const bool in = col >= now.col0 && col < now.ncols;
               e[h] = in ? fast_exp2(fmaf(__uint_as_float(r[k + h]), c, lse_s[in ? col : 0])) : 0.f;
             }
             sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(__float_as_uint(e[0]), __float_as_uint(e[1])));
@@ -637,13 +673,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       f2_unpack(f2_add(sum[0], sum[1]), x0, x1);
       float s = __uint_as_float(x0) + __uint_as_float(x1);
       if (a.ngroups > 1) {  // this thread's own entry
-        float* acc = acc_s + w.i * kKeys + warp * 32 + lane;
-        if (w.g > 0) s += *acc;
+        float* acc = acc_s + now.i * kKeys + warp * 32 + lane;
+        if (now.add) s += *acc;
         *acc = s;
       }
-      if (done && live && page >= 0 && page < a.pool_pages) *wp = old + s;
+      if (now.wp && now.page >= 0 && now.page < a.pool_pages) *now.wp = a.decay * now.old + s;
       ++j;
-      more = w.next(a, rank);
     }
   } else if (kQ4 && warp >= kDequantWarp && any) {
     // ------------------------------------------------------------------ 4-bit rows -> operands in TMEM
@@ -652,25 +687,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
     const uint32_t tiles = (uint32_t)start_s[2] * a.ngroups;
+    const Swap swap(lane);
     uint32_t rb = 0, rph = 0;  // raw tile and its parity
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
-      ok = warp_wait(&bars[kRFull + rb], rph, abort_s, lane);
+      ok = sleep_wait(&bars[kRFull + rb], rph, abort_s);
       const uint32_t row_s = smem_u32(smem) + sl.ring + rb * kRawTile + (quarter * 32 + lane) * kQ4RowBytes;
       for (int part = 0; part < kAParts && ok; ++part) {
         const uint32_t n = j * kAParts + part, slot = n % kASlots;
         if (n % kDequantSets != (uint32_t)set) continue;
-        uint32_t raw[9];
-        load_chunk(row_s, 2 * part, raw);
-        ok = warp_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s, lane);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int h = 0; h < (part < kAParts - 1 ? 2 : 1); ++h) {
-          uint32_t v[32];
-          dequant_chunk(row_s, 2 * part + h, raw, v);
-          if (h == 0) load_chunk(row_s, 2 * part + 1, raw);
-          tmem_st32(lane_addr + 64 * slot + 32 * h, v);
+        const uint32_t to = lane_addr + 64 * slot;
+        uint32_t v[32];
+        if (part < kAParts - 1) {
+          uint32_t c0[8], c1[8], s0, s1;
+          swap.load(row_s + 64 * part, c0);
+          swap.load(row_s + 64 * part + 32, c1);
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(row_s + kQ4ScaleOff + 8 * part));
+          ok = sleep_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s);
+          if (!ok) break;
+          tc_fence_after();
+          dequant_chunk(c0, s0, v);
+          tmem_st32(to, v);
+          dequant_chunk(c1, s1, v);
+          tmem_st32(to + 32, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) swap.load(row_s + kQ4RopeOff + 32 * k, v + 8 * k);
+          ok = sleep_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st32(to, v);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -688,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     const uint32_t n = tiles * kAParts;
     for (uint32_t s = 0; s < kASlots && s < n && ok; ++s) {
       const uint32_t uses = (n - 1 - s) / kASlots;
-      ok = warp_wait(&bars[kAEmpty + s], uses & 1, abort_s, lane);
+      ok = sleep_wait(&bars[kAEmpty + s], uses & 1, abort_s);
     }
   }
   __syncthreads();

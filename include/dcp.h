@@ -707,7 +707,7 @@ int32_t dcp_block_tables(const dcp_layout_t* layout, int32_t B, int64_t* seq_len
  *            it otherwise
  *   status   device word (may be NULL)
  * q and out are 16-byte aligned.  T == 0 is a no-op.  Errors: DCP_ERR_INVALID on T < 0,
- * H < 1, a bad stride, gamma_dtype, eps or rope_style, or a null / misaligned pointer.
+ * H < 1 or H > 65535, a bad stride, gamma_dtype, eps or rope_style, or a null / misaligned pointer.
  */
 int32_t dcp_q_norm_rope(int64_t T, int32_t H, const void* q, int64_t q_stride, const int64_t* pos,
                         const void* gamma, int32_t gamma_dtype, float eps, const float* inv_freq,

@@ -27,7 +27,7 @@ def call(fn, defaults, **kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(T=-1), dict(H=0), dict(q=None), dict(q=P(24)), dict(qs=191), dict(qs=196), dict(pos=None), dict(g=P(24)),
+    dict(T=-1), dict(H=0), dict(H=65536), dict(q=None), dict(q=P(24)), dict(qs=191), dict(qs=196), dict(pos=None), dict(g=P(24)),
     dict(gd=2), dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(style=2), dict(out=None), dict(out=P(40))])
 def test_q_norm_rope(lib, kw):
     base = dict(T=1, H=2, q=P(16), qs=192, pos=P(16), g=P(16), gd=1, eps=1e-6, f=P(16), style=0, out=P(32), status=None,
