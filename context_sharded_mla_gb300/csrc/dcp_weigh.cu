@@ -21,8 +21,8 @@
 // tiles (1.2 MB a pair, 90 MB over the card: the later groups find them in L2), each
 // chunk of the queries replaced as soon as the last product with it is done.
 //
-// The 4-bit cache: 416-byte rows land raw, eight warps turn 64 dims of a row each (a lane
-// a key) into bf16 operands and write them to TMEM, where the product takes its A operand
+// The 4-bit cache: 416-byte rows land raw, eight warps turn them (a lane a key, 128 dims at
+// a time) into bf16 operands and write them to TMEM, where the product takes its A operand
 // from (lanes are keys there too); no dequantised tile is stored.  Groups of 128 rows.
 //
 // Work: the pair-tiles (2 x 128 rows of one request) of all requests in a row, cut into as
@@ -50,11 +50,10 @@ constexpr int kAParts = 5;                 // slots a tile fills: 4 of codes, on
 constexpr int kACol = 256;
 constexpr uint32_t kAllCols = 512;
 
-// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8 on dequantise, in sets of four
-#ifndef SETS
-#define SETS 2
-#endif
-constexpr int kDequantSets = SETS;
+// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8-15 dequantise, two sets of four that take
+// slots in turn.  With three 128 us against 117 (32 requests of 32k tokens, 128 heads), with four 135;
+// both sets on every slot, 64 dims each: 128 (a warp's waits for its slots are then twice as many).
+constexpr int kDequantSets = 2;
 constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kDequantWarp = 8;
 constexpr int kThreads = 256, kThreadsQ4 = kThreads + 128 * kDequantSets;
 
