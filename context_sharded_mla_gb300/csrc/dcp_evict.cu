@@ -175,27 +175,48 @@ __device__ void choose_bin(SelectSmem& sm, int d, uint32_t want, uint32_t nranks
   __syncthreads();
 }
 
-// The same for the first digit of the keys in registers, 4096 bins: 8 a thread, from the top.
-__device__ void choose_top(SelectSmem& sm, uint32_t* warp_s, uint32_t want, uint32_t nranks) {
+// The same for the first digit of the keys in registers, 4096 bins.  In a cluster every CTA adds up an equal part of the
+// bins over all of them (each reading all 4096 bins of all took 40000 clocks with 8 CTAs, distributed shared memory giving
+// some 3 bytes a clock), then all look through the part that holds the bin.  `sums`: room for kTopBins / 2 of them.
+__device__ void choose_top(SelectSmem& sm, uint32_t* sums, uint32_t* warp_s, uint32_t want, uint32_t rank,
+                           uint32_t nranks) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (nranks > 1) cluster_sync(); else __syncthreads();
-  uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0}, s = 0;  // bins from 4088 - 8 tid on, lowest first
-  const uint32_t at = smem_u32(sm.hist + (kTopBins - 8 - 8 * tid));
-  for (uint32_t r = 0; r < nranks; ++r) {
-    const uint32_t from = nranks > 1 ? mapa_shared(at, r) : at;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t x[4];
-      asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                   : "r"(from + 16 * k)
-                   : "memory");
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[4 * k + e] += x[e];
+  const uint32_t part = kTopBins / nranks;  // nranks is a power of two
+  uint32_t first = 0, from = smem_u32(sm.hist);
+  if (nranks > 1) {
+    if (tid == 0) sm.cta_n[1] = 0;
+    cluster_sync();
+    uint32_t mine = 0;
+    for (uint32_t i = tid; i < part; i += kSelThreads) {
+      uint32_t s = 0;
+#pragma unroll 8
+      for (uint32_t r = 0; r < nranks; ++r) s += ld_cluster_u32(mapa_shared(smem_u32(sm.hist + rank * part + i), r));
+      sums[i] = s;
+      mine += s;
     }
+    mine = warp_sum(mine);
+    if (lane == 0) atomicAdd(&sm.cta_n[1], mine);
+    cluster_sync();
+    uint32_t r = nranks, n = 0;
+    do {  // parts from the top, until the one that holds the want-th
+      want -= n;
+      --r;
+      n = ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[1]), r));
+    } while (n < want && r > 0);
+    first = r * part;
+    from = mapa_shared(smem_u32(sums), r);
+  } else {
+    __syncthreads();
   }
+  // part / 512 bins a thread, from the top
+  const uint32_t per = part / kSelThreads, at = part - per * (tid + 1);
+  uint32_t c[8], s = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s += c[k];
+  for (uint32_t k = 0; k < 8; ++k) {
+    c[k] = 0;
+    if (k < per) c[k] = nranks > 1 ? ld_cluster_u32(from + 4 * (at + k)) : sm.hist[at + k];
+    s += c[k];
+  }
   uint32_t incl = s;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
@@ -210,7 +231,7 @@ __device__ void choose_top(SelectSmem& sm, uint32_t* warp_s, uint32_t want, uint
 #pragma unroll
     for (int k = 7; k >= 0; --k) {
       if (before < want && want <= before + c[k]) {
-        sm.pick[0] = kTopBins - 8 - 8 * tid + k;
+        sm.pick[0] = first + at + k;
         sm.pick[1] = want - before;
         sm.pick[2] = c[k];
       }
@@ -259,36 +280,64 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
 #pragma unroll
   for (int k = 0; k < kPer; ++k) atomicAdd(&sm.hist[key[k] >> (32 - kTopBits)], 1u);
   uint32_t want = u.want;
-  choose_top(sm, warp_s, want, nranks);
+  choose_top(sm, few, warp_s, want, rank, nranks);
   uint32_t limit = sm.pick[0] << (32 - kTopBits);
   want = sm.pick[1];
   if (want < sm.pick[2]) {
-    const bool listed = nranks == 1 && sm.pick[2] <= kFewKeys;
     const uint32_t n = sm.pick[2];
+    const bool listed = n <= kFewKeys;  // on the first CTA, which looks through the list alone
     if (listed) {
+      // each CTA's own first; then to their place behind the first CTA's (one after the other, from every thread that
+      // has one, they took 8000 clocks)
+      if (rank != 0 && tid == 0) sm.cta_n[0] = 0;
+      __syncthreads();
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
         if (key[k] >> (32 - kTopBits) == limit >> (32 - kTopBits)) few[atomicAdd(&sm.cta_n[0], 1u)] = key[k];
-    }
-#pragma unroll 1
-    for (int d = 0; d < 3; ++d) {  // 8, 8 and 4 bits
-      const int shift = d == 0 ? 12 : d == 1 ? 4 : 0, above = shift + (d == 2 ? 4 : 8);
-      const uint32_t bins = (1u << (above - shift)) - 1;
-      clear_hist(sm);
-      if (listed) {
-        for (uint32_t i = tid; i < n; i += kSelThreads) {
-          const uint32_t x = few[i];
-          if ((x ^ limit) >> above == 0) count_digit(sm, x >> shift & bins);
+      if (nranks > 1) {
+        cluster_sync();
+        if (rank != 0) {
+          uint32_t to = 0;
+          for (uint32_t c = 0; c < rank; ++c) to += ld_cluster_u32(mapa_shared(smem_u32(&sm.cta_n[0]), c));
+          for (uint32_t i = tid; i < sm.cta_n[0]; i += kSelThreads)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(few + to + i), 0)), "r"(few[i]) : "memory");
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if ((key[k] ^ limit) >> above == 0) count_digit(sm, key[k] >> shift & bins);
+        cluster_sync();
       }
-      choose_bin(sm, d, want, nranks);
-      limit |= sm.pick[0] << shift;
-      want = sm.pick[1];
-      if (want == sm.pick[2]) break;
+    }
+    if (!listed || rank == 0) {
+#pragma unroll 1
+      for (int d = 0; d < 3; ++d) {  // 8, 8 and 4 bits
+        const int shift = d == 0 ? 12 : d == 1 ? 4 : 0, above = shift + (d == 2 ? 4 : 8);
+        const uint32_t bins = (1u << (above - shift)) - 1;
+        clear_hist(sm);
+        if (listed) {
+          for (uint32_t i = tid; i < n; i += kSelThreads) {
+            const uint32_t x = few[i];
+            if ((x ^ limit) >> above == 0) count_digit(sm, x >> shift & bins);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            if ((key[k] ^ limit) >> above == 0) count_digit(sm, key[k] >> shift & bins);
+        }
+        choose_bin(sm, d, want, listed ? 1 : nranks);
+        limit |= sm.pick[0] << shift;
+        want = sm.pick[1];
+        if (want == sm.pick[2]) break;
+      }
+    }
+    if (listed && nranks > 1) {  // the first CTA's answer
+      if (rank == 0 && tid == 0) sm.all[0] = limit;
+      cluster_sync();
+      limit = ld_cluster_u32(mapa_shared(smem_u32(&sm.all[0]), 0));
+      want = ld_cluster_u32(mapa_shared(smem_u32(&sm.pick[1]), 0));
+      const uint32_t in_bin = ld_cluster_u32(mapa_shared(smem_u32(&sm.pick[2]), 0));
+      if (rank != 0) {
+        __syncthreads();  // all have read their own
+        if (tid == 0) sm.pick[2] = in_bin;
+        __syncthreads();
+      }
     }
   }
   if (want == sm.pick[2]) {  // the whole bin stays: every key from `limit` on
