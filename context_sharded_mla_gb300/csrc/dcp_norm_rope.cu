@@ -12,9 +12,9 @@
 // product: the fraction of a turn to 2^-64 * position.  The step itself is off by
 // 1.5 * 2^-53 of its value, 2e-10 rad at 10^6 rad.
 //
-// dcp_q_norm_rope: 8 lanes a row of 192 dims (three 16-byte accesses a lane, 128 bytes
-// of each row side by side), 4 rows a warp step; a warp serves heads of one token, so
-// that it computes the token's sines once.
+// dcp_q_norm_rope: 8 lanes a row of 192 dims, 48 bytes each, 4 rows a warp step; a warp
+// serves heads of one token, so that it computes the token's sines once.  Memory-bound:
+// 768 bytes a row.
 // dcp_kv_norm_rope_append(_q4): a warp a token at a time, dims as store_q4_kernel has
 // them; the row is never written anywhere but into its pool.
 #include "dcp_norm_rope.cuh"
@@ -26,53 +26,109 @@ constexpr int kQDims = 192;  // 128 content + 64 position dims a head
 // ---------------------------------------------------------------- queries
 constexpr int kQThreads = 256;
 
-// Warp task: token task / parts, its heads [part * per, part * per + per).  The next step's row is on its way while
-// this one's is worked on; sines lie in shared memory (an angle is computed once a warp, by lane `pair`).
+// Lane l of a row's 8 has dims [8 l, 8 l + 8) of each 64.  For the rotation a lane wants whole pairs: of pairs
+// (2 i, 2 i + 1) it has four, first to last; of halves (i, i + 32) it trades four dims with lane l ^ 4 (both ways as
+// bf16), so that it has pairs first(l) .. first(l) + 3, their first dims in the low and their second in the high words.
 template <bool kHalves>
-__global__ void __launch_bounds__(kQThreads, 4) q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts,
-                                                                   const __nv_bfloat16* q, int64_t stride,
-                                                                   const int64_t* __restrict__ pos, const void* gamma,
-                                                                   int gamma_bf16, float eps,
-                                                                   const float* __restrict__ inv_freq,
-                                                                   __nv_bfloat16* out, int32_t* status) {
-  __shared__ __align__(16) float gamma_s[kQDims];
+struct Pairs {
+  __device__ static int first(int l) { return !kHalves ? 4 * l : l < 4 ? 8 * l : 8 * (l - 4) + 4; }
+  __device__ static uint4 in(const uint4& x, int l) {
+    if (!kHalves) return x;
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, l < 4 ? x.z : x.x, 4), b = __shfl_xor_sync(0xffffffffu, l < 4 ? x.w : x.y, 4);
+    return l < 4 ? make_uint4(x.x, x.y, a, b) : make_uint4(a, b, x.z, x.w);
+  }
+  __device__ static uint4 out(const uint4& x, int l) {
+    if (!kHalves) return x;
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, l < 4 ? x.z : x.x, 4), b = __shfl_xor_sync(0xffffffffu, l < 4 ? x.w : x.y, 4);
+    return l < 4 ? make_uint4(x.x, x.y, a, b) : make_uint4(a, b, x.z, x.w);
+  }
+  // where value k of the eight that in() gives lies in the 64 dims
+  __device__ static int dim(int l, int k) { return kHalves ? first(l) + (k & 3) + 32 * (k >> 2) : 8 * l + k; }
+};
+
+// A lane's norm weights in registers, the last eight in the order of Pairs: as they are (bf16, half the registers) or f32.
+template <bool kHalves, bool kBf16>
+struct QGamma;
+template <bool kHalves>
+struct QGamma<kHalves, true> {
+  uint4 g[3];
+  __device__ void load(const void* gamma, int l) {
+    const uint4* p = static_cast<const uint4*>(gamma) + l;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) g[j] = __ldg(p + 8 * j);
+    g[2] = Pairs<kHalves>::in(g[2], l);
+  }
+  __device__ void get(int j, float (&v)[8]) const { unpack8(g[j], v); }
+};
+template <bool kHalves>
+struct QGamma<kHalves, false> {
+  float g[3][8];
+  __device__ void load(const void* gamma, int l) {
+    const float* f = static_cast<const float*>(gamma);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[0][k] = f[8 * l + k];
+      g[1][k] = f[64 + 8 * l + k];
+      g[2][k] = f[128 + Pairs<kHalves>::dim(l, k)];
+    }
+  }
+  __device__ void get(int j, float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = g[j][k];
+  }
+};
+
+// Warp task: token task / parts, its heads [part * per, part * per + per).  The next step's row is on its way while
+// this one's is worked on; a lane's weights and the sines of its four pairs stay in registers.  8192 tokens of 128 heads:
+// 131 us (halves) and 129 (pairs), 6.2 TB/s; with weights and sines in shared memory and eight dims traded one by one 136,
+// bound there.  Four blocks an SM (two with f32 weights); three take 133, two 144.
+template <bool kHalves, bool kGammaBf16>
+__global__ void __launch_bounds__(kQThreads, kGammaBf16 ? 4 : 2)
+    q_norm_rope_kernel(int64_t T, int32_t H, int32_t per, int32_t parts, const __nv_bfloat16* q, int64_t stride,
+                       const int64_t* __restrict__ pos, const void* gamma, float eps, const float* __restrict__ inv_freq,
+                       __nv_bfloat16* out, int32_t* status) {
+  using P = Pairs<kHalves>;
   __shared__ uint64_t steps_s[kRope / 2];
-  __shared__ __align__(16) float2 turn_s[kQThreads / 32][kRope / 2];
   const int64_t task = blockIdx.x * (int64_t)(kQThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = parts == 1 ? task : (int64_t)((uint64_t)task / (uint32_t)parts);
-  const int lane = threadIdx.x & 31, l = lane & 7;  // lane of its row: dims 64 j + [8 l, 8 l + 8), j < 3
+  const int lane = threadIdx.x & 31, l = lane & 7;  // 8 lanes a row
   const int h0 = (int)(task - t * parts) * per, h1 = min(h0 + per, H);
-  const __nv_bfloat16* src = q + (t * H + h0 + (lane >> 3)) * stride + 8 * l;
+  int h = h0 + (lane >> 3);
+  const __nv_bfloat16* src = q + (t * H + h) * stride + 8 * l;
+  __nv_bfloat16* dst = out + (t * H + h) * (int64_t)kQDims + 8 * l;
   uint4 x[3];
-  auto load = [&](int h) {
+  auto load = [&](int head) {
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-      x[j] = h < h1 ? *reinterpret_cast<const uint4*>(src + 64 * j) : make_uint4(0, 0, 0, 0);
+      x[j] = head < h1 ? *reinterpret_cast<const uint4*>(src + 64 * j) : make_uint4(0, 0, 0, 0);
     src += 4 * stride;
   };
-  int h = h0 + (lane >> 3);
   int64_t p = -1;
   if (t < T) {
     p = __ldg(pos + t);
     load(h);
   }
-  load_shared(gamma, gamma_bf16, kQDims, gamma_s, inv_freq, steps_s);
+  load_steps(inv_freq, steps_s);
+  __syncthreads();
   if (p < 0) {
     if (t < T && p != -1 && lane == 0) flag(status, DCP_STATUS_BAD_POSITION);
     return;
   }
-  if (inv_freq) {
-    const Turn turn = turn_of(steps_s[lane], p);
-    turn_s[threadIdx.x >> 5][lane] = make_float2(turn.s, turn.c);
-    __syncwarp();
+  QGamma<kHalves, kGammaBf16> g;
+  if (gamma) g.load(gamma, l);
+  Turn turn[4];
+  if (inv_freq) {  // an angle a lane, handed to the lanes that turn that pair
+    const Turn mine = turn_of(steps_s[lane], p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      turn[k].s = __shfl_sync(0xffffffffu, mine.s, P::first(l) + k);
+      turn[k].c = __shfl_sync(0xffffffffu, mine.c, P::first(l) + k);
+    }
   }
-  // pairs (2 i, 2 i + 1) lie in one lane, halves (i, i + 32) in lanes l and l ^ 4
-  const float4* turns = reinterpret_cast<const float4*>(turn_s[threadIdx.x >> 5] + (kHalves ? 8 * (l & 3) : 4 * l));
-  __nv_bfloat16* dst = out + (t * H + h) * (int64_t)kQDims + 8 * l;
   for (; h - (lane >> 3) < h1; h += 4) {
     uint4 y[3] = {x[0], x[1], x[2]};
     load(h + 4);
-    float r = 1.f, v[8];
+    float r = 1.f, v[8], w[8];
     if (gamma) {
       float sum = 0.f;
 #pragma unroll
@@ -86,31 +142,26 @@ __global__ void __launch_bounds__(kQThreads, 4) q_norm_rope_kernel(int64_t T, in
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         unpack8(y[j], v);
-        scale8(v, r, gamma_s + 64 * j + 8 * l);
+        g.get(j, w);
+        scale8(v, r, w);
         y[j] = pack8(v);
       }
     }
-    unpack8(y[2], v);
-    if (gamma) scale8(v, r, gamma_s + 128 + 8 * l);
+    unpack8(P::in(y[2], l), v);
+    if (gamma) {
+      g.get(2, w);
+      scale8(v, r, w);
+    }
     if (inv_freq) {
 #pragma unroll
-      for (int k = 0; k < (kHalves ? 4 : 2); ++k) {
-        const float4 sc = turns[k];  // sine, cosine of two angles
-        if (kHalves) {
-          const float a = __shfl_xor_sync(0xffffffffu, v[2 * k], 4), b = __shfl_xor_sync(0xffffffffu, v[2 * k + 1], 4);
-          v[2 * k] = fmaf(v[2 * k], sc.y, l < 4 ? -a * sc.x : a * sc.x);
-          v[2 * k + 1] = fmaf(v[2 * k + 1], sc.w, l < 4 ? -b * sc.z : b * sc.z);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = e ? sc.z : sc.x, c = e ? sc.w : sc.y, a = v[4 * k + 2 * e], b = v[4 * k + 2 * e + 1];
-            v[4 * k + 2 * e] = fmaf(a, c, -b * s);
-            v[4 * k + 2 * e + 1] = fmaf(a, s, b * c);
-          }
-        }
+      for (int k = 0; k < 4; ++k) {
+        float &a = v[kHalves ? k : 2 * k], &b = v[kHalves ? 4 + k : 2 * k + 1];
+        const float u = a;
+        a = fmaf(u, turn[k].c, -b * turn[k].s);
+        b = fmaf(u, turn[k].s, b * turn[k].c);
       }
     }
-    y[2] = pack8(v);
+    y[2] = P::out(pack8(v), l);
     if (h < h1)
 #pragma unroll
       for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(dst + 64 * j) = y[j];
@@ -138,10 +189,12 @@ extern "C" int32_t dcp_q_norm_rope(int64_t T, int32_t H, const void* q, int64_t 
   parts = (H + per - 1) / per;
   const int64_t blocks = (T * parts + kQThreads / 32 - 1) / (kQThreads / 32);
   if (blocks > INT32_MAX) return DCP_ERR_UNSUPPORTED;
-  const auto kernel = rope_style == DCP_ROPE_HALVES ? q_norm_rope_kernel<true> : q_norm_rope_kernel<false>;
+  const bool halves = rope_style == DCP_ROPE_HALVES, bf16 = gamma_dtype == DCP_BF16;
+  const auto kernel = halves ? (bf16 ? q_norm_rope_kernel<true, true> : q_norm_rope_kernel<true, false>)
+                             : (bf16 ? q_norm_rope_kernel<false, true> : q_norm_rope_kernel<false, false>);
   kernel<<<(unsigned)blocks, kQThreads, 0, as_stream(stream)>>>(
-      T, H, per, (int32_t)parts, static_cast<const __nv_bfloat16*>(q), q_stride, pos, gamma, gamma_dtype == DCP_BF16, eps,
-      inv_freq, static_cast<__nv_bfloat16*>(out), status);
+      T, H, per, (int32_t)parts, static_cast<const __nv_bfloat16*>(q), q_stride, pos, gamma, eps, inv_freq,
+      static_cast<__nv_bfloat16*>(out), status);
   return launch_status();
 }
 

@@ -43,22 +43,15 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return u;
 }
 
-// What a block's tokens share, in shared memory: norm weights (f32 or bf16) in f32, and the frequencies' steps (f64 runs
-// at 2 operations a clock and SM: once a block, not once a warp).
-__device__ __forceinline__ void load_shared(const void* gamma, int bf16, int dims, float* g, const float* inv_freq,
-                                            uint64_t* steps) {
-  if (gamma)
-    for (int i = threadIdx.x; i < dims; i += blockDim.x)
-      g[i] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(gamma)[i]) : static_cast<const float*>(gamma)[i];
+// The frequencies' steps into shared memory (f64 runs at 2 operations a clock and SM: once a block, not once a warp).
+__device__ __forceinline__ void load_steps(const float* inv_freq, uint64_t* steps) {
   if (inv_freq && threadIdx.x < kRope / 2) steps[threadIdx.x] = turn_step(__ldg(inv_freq + threadIdx.x));
-  __syncthreads();
 }
 
 // 8 normed values: x * inv * gamma.
-__device__ __forceinline__ void scale8(float (&v)[8], float inv, const float* g) {
-  const float4 a = *reinterpret_cast<const float4*>(g), b = *reinterpret_cast<const float4*>(g + 4);
-  v[0] = v[0] * inv * a.x; v[1] = v[1] * inv * a.y; v[2] = v[2] * inv * a.z; v[3] = v[3] * inv * a.w;
-  v[4] = v[4] * inv * b.x; v[5] = v[5] * inv * b.y; v[6] = v[6] * inv * b.z; v[7] = v[7] * inv * b.w;
+__device__ __forceinline__ void scale8(float (&v)[8], float inv, const float (&g)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = v[k] * inv * g[k];
 }
 
 __device__ __forceinline__ float square8(const float (&v)[8], float sum) {
@@ -105,7 +98,14 @@ __global__ void __launch_bounds__(256, 4) norm_rope_store_kernel(Layout L, int32
   const int64_t t0 = (blockIdx.x * (int64_t)(blockDim.x / 32) + (threadIdx.x >> 5)) * per_warp;
   const int lane = threadIdx.x & 31;
   const int n = (int)min((int64_t)per_warp, T - t0);
-  load_shared(in.gamma, in.gamma_bf16, kDv, gamma_s, in.inv_freq, steps_s);
+  // norm weights in f32, as four planes: [2 j + h][lane] holds dims 256 j + 8 lane + 4 h + [0, 4)
+  if (in.gamma)
+    for (int i = threadIdx.x; i < kDv; i += blockDim.x)
+      gamma_s[128 * (2 * (i >> 8) + (i >> 2 & 1)) + 4 * (i >> 3 & 31) + (i & 3)] =
+          in.gamma_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(in.gamma)[i])
+                        : static_cast<const float*>(in.gamma)[i];
+  load_steps(in.inv_freq, steps_s);
+  __syncthreads();
   if (n <= 0) return;
   Spot spot{-1, -1, 0};
   int64_t angle_pos = 0, to = -1;  // lane: of token t0 + lane
@@ -152,7 +152,11 @@ __global__ void __launch_bounds__(256, 4) norm_rope_store_kernel(Layout L, int32
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           unpack8(x[e][j], v);
-          scale8(v, inv, gamma_s + 256 * j + 8 * lane);
+          float g[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4*>(g + 4 * h) = *reinterpret_cast<const float4*>(gamma_s + 128 * (2 * j + h) + 4 * lane);
+          scale8(v, inv, g);
           x[e][j] = pack8(v);
         }
       }
