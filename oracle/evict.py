@@ -18,7 +18,7 @@ def key_weights(q, kv, S, scale, lse, base):
     """(weights [S], their error scale [S]) of one request: q [q_len, H, 576], kv [S, 576] in position order, lse
     [q_len, H] in base e (0) or base 2 (1).  The second sums each term times 1 + |score| + |lse|."""
     q_len, H, _ = q.shape
-    s = np.einsum("thd,pd->thp", q, kv) * scale
+    s = (q.reshape(-1, q.shape[-1]) @ kv.T).reshape(q_len, H, S) * scale
     z = np.asarray(lse, np.float64) * (np.log(2.0) if base else 1.0)
     with np.errstate(invalid="ignore", over="ignore"):
         e = np.where(np.isneginf(z)[..., None], 0.0, np.exp(s - z[..., None]))

@@ -184,3 +184,34 @@ def test_weights_and_evictions_of_a_ranks_shards():
         d.evict(whole.tables.block_table, whole.tables.seq_lens, new, 2, 5)
         assert torch.equal(d.arena, whole.dec.arena[a:e]) and torch.equal(d.weights, whole.dec.weights[a:e])
         assert d.status_bits() == 0
+
+
+def test_two_threads_at_once():
+    """Weights, selection and move from two host threads, a stream each, give what they give one after the other."""
+    import threading
+    runs = [Run("bf16", seed=11), Run("q4", seed=12)]
+    want = [Run("bf16", seed=11), Run("q4", seed=12)]
+
+    def go(r):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for lens, evicts in (([180, 60, 40], False), ([181, 61, 41], False), ([90, 61, 11], True), ([91, 62, 12], False)):
+                r.new.copy_(torch.tensor(lens))
+                r.shrink(2, 6) if evicts else r.grow()
+        stream.synchronize()
+
+    for r in runs + want:
+        r.draw()
+    torch.cuda.synchronize()
+    for r in want:
+        go(r)
+    threads = [threading.Thread(target=go, args=(r,)) for r in runs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for r, w in zip(runs, want):
+        assert torch.equal(r.dec.o, w.dec.o) and torch.equal(r.dec.weighed, w.dec.weighed)
+        for b, S in enumerate([91, 62, 12]):
+            assert np.array_equal(r.rows(b, S), w.rows(b, S))
+        assert r.dec.status_bits() == 0

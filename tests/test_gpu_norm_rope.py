@@ -52,7 +52,8 @@ def check(got, want, bound, what):
 
 @pytest.mark.parametrize("T,H", [(1, 1), (3, 5), (2, 96), (64, 96), (301, 128), (5000, 7)])
 @pytest.mark.parametrize("halves", [False, True])
-@pytest.mark.parametrize("norm,rope", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("norm,rope", [(torch.bfloat16, True), (torch.float32, True), (None, True), (torch.bfloat16, False),
+                                       (torch.float32, False), (None, False)])
 def test_query(T, H, halves, norm, rope):
     dcp = _dcp()
     g = torch.Generator().manual_seed(T * 131 + H)
@@ -61,7 +62,7 @@ def test_query(T, H, halves, norm, rope):
     pos[0] = 0
     if T > 2:
         pos[1], pos[2] = (1 << 24) - 1, 1 << 31
-    gamma = (1 + 0.3 * torch.randn(192, generator=g)).to(torch.bfloat16 if halves else torch.float32)
+    gamma = (1 + 0.3 * torch.randn(192, generator=g)).to(norm or torch.float32)
     out = torch.full_like(q, 9.0).cuda()
     dcp.dcp_q_norm_rope(q.cuda(), pos.cuda(), out, gamma=gamma.cuda() if norm else None, eps=1e-5,
                         inv_freq=FREQ.cuda() if rope else None, rope_style=int(halves))

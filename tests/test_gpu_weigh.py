@@ -27,6 +27,11 @@ def _dcp():
     return dcp
 
 
+def scores(q, kv):
+    """q [q_len, H, 576] . kv [S, 576] -> [q_len, H, S]."""
+    return (q.reshape(-1, 576) @ kv.T).reshape(*q.shape[:2], len(kv))
+
+
 class Case:
     """Requests in a cache (rows that belong to nobody are NaN), their queries and merged lse."""
 
@@ -61,7 +66,7 @@ class Case:
         for b, S in enumerate(lens):
             if S < q_len:
                 continue
-            s = np.einsum("thd,pd->thp", to_f64(self.q[b]), self.values[b]) * SCALE
+            s = scores(to_f64(self.q[b]), self.values[b]) * SCALE
             s = np.where(np.arange(S) <= (S - q_len + np.arange(q_len))[:, None, None], s, -np.inf)
             m = s.max(-1)
             self.lse[b] = torch.from_numpy(m + np.log(np.exp(s - m[..., None]).sum(-1)))
@@ -89,8 +94,8 @@ class Case:
         worst = 0.0
         for b, S in enumerate(self.lens):
             want, size = evict.key_weights(to_f64(self.q[b]), self.values[b], S, SCALE, to_f64(self.lse[b]), self.base)
-            dots = np.einsum("thd,pd->thp", np.abs(to_f64(self.q[b])), np.abs(self.values[b])) if S else np.zeros((1, 1, 0))
-            ds = 576 * 2 * U * SCALE * (dots.max((0, 1)) if S else np.zeros(0))
+            dots = scores(np.abs(to_f64(self.q[b])), np.abs(self.values[b]))
+            ds = 576 * 2 * U * SCALE * dots.max((0, 1))
             p = np.arange(S)
             own, row = olayout.owner(p, self.N, self.I), olayout.local_row(p, self.N, self.I)
             for r in range(self.begin, self.end):
@@ -250,7 +255,7 @@ def test_rows_beyond_four_gigabytes():
     for k in range(4):
         arena[0, int(ids[0, k]) * P:int(ids[0, k]) * P + len(x[64 * k:64 * k + 64])] = x[64 * k:64 * k + 64]
     q = torch.randn(1, 1, 20, 576, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
-    s = np.einsum("hd,pd->hp", to_f64(q)[0, 0], to_f64(x)) * SCALE
+    s = to_f64(q)[0, 0] @ to_f64(x).T * SCALE
     lse = np.log(np.exp(s).sum(-1))
     w = torch.zeros(1, 1, 256, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
