@@ -1,8 +1,9 @@
 """Norm and rotation of queries and latent rows on the GPU, against fp64.
 
 Bounds (u = 2^-24).  A normed value x r g: the squares' sum has at most 30 roundings, r = rsqrt(..) 4 u, two products:
-below 2^-18 of itself.  A rotated one: products of such values with a sine and a cosine that are off by 2^-22 (their
-arguments' 2^-23 of a half turn, the functions' own 2 u), two roundings: 2^-17 (|a| + |b|).  Then one rounding to
+below 2^-18 of itself.  A rotated one: products of such values with a sine and a cosine that are off by 2^-20 (their
+arguments' roundings, 2 pi u + pi u, and the hardware functions' 2^-21 in [-pi, pi]), two roundings: 2^-18 + 2^-20 + 2 u,
+below 2^-17 (|a| + |b|).  Then one rounding to
 bf16, half a step: 2^-8 of the value."""
 
 import numpy as np
