@@ -654,88 +654,83 @@ def dcp_q_norm_rope(q, pos, out, gamma=None, eps=1e-6, inv_freq=None, rope_style
     _check("dcp_q_norm_rope", rc)
 
 
-def _norm_rope_append(name, width, dtype, layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena,
-                      pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos, stream):
-    dev = torch.cuda.current_device()
-    T = pos.numel()
-    B, stride = _table(block_table, "block_table")
-    at_kv, kv_stride = _strided(kv, "kv", (T, 576), dev)
-    at_gamma, code = _gamma(gamma, 512, dev)
-    rc = getattr(load_library(), name)(
-        layout, shard_begin, shard_end, at_kv, kv_stride, at_gamma, code, eps,
-        None if inv_freq is None else _at(inv_freq, "inv_freq", torch.float32, (32,), dev), rope_style,
-        None if rope_pos is None else _at(rope_pos, "rope_pos", torch.int64, (T,), dev),
-        _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T,
-        _at(block_table, "block_table", torch.int32, None, dev), B, stride, max_pages,
-        _at(arena, "arena", dtype, (shard_end - shard_begin, pool_pages * layout.page_size, width), dev), pool_pages,
-        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
-    _check(name, rc)
+def _norm_rope_append(name, width, dtype, doc):
+    def call(layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena, pool_pages, status, gamma=None,
+             eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, rope_pos=None, stream=None):
+        dev = torch.cuda.current_device()
+        T = pos.numel()
+        B, stride = _table(block_table, "block_table")
+        at_kv, kv_stride = _strided(kv, "kv", (T, 576), dev)
+        at_gamma, code = _gamma(gamma, 512, dev)
+        rc = getattr(load_library(), name)(
+            layout, shard_begin, shard_end, at_kv, kv_stride, at_gamma, code, eps,
+            None if inv_freq is None else _at(inv_freq, "inv_freq", torch.float32, (32,), dev), rope_style,
+            None if rope_pos is None else _at(rope_pos, "rope_pos", torch.int64, (T,), dev),
+            _at(pos, "pos", torch.int64, (T,), dev), _at(req, "req", torch.int32, (T,), dev), T,
+            _at(block_table, "block_table", torch.int32, None, dev), B, stride, max_pages,
+            _at(arena, "arena", dtype, (shard_end - shard_begin, pool_pages * layout.page_size, width), dev), pool_pages,
+            _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+        if rc:
+            _check(name, rc)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = doc
+    return call
 
 
-def dcp_kv_norm_rope_append(layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena, pool_pages,
-                            status, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, rope_pos=None,
-                            stream=None):
+dcp_kv_norm_rope_append = _norm_rope_append(
+    "dcp_kv_norm_rope_append", 576, torch.bfloat16,
     """dcp_kv_append of a projection's rows kv [T, 576] bf16 (a view with equally strided rows): dims [0, 512) RMS-normed
     (gamma [512]; None: no norm), dims [512, 576) rotated by rope_pos (None: pos) times inv_freq f32 [32] (None: no
-    rotation), rounded once and written into their owners' pools."""
-    _norm_rope_append("dcp_kv_norm_rope_append", 576, torch.bfloat16, layout, shard_begin, shard_end, kv, pos, req,
-                      block_table, max_pages, arena, pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos,
-                      stream)
+    rotation), rounded once and written into their owners' pools.""")
+dcp_kv_norm_rope_append_q4 = _norm_rope_append(
+    "dcp_kv_norm_rope_append_q4", Q4_ROW_BYTES, torch.uint8,
+    """dcp_kv_norm_rope_append into a 4-bit arena [shards, pool_pages*P, 416] uint8.""")
 
 
-def dcp_kv_norm_rope_append_q4(layout, shard_begin, shard_end, kv, pos, req, block_table, max_pages, arena, pool_pages,
-                               status, gamma=None, eps=1e-6, inv_freq=None, rope_style=DCP_ROPE_PAIRS, rope_pos=None,
-                               stream=None):
-    """dcp_kv_norm_rope_append into a 4-bit arena [shards, pool_pages*P, 416] uint8."""
-    _norm_rope_append("dcp_kv_norm_rope_append_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, kv, pos,
-                      req, block_table, max_pages, arena, pool_pages, status, gamma, eps, inv_freq, rope_style, rope_pos,
-                      stream)
+def _key_weights(name, width, dtype, doc):
+    def call(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale, lse_base, lse,
+             weights, status, old_lens=None, decay=1.0, stream=None):
+        dev = torch.cuda.current_device()
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be [B, q_len, H, 576]")
+        B, q_len, H, _ = q.shape
+        n = shard_end - shard_begin
+        rows, stride = _table(block_table, "block_table")
+        if rows != B:
+            raise ValueError("block_table must have one row per request")
+        rc = getattr(load_library(), name)(
+            layout, shard_begin, shard_end, _at(q, "q", torch.bfloat16, (B, q_len, H, 576), dev), B, q_len, H,
+            _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
+            _at(block_table, "block_table", torch.int32, None, dev), stride, max_pages,
+            _at(seq_lens, "seq_lens", torch.int64, (B,), dev), scale, lse_base,
+            _at(lse, "lse", torch.float32, (B, q_len, H), dev),
+            None if old_lens is None else _at(old_lens, "old_lens", torch.int64, (B,), dev), decay,
+            _at(weights, "weights", torch.float32, (n, B, _unit_rows(weights, "weights")), dev), weights.shape[2],
+            _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+        if rc:
+            _check(name, rc)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = doc
+    return call
 
 
-def _key_weights(name, width, dtype, layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages,
-                 seq_lens, scale, lse_base, lse, weights, status, old_lens, decay, stream):
-    dev = torch.cuda.current_device()
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [B, q_len, H, 576]")
-    B, q_len, H, _ = q.shape
-    n = shard_end - shard_begin
-    if _table(block_table, "block_table")[0] != B:
-        raise ValueError("block_table must have one row per request")
-    if not isinstance(weights, torch.Tensor) or weights.dim() != 3 or weights.shape[:2] != (n, B):
-        raise ValueError(f"weights must be [{n}, {B}, max_pages * P or more]")
-    rc = getattr(load_library(), name)(
-        layout, shard_begin, shard_end, _at(q, "q", torch.bfloat16, (B, q_len, H, 576), dev), B, q_len, H,
-        _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
-        _at(block_table, "block_table", torch.int32, None, dev), block_table.shape[1], max_pages,
-        _at(seq_lens, "seq_lens", torch.int64, (B,), dev), scale, lse_base,
-        _at(lse, "lse", torch.float32, (B, q_len, H), dev),
-        None if old_lens is None else _at(old_lens, "old_lens", torch.int64, (B,), dev), decay,
-        _at(weights, "weights", torch.float32, None, dev), weights.shape[2],
-        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
-    _check(name, rc)
+def _unit_rows(t, name):
+    """Entries of a (request, shard) unit in a tensor [shards, B, entries]."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be [shards, B, rows]")
+    return t.shape[2]
 
 
-def dcp_mla_key_weights(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale,
-                        lse_base, lse, weights, status, old_lens=None, decay=1.0, stream=None):
+dcp_mla_key_weights = _key_weights(
+    "dcp_mla_key_weights", 576, torch.bfloat16,
     """weights [shards, B, >= max_pages * P] f32: to every cached row the softmax weight that the queries q [B, q_len, H,
     576] give it under their merged lse [B, q_len, H], summed over them, is added; rows at positions below old_lens (int64
-    [B]; None: 0) keep decay times what they had, the others start from 0."""
-    _key_weights("dcp_mla_key_weights", 576, torch.bfloat16, layout, shard_begin, shard_end, q, arena, pool_pages,
-                 block_table, max_pages, seq_lens, scale, lse_base, lse, weights, status, old_lens, decay, stream)
-
-
-def dcp_mla_key_weights_q4(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale,
-                           lse_base, lse, weights, status, old_lens=None, decay=1.0, stream=None):
-    """dcp_mla_key_weights over a 4-bit arena [shards, pool_pages*P, 416] uint8."""
-    _key_weights("dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, q, arena,
-                 pool_pages, block_table, max_pages, seq_lens, scale, lse_base, lse, weights, status, old_lens, decay,
-                 stream)
-
-
-def _unit_rows(t, name, n, B):
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[:2] != (n, B):
-        raise ValueError(f"{name} must be [{n}, {B}, rows]")
-    return t.shape[2]
+    [B]; None: 0) keep decay times what they had, the others start from 0.""")
+dcp_mla_key_weights_q4 = _key_weights(
+    "dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8,
+    """dcp_mla_key_weights over a 4-bit arena [shards, pool_pages*P, 416] uint8.""")
 
 
 def dcp_evict_select(layout, shard_begin, shard_end, seq_lens, new_lens, sinks, recent, weights, kept, status,
@@ -749,37 +744,39 @@ def dcp_evict_select(layout, shard_begin, shard_end, seq_lens, new_lens, sinks, 
     rc = load_library().dcp_evict_select(
         layout, shard_begin, shard_end, B, _at(seq_lens, "seq_lens", torch.int64, (B,), dev),
         _at(new_lens, "new_lens", torch.int64, (B,), dev), sinks, recent,
-        _at(weights, "weights", torch.float32, None, dev), _unit_rows(weights, "weights", n, B),
-        _at(kept, "kept", torch.int32, None, dev), _unit_rows(kept, "kept", n, B),
+        _at(weights, "weights", torch.float32, (n, B, _unit_rows(weights, "weights")), dev), weights.shape[2],
+        _at(kept, "kept", torch.int32, (n, B, _unit_rows(kept, "kept")), dev), kept.shape[2],
         _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
     _check("dcp_evict_select", rc)
 
 
-def _compact(name, width, dtype, layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages,
-             status, weights, stream):
-    dev = torch.cuda.current_device()
-    B, stride = _table(block_table, "block_table")
-    n = shard_end - shard_begin
-    rc = getattr(load_library(), name)(
-        layout, shard_begin, shard_end, _at(kept, "kept", torch.int32, None, dev), _unit_rows(kept, "kept", n, B), B,
-        _at(new_lens, "new_lens", torch.int64, (B,), dev), _at(block_table, "block_table", torch.int32, None, dev),
-        stride, max_pages, _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
-        None if weights is None else _at(weights, "weights", torch.float32, None, dev),
-        0 if weights is None else _unit_rows(weights, "weights", n, B),
-        _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
-    _check(name, rc)
+def _compact(name, width, dtype, doc):
+    def call(layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages, status, weights=None,
+             stream=None):
+        dev = torch.cuda.current_device()
+        B, stride = _table(block_table, "block_table")
+        n = shard_end - shard_begin
+        at_weights, w_stride = None, 0
+        if weights is not None:
+            w_stride = _unit_rows(weights, "weights")
+            at_weights = _at(weights, "weights", torch.float32, (n, B, w_stride), dev)
+        entries = _unit_rows(kept, "kept")
+        rc = getattr(load_library(), name)(
+            layout, shard_begin, shard_end, _at(kept, "kept", torch.int32, (n, B, entries), dev), entries, B,
+            _at(new_lens, "new_lens", torch.int64, (B,), dev), _at(block_table, "block_table", torch.int32, None, dev),
+            stride, max_pages, _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
+            at_weights, w_stride, _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+        if rc:
+            _check(name, rc)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = doc
+    return call
 
 
-def dcp_kv_compact(layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages, status,
-                   weights=None, stream=None):
+dcp_kv_compact = _compact(
+    "dcp_kv_compact", 576, torch.bfloat16,
     """Row i of every shard and request becomes its row kept[shard, b, i] >= i, in place, for the rows that new_lens (int64
-    [B]) leaves; weights [shards, B, rows] f32 move with them.  block_table still holds the pages of the old lengths."""
-    _compact("dcp_kv_compact", 576, torch.bfloat16, layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages,
-             arena, pool_pages, status, weights, stream)
-
-
-def dcp_kv_compact_q4(layout, shard_begin, shard_end, kept, new_lens, block_table, max_pages, arena, pool_pages, status,
-                      weights=None, stream=None):
-    """dcp_kv_compact on a 4-bit arena [shards, pool_pages*P, 416] uint8."""
-    _compact("dcp_kv_compact_q4", Q4_ROW_BYTES, torch.uint8, layout, shard_begin, shard_end, kept, new_lens, block_table,
-             max_pages, arena, pool_pages, status, weights, stream)
+    [B]) leaves; weights [shards, B, rows] f32 move with them.  block_table still holds the pages of the old lengths.""")
+dcp_kv_compact_q4 = _compact(
+    "dcp_kv_compact_q4", Q4_ROW_BYTES, torch.uint8, """dcp_kv_compact on a 4-bit arena [shards, pool_pages*P, 416] uint8.""")

@@ -7,17 +7,19 @@
 //
 // select_kernel: one cluster of CTAs for a (request, shard) unit, each thread holding its
 // rows' weights in registers as integers of the same order.  The k-th largest of the rows
-// that compete is found digit by digit, 8 bits at a time: histograms in shared memory, one
-// copy a lane, so that the lanes of a warp never meet in a bank however alike their
-// weights are (weights of one magnitude share their first digit); the CTAs add theirs up
-// through distributed shared memory.  Rows are then written in order: ballots, one block
-// scan of their counts.  Only whole numbers are added, so the result depends on no order.
+// that compete is found digit by digit: 12 bits first (one histogram a CTA; weights of one
+// magnitude share their first bits, but few lanes of a warp the first 12), the others among
+// the keys of that bin alone.  Rows are then written in order: ballots, and a sum over the
+// warps.  Only whole numbers are added, so the result depends on no order.  Bound by its
+// instructions and block barriers: 512 units of 16384 rows (33 MB) take 28 us, 1.2 TB/s; a
+// unit of a few rows 5 us.
 //
 // compact_kernel: row i <- row kept[i] >= i.  Writing row i is safe once the rows up to
 // i have been read: a later row j > i reads kept[j] >= j.  So a cluster walks a unit in
 // windows, reads a window (bulk copies into a ring of slots in shared memory, several
 // windows ahead), and writes it when every CTA of the cluster has its part of it.
-// Memory-bound: 2 * 1152 (or 416) bytes a row; a warp issues everything.
+// Memory-bound: 2 * 1152 (or 416) bytes a row; 524288 rows in 194 us, 6.3 TB/s (4-bit: 236
+// us with their read-back).
 #include "dcp_internal.cuh"
 
 #include "sm100_ptx.cuh"
@@ -211,12 +213,18 @@ __device__ void choose_top(SelectSmem& sm, uint32_t* sums, uint32_t* warp_s, uin
   // part / 512 bins a thread, from the top
   const uint32_t per = part / kSelThreads, at = part - per * (tid + 1);
   uint32_t c[8], s = 0;
+  if (nranks > 1) {
 #pragma unroll
-  for (uint32_t k = 0; k < 8; ++k) {
-    c[k] = 0;
-    if (k < per) c[k] = nranks > 1 ? ld_cluster_u32(from + 4 * (at + k)) : sm.hist[at + k];
-    s += c[k];
+    for (uint32_t k = 0; k < 8; ++k) c[k] = k < per ? ld_cluster_u32(from + 4 * (at + k)) : 0;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 x = ld_shared_v4(from + 4 * at + 16 * k);
+      c[4 * k] = x.x; c[4 * k + 1] = x.y; c[4 * k + 2] = x.z; c[4 * k + 3] = x.w;
+    }
   }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += c[k];
   uint32_t incl = s;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
@@ -325,6 +333,34 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectArgs a) {
         limit |= sm.pick[0] << shift;
         want = sm.pick[1];
         if (want == sm.pick[2]) break;
+        if (listed && d == 0 && sm.pick[2] <= 32) {  // as few as that are ranked one against another
+          const uint32_t last = sm.pick[2];
+          if (tid == 0) sm.cta_n[1] = 0;
+          __syncthreads();
+          for (uint32_t i = tid; i < n; i += kSelThreads) {
+            const uint32_t x = few[i];
+            if ((x ^ limit) >> shift == 0) sm.all[atomicAdd(&sm.cta_n[1], 1u)] = x;
+          }
+          __syncthreads();
+          if (warp == 0) {
+            const uint32_t mine = lane < last ? sm.all[lane] : 0u;
+            uint32_t gt = 0, ge = 0;
+            for (uint32_t i = 0; i < last; ++i) {
+              const uint32_t other = __shfl_sync(0xffffffffu, mine, i);
+              gt += other > mine;
+              ge += other >= mine;
+            }
+            if (lane < last && gt < want && want <= ge) {  // the want-th largest and its equals: the same answer
+              sm.pick[0] = mine;
+              sm.pick[1] = want - gt;
+              sm.pick[2] = ge - gt;
+            }
+          }
+          __syncthreads();
+          limit = sm.pick[0];
+          want = sm.pick[1];
+          break;
+        }
       }
     }
     if (listed && nranks > 1) {  // the first CTA's answer

