@@ -306,19 +306,13 @@ __device__ __forceinline__ int32_t pool_row(const WeighArgs& a, int32_t rs, int3
   return (int32_t)(rs * a.pool_rows + page * a.L.P + rho % (int32_t)a.L.P);
 }
 
-// 4-bit rows lie 416 bytes apart: 16-byte loads of eight neighbouring lanes meet two to a bank.  Lanes 4 to 7 of each
-// eight take every other piece first, which they do not meet, and swap.
-struct Swap {
-  bool odd;
-  __device__ explicit Swap(int lane) : odd((lane & 4) != 0) {}
-  // 32 bytes at `at`, in order
-  __device__ __forceinline__ void load(uint32_t at, uint32_t* w) const {
-    const uint32_t d = odd ? 16u : 0u;
-    const uint4 x = ld_shared_v4(at + d), y = ld_shared_v4(at + 16 - d);
-    w[0] = odd ? y.x : x.x; w[1] = odd ? y.y : x.y; w[2] = odd ? y.z : x.z; w[3] = odd ? y.w : x.w;
-    w[4] = odd ? x.x : y.x; w[5] = odd ? x.y : y.y; w[6] = odd ? x.z : y.z; w[7] = odd ? x.w : y.w;
-  }
-};
+// 32 bytes of shared memory.  (4-bit rows lie 416 bytes apart, so that eight neighbouring lanes meet two to a bank;
+// sparing that by a trade of the halves costs more instructions than it is worth.)
+__device__ __forceinline__ void load32(uint32_t at, uint32_t* w) {
+  const uint4 x = ld_shared_v4(at), y = ld_shared_v4(at + 16);
+  w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+}
 // Four scales (64 dims) and 8 words of codes -> 32 bf16 pairs.
 __device__ __forceinline__ void dequant_chunk(const uint32_t (&w)[8], uint32_t four, uint32_t (&v)[32]) {
 #pragma unroll
@@ -686,7 +680,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
     const uint32_t tiles = (uint32_t)start_s[2] * a.ngroups;
-    const Swap swap(lane);
     uint32_t rb = 0, rph = 0;  // raw tile and its parity
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
@@ -699,8 +692,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         uint32_t v[32];
         if (part < kAParts - 1) {
           uint32_t c0[8], c1[8], s0, s1;
-          swap.load(row_s + 64 * part, c0);
-          swap.load(row_s + 64 * part + 32, c1);
+          load32(row_s + 64 * part, c0);
+          load32(row_s + 64 * part + 32, c1);
           asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(row_s + kQ4ScaleOff + 8 * part));
           ok = sleep_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s);
           if (!ok) break;
@@ -711,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
           tmem_st32(to + 32, v);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) swap.load(row_s + kQ4RopeOff + 32 * k, v + 8 * k);
+          for (int k = 0; k < 4; ++k) load32(row_s + kQ4RopeOff + 32 * k, v + 8 * k);
           ok = sleep_wait(&bars[kAEmpty + slot], ((n / kASlots) & 1) ^ 1, abort_s);
           if (!ok) break;
           tc_fence_after();
