@@ -17,9 +17,12 @@
 // through a ring of 16-KB chunks (128 keys x 64 dims); the chunks of a tile are consumed
 // in order, so a product starts when its first chunk is there.
 //
-// More than 256 rows: groups of at most 256, one after the other over a block of kBlock
-// tiles (1.2 MB a pair, 90 MB over the card: the later groups find them in L2), each
-// chunk of the queries replaced as soon as the last product with it is done.
+// More than 256 rows: groups of at most 256, one after the other over a block of pair-tiles
+// that the later groups find in L2, each chunk of the queries replaced as soon as the last
+// product with it is done.  Blocks of two pair-tiles (0.6 MB a pair of SMs, 45 MB over the
+// card), the last up to four of a run as one: 4 requests of 128k tokens with 64 queries of
+// 96 heads take 2091 us, with blocks of four 2309, of eight 2646, of one 2132.  4-bit:
+// blocks of eight (65 MB): 871 us where four take 931 and sixteen 891.
 //
 // The 4-bit cache: 416-byte rows land raw, eight warps turn them (a lane a key, 128 dims at
 // a time) into bf16 operands and write them to TMEM, where the product takes its A operand
@@ -36,7 +39,8 @@ constexpr int kKeys = 128;                 // keys a CTA brings to a tile
 constexpr int kChunks = kDk / kChunkDims;  // 9
 constexpr int kStageBytes = kKeys * 128;   // 16 KB: 128 keys x 64 dims
 constexpr int kMaxStages = 12;
-constexpr int kBlock = 4;                  // pair-tiles of a block when there is more than one row group
+constexpr int kBlock = 2, kBlockLast = 4;  // pair-tiles of a block when there is more than one row group
+constexpr int kBlockQ4 = 8;
 constexpr int kRawTile = kKeys * kQ4RowBytes;
 constexpr int kMaxRaw = 3;
 // The tensor core cuts its running sum off toward zero at each of the 36 steps of a score instead of rounding it: half
@@ -65,6 +69,7 @@ struct WeighArgs {
   int32_t stages;               // ring stages (bf16) or raw tiles (4-bit)
   int32_t box_rows, nbox;       // rows a copy (min(P, 64)), copies a tile
   int32_t npairs;
+  int32_t block, block_last;    // pair-tiles of a block; a rest of up to block_last is one
   int64_t pool_rows, pool_pages, max_rows;
   const unsigned char* arena;
   const int32_t* bt;
@@ -162,16 +167,15 @@ enum : int {
 struct Smem {
   uint32_t q, ring, bars, lse, acc, misc, total;
 };
-// Queries (9 chunks of Rg / 2 rows), the ring, barriers, lse of the group's rows (a copy a warp: no
-// barrier among warps that may give up a wait), a block's sums.
-__host__ __device__ inline Smem smem_of(int Rg, int stages, int stage_bytes) {
+// Queries (9 chunks of Rg / 2 rows), the ring, barriers, lse of the rows of two groups, a block's sums (4-bit), the rest.
+__host__ __device__ inline Smem smem_of(int Rg, int stages, int stage_bytes, bool q4) {
   Smem s;
   s.q = 0;
   s.ring = (uint32_t)kChunks * Rg / 2 * 128;
   s.bars = s.ring + (uint32_t)stages * stage_bytes;
   s.lse = s.bars + (kNumBars * 8 + 15) / 16 * 16;
-  s.acc = s.lse + 4 * 256 * 4;
-  s.misc = s.acc + kBlock * kKeys * 4;
+  s.acc = s.lse + 2 * 256 * 4;
+  s.misc = s.acc + (q4 ? kBlockQ4 * kKeys * 4 : 0);
   s.total = s.misc + 128;
   return s;
 }
@@ -230,7 +234,7 @@ struct Walk {
   }
   __device__ void block(const WeighArgs& a) {
     nblk = min(left, npt - pt);
-    if (a.ngroups > 1) nblk = min(nblk, kBlock);
+    if (a.ngroups > 1 && nblk > a.block_last) nblk = a.block;
     g = i = 0;
     rs0 = rs;
     t0 = t;
@@ -334,18 +338,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv, WeighArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int kBlockThreads = kQ4 ? kThreadsQ4 : kThreads, kWarps = kBlockThreads / 32;
-  __shared__ int32_t warp_sums[kWarps];
-  __shared__ int32_t start_s[3];
   if ((smem_u32(smem) & 1023u) != 0) {  // every CTA of the launch sees the same base: all leave
     if (threadIdx.x == 0) flag(a.status, DCP_STATUS_INTERNAL);
     return;
   }
-  const Smem sl = smem_of(a.Rg, a.stages, kQ4 ? kRawTile : kStageBytes);
+  const Smem sl = smem_of(a.Rg, a.stages, kQ4 ? kRawTile : kStageBytes, kQ4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sl.bars);
-  float* lse_s = reinterpret_cast<float*>(smem + sl.lse) + 256 * (threadIdx.x >> 5 & 3);
+  float* lse_s = reinterpret_cast<float*>(smem + sl.lse);
   float* acc_s = reinterpret_cast<float*>(smem + sl.acc);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + sl.misc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + sl.misc + 4);
+  int32_t* start_s = reinterpret_cast<int32_t*>(smem + sl.misc + 8);       // request, pair-tile, pair-tiles of the run
+  int32_t* warp_sums = reinterpret_cast<int32_t*>(smem + sl.misc + 32);
+  static_assert(32 + 4 * kWarps <= 128, "room for them");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
   const int pair = blockIdx.x >> 1;
@@ -607,24 +612,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     };
     bool ok = true, more = true;
     uint32_t j = 0;
+    float part[kBlockLast] = {0.f, 0.f, 0.f, 0.f};  // sums over the groups so far, by pair-tile of the block
     Key key = look();
     while (more && ok) {
-      if (key.lse_at >= 0) {
-        __syncwarp();  // the columns' lse of the group before have been used
-        for (int k = lane; k < key.ncols; k += 32) {
-          const float l = __ldg(a.lse + key.lse_at + k);
-          // a row that saw nothing adds 2^-inf
-          lse_s[k] = l == -INFINITY ? -INFINITY : -(a.base2 ? l : l * kLog2e);
-        }
-        __syncwarp();
-      }
       const Key now = key;
+      float l[8];
+      if (now.lse_at >= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) l[k] = lane + 32 * k < now.ncols ? __ldg(a.lse + now.lse_at + lane + 32 * k) : 0.f;
+      }
       more = w.next(a, rank);
       if (more) key = look();
       const uint32_t buf = j & 1;
       ok = sleep_wait(&bars[kSFull + buf], (j >> 1) & 1, abort_s);
       if (!ok) break;
       tc_fence_after();
+      if (now.lse_at >= 0) {
+        // A new group's columns, in the buffer of the group before last: this tile's scores are there, so every warp has
+        // freed those of the tile before last, and with them that group.  All warps write the same values.
+        lse_s = reinterpret_cast<float*>(smem + sl.lse) + (lse_s == reinterpret_cast<float*>(smem + sl.lse) ? 256 : 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)  // a row that saw nothing adds 2^-inf
+          lse_s[lane + 32 * k] = l[k] == -INFINITY ? -INFINITY : -(a.base2 ? l[k] : l[k] * kLog2e);
+        __syncwarp();
+      }
       const uint32_t s_addr = tmem + ((uint32_t)(warp * 32) << 16) + (kQ4 ? 128 : 256) * buf;
       const bool masked = __any_sync(0xffffffffu, now.col0 > 0);
       uint64_t sum[2] = {0, 0};
@@ -665,10 +676,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       uint32_t x0, x1;
       f2_unpack(f2_add(sum[0], sum[1]), x0, x1);
       float s = __uint_as_float(x0) + __uint_as_float(x1);
-      if (a.ngroups > 1) {  // this thread's own entry
-        float* acc = acc_s + now.i * kKeys + warp * 32 + lane;
-        if (now.add) s += *acc;
-        *acc = s;
+      if (a.ngroups > 1) {
+        if (kQ4) {  // this thread's own entry
+          float* acc = acc_s + now.i * kKeys + warp * 32 + lane;
+          if (now.add) s += *acc;
+          *acc = s;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kBlockLast; ++k)
+            if (now.i == k) {
+              if (now.add) s += part[k];
+              part[k] = s;
+            }
+        }
       }
       if (now.wp && now.page >= 0 && now.page < a.pool_pages) *now.wp = a.decay * now.old + s;
       ++j;
@@ -791,9 +811,11 @@ int32_t weigh(const WeighCall& c) {
   a.Rg = ((a.R + groups - 1) / groups + 31) / 32 * 32;
   a.ngroups = (a.R + a.Rg - 1) / a.Rg;
   const int stage_bytes = kQ4 ? kRawTile : kStageBytes, most_stages = kQ4 ? kMaxRaw : kMaxStages;
-  a.stages = (int32_t)(kSmemBudget - 1024 - smem_of(a.Rg, 0, 0).total) / stage_bytes;  // 1 KB: the static variables
+  a.stages = (int32_t)(kSmemBudget - smem_of(a.Rg, 0, 0, kQ4).total) / stage_bytes;
   a.stages = std::min(a.stages, (int32_t)most_stages);
-  const size_t smem = smem_of(a.Rg, a.stages, stage_bytes).total;
+  const size_t smem = smem_of(a.Rg, a.stages, stage_bytes, kQ4).total;
+  a.block = kQ4 ? kBlockQ4 : kBlock;
+  a.block_last = kQ4 ? kBlockQ4 : kBlockLast;
   a.box_rows = std::min(c.layout->page_size, kTile);
   a.nbox = kKeys / a.box_rows;
   PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
