@@ -39,8 +39,7 @@ constexpr int kKeys = 128;                 // keys a CTA brings to a tile
 constexpr int kChunks = kDk / kChunkDims;  // 9
 constexpr int kStageBytes = kKeys * 128;   // 16 KB: 128 keys x 64 dims
 constexpr int kMaxStages = 12;
-constexpr int kBlock = 2, kBlockLast = 4;  // pair-tiles of a block when there is more than one row group
-constexpr int kBlockQ4 = 8;
+constexpr int kBlockQ4 = 8;                // 4-bit: pair-tiles of a block when there is more than one row group
 constexpr int kRawTile = kKeys * kQ4RowBytes;
 constexpr int kMaxRaw = 3;
 // The tensor core cuts its running sum off toward zero at each of the 36 steps of a score instead of rounding it: half
@@ -66,10 +65,12 @@ struct WeighArgs {
   int32_t shard_begin, n_held;
   int32_t B, q_len, H, R;       // R = q_len * H
   int32_t Rg, ngroups;          // columns a group, groups
-  int32_t stages;               // ring stages (bf16) or raw tiles (4-bit)
+  bool keys_held;               // the keys of a tile stay and the queries pass through the ring
+  int32_t stages;               // ring stages, or raw tiles (4-bit)
+  int32_t held_bytes, ring_bytes;  // of a held chunk, of a stage
   int32_t box_rows, nbox;       // rows a copy (min(P, 64)), copies a tile
   int32_t npairs;
-  int32_t block, block_last;    // pair-tiles of a block; a rest of up to block_last is one
+  int32_t block;                // most pair-tiles of a block
   int64_t pool_rows, pool_pages, max_rows;
   const unsigned char* arena;
   const int32_t* bt;
@@ -151,11 +152,11 @@ __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, volat
 
 // ---------------------------------------------------------------- barriers and shared memory
 enum : int {
-  kFull = 0,                            // key chunk in both CTAs (bf16; counted at the leader)
+  kFull = 0,                            // stage of the ring full in both CTAs (bf16; counted at the leader)
   kEmpty = kFull + kMaxStages,          // its products are done
-  kQFull = kEmpty + kMaxStages,         // query chunk in both CTAs (at the leader)
-  kQEmpty = kQFull + kChunks,
-  kSFull = kQEmpty + kChunks,           // scores of a tile
+  kHeldFull = kEmpty + kMaxStages,      // held chunk there in both CTAs (at the leader)
+  kHeldEmpty = kHeldFull + kChunks,
+  kSFull = kHeldEmpty + kChunks,        // scores of a tile
   kSFree = kSFull + 2,                  // read by the sums' warps of both CTAs (at the leader)
   kAFull = kSFree + 2,                  // 4-bit: operand slot written in both CTAs (at the leader)
   kAEmpty = kAFull + kASlots,
@@ -165,20 +166,43 @@ enum : int {
 };
 
 struct Smem {
-  uint32_t q, ring, bars, lse, acc, misc, total;
+  uint32_t held, ring, bars, lse, acc, misc, total;
 };
-// Queries (9 chunks of Rg / 2 rows), the ring, barriers, lse of the rows of two groups, a block's sums (4-bit), the rest.
-__host__ __device__ inline Smem smem_of(int Rg, int stages, int stage_bytes, bool q4) {
+// The held chunks, the ring, barriers, lse of the rows of two groups, a block's sums (4-bit), the rest.
+__host__ __device__ inline Smem smem_of(int held_bytes, int stages, int ring_bytes, bool q4) {
   Smem s;
-  s.q = 0;
-  s.ring = (uint32_t)kChunks * Rg / 2 * 128;
-  s.bars = s.ring + (uint32_t)stages * stage_bytes;
+  s.held = 0;
+  s.ring = (uint32_t)kChunks * held_bytes;
+  s.bars = s.ring + (uint32_t)stages * ring_bytes;
   s.lse = s.bars + (kNumBars * 8 + 15) / 16 * 16;
   s.acc = s.lse + 2 * 256 * 4;
   s.misc = s.acc + (q4 ? kBlockQ4 * kKeys * 4 : 0);
   s.total = s.misc + 128;
   return s;
 }
+
+// The slots that a role fills one after the other, held or of the ring.
+struct Slots {
+  uint64_t* empty;
+  uint32_t full;     // the leader's barriers, by cluster address
+  uint32_t at0, bytes, n;
+  uint32_t at = 0, ph = 0, uses = 0;
+  __device__ bool wait(volatile int* abort_s) const { return sleep_wait(empty + at, ph ^ 1, abort_s); }
+  __device__ uint32_t full_bar() const { return full + 8 * at; }
+  __device__ uint32_t dst() const { return at0 + at * bytes; }
+  __device__ void advance() {
+    ++uses;
+    if (++at == n) {
+      at = 0;
+      ph ^= 1;
+    }
+  }
+  // every slot's last release lands before the CTA may leave
+  __device__ void drain(volatile int* abort_s) const {
+    for (uint32_t s = 0; s < n && s < uses; ++s)
+      if (!sleep_wait(empty + s, ((uses - 1 - s) / n) & 1, abort_s)) return;
+  }
+};
 
 // ---------------------------------------------------------------- work
 // Rows of a request on the shards, from one division.
@@ -234,7 +258,7 @@ struct Walk {
   }
   __device__ void block(const WeighArgs& a) {
     nblk = min(left, npt - pt);
-    if (a.ngroups > 1 && nblk > a.block_last) nblk = a.block;
+    if (a.ngroups > 1) nblk = min(nblk, a.block);
     g = i = 0;
     rs0 = rs;
     t0 = t;
@@ -287,8 +311,10 @@ struct Walk {
     block(a);
     return true;
   }
-  __device__ bool first() const { return i == 0; }
-  __device__ bool last() const { return i == nblk - 1; }
+  __device__ bool group_begins() const { return i == 0; }
+  // the held operand is taken up with this tile and group, is done with after them
+  __device__ bool first(const WeighArgs& a) const { return a.keys_held ? g == 0 : i == 0; }
+  __device__ bool last(const WeighArgs& a) const { return a.keys_held ? g == a.ngroups - 1 : i == nblk - 1; }
 };
 
 // Where copy `box` of the walk's tile starts: its page id, loaded here and looked at later.
@@ -342,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     if (threadIdx.x == 0) flag(a.status, DCP_STATUS_INTERNAL);
     return;
   }
-  const Smem sl = smem_of(a.Rg, a.stages, kQ4 ? kRawTile : kStageBytes, kQ4);
+  const Smem sl = smem_of(a.held_bytes, a.stages, a.ring_bytes, kQ4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sl.bars);
   float* lse_s = reinterpret_cast<float*>(smem + sl.lse);
   float* acc_s = reinterpret_cast<float*>(smem + sl.acc);
@@ -362,8 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       mbar_init(&bars[kEmpty + i], 1);
     }
     for (int i = 0; i < kChunks; ++i) {
-      mbar_init(&bars[kQFull + i], 2);
-      mbar_init(&bars[kQEmpty + i], 1);
+      mbar_init(&bars[kHeldFull + i], 2);
+      mbar_init(&bars[kHeldEmpty + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[kSFull + i], 1);
@@ -438,120 +464,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   Walk w;
   const bool any = start_s[2] > 0;
   if (any && (!kQ4 || warp < kDequantWarp)) w.start(a, start_s[0], start_s[1], start_s[2], rank);
-  const uint32_t q_chunk = (uint32_t)a.Rg / 2 * 128;
+  auto slots_of = [&](bool held) -> Slots {
+    return held ? Slots{&bars[kHeldEmpty], lead + 8 * kHeldFull, smem_u32(smem) + sl.held, (uint32_t)a.held_bytes, kChunks}
+                : Slots{&bars[kEmpty], lead + 8 * kFull, smem_u32(smem) + sl.ring, (uint32_t)a.ring_bytes,
+                        (uint32_t)a.stages};
+  };
 
   if (warp == kKeyWarp && any) {
     // ------------------------------------------------------------------ keys in
     // A lane a copy; the next tile's page ids are on their way while this one's copies go out.
     if (lane == 0) prefetch_tmap(&tmap_kv);
     int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
-    uint32_t st = 0, ph = 0;
+    Slots slots = slots_of(a.keys_held);
+    if (kQ4) slots.empty = &bars[kRFree];
     bool ok = true, more = true;
-    uint32_t tiles = 0;
     while (more && ok) {
       const int32_t y = pool_row(a, w.rs, rho, page);
+      if (a.keys_held) w.g = a.ngroups - 1;  // the groups between meet the same keys
       more = w.next(a, rank);
       rho = more ? box_row(a, w, lane) : -1;
       page = page_of(a, w, rho);
       const uint32_t who = __ballot_sync(0xffffffffu, y >= 0);
       if (kQ4) {
-        ok = sleep_wait(&bars[kRFree + st], ph ^ 1, abort_s);
+        ok = slots.wait(abort_s);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull + st], __popc(who) * a.box_rows * kQ4RowBytes);
+        uint64_t* full = &bars[kRFull + slots.at];
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(who) * a.box_rows * kQ4RowBytes);
         __syncwarp();
         if (y >= 0)
-          bulk_load(smem + sl.ring + st * kRawTile + lane * a.box_rows * kQ4RowBytes, a.arena + (int64_t)y * kQ4RowBytes,
-                    a.box_rows * kQ4RowBytes, &bars[kRFull + st]);
-        if (++st == (uint32_t)a.stages) {
-          st = 0;
-          ph ^= 1;
-        }
+          bulk_load(smem + sl.ring + slots.at * kRawTile + lane * a.box_rows * kQ4RowBytes,
+                    a.arena + (int64_t)y * kQ4RowBytes, a.box_rows * kQ4RowBytes, full);
+        slots.advance();
       } else {
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = sleep_wait(&bars[kEmpty + st], ph ^ 1, abort_s);
+          ok = slots.wait(abort_s);
           if (!ok) break;
-          const uint32_t full = lead + 8 * (kFull + st);
-          if (lane == 0) expect_tx_cluster(full, __popc(who) * a.box_rows * 128);
+          if (lane == 0) expect_tx_cluster(slots.full_bar(), __popc(who) * a.box_rows * 128);
           __syncwarp();
           if (y >= 0)
-            tma_load_2d_pair(smem_u32(smem) + sl.ring + st * kStageBytes + lane * a.box_rows * 128, &tmap_kv, full,
-                             c * kChunkDims, y);
-          if (++st == (uint32_t)a.stages) {
-            st = 0;
-            ph ^= 1;
-          }
+            tma_load_2d_pair(slots.dst() + lane * a.box_rows * 128, &tmap_kv, slots.full_bar(), c * kChunkDims, y);
+          slots.advance();
         }
       }
-      ++tiles;
     }
-    // every slot's last release lands before the CTA may leave
-    if (ok) {
-      const uint32_t uses = kQ4 ? tiles : tiles * kChunks;
-      for (uint32_t s = 0; s < (uint32_t)a.stages && s < uses; ++s) {
-        const uint32_t n = (uses - 1 - s) / a.stages;  // its last use
-        if (!sleep_wait(&bars[(kQ4 ? kRFree : kEmpty) + s], n & 1, abort_s)) break;
-      }
-    }
+    if (ok) slots.drain(abort_s);
   } else if (warp == kQueryWarp && any) {
     // ------------------------------------------------------------------ queries in
     if (lane == 0) prefetch_tmap(&tmap_q);
-    uint32_t ph = 0;
+    Slots slots = slots_of(!a.keys_held);
     bool ok = true, more = true;
     while (more && ok) {
-      if (w.first()) {
+      if (w.group_begins()) {
         const int32_t y = w.b * a.R + w.g * a.Rg + rank * (a.Rg / 2);
         for (int c = 0; c < kChunks && ok; ++c) {
-          ok = sleep_wait(&bars[kQEmpty + c], ph ^ 1, abort_s);
-          if (ok && lane == 0) {
-            expect_tx_cluster(lead + 8 * (kQFull + c), q_chunk);
-            tma_load_2d_pair(smem_u32(smem) + sl.q + c * q_chunk, &tmap_q, lead + 8 * (kQFull + c), c * kChunkDims, y);
+          ok = slots.wait(abort_s);
+          if (!ok) break;
+          if (lane == 0) {
+            expect_tx_cluster(slots.full_bar(), a.Rg / 2 * 128);
+            tma_load_2d_pair(slots.dst(), &tmap_q, slots.full_bar(), c * kChunkDims, y);
           }
+          slots.advance();
         }
-        ph ^= 1;
       }
       more = w.next(a, rank);
     }
-    for (int c = 0; c < kChunks && ok; ++c) ok = sleep_wait(&bars[kQEmpty + c], ph ^ 1, abort_s);
+    if (ok) slots.drain(abort_s);
   } else if (warp == kMmaWarp && any && rank == 0) {
     // ------------------------------------------------------------------ products (the leader's alone)
     // The whole warp walks and waits, one lane issues: the operands' descriptors are then uniform values.  (With one
     // lane in a loop of its own each product's came through vector registers, 760 cycles a chunk in all.)
     const bool one = elect_one();
     const uint32_t idesc = idesc_bf16_f32(2 * kKeys, a.Rg, 0, 0);
-    const uint64_t kdesc = sw128_desc(smem_u32(smem) + sl.ring, 16, 1024);
-    const uint64_t qdesc = sw128_desc(smem_u32(smem) + sl.q, 16, 1024);
+    const uint64_t held0 = sw128_desc(smem_u32(smem) + sl.held, 16, 1024);
+    const uint64_t ring0 = sw128_desc(smem_u32(smem) + sl.ring, 16, 1024);
+    const uint32_t held_step = (uint32_t)a.held_bytes >> 4, ring_step = (uint32_t)a.ring_bytes >> 4;
     const uint32_t slots = kQ4 ? kASlots : a.stages;
-    uint32_t st = 0, ph = 0, qph = 0, j = 0;
+    uint32_t st = 0, ph = 0, hph = 0, j = 0;
     bool ok = true, more = true;
     while (more && ok) {
-      const bool first = w.first(), last = w.last();
+      const bool first = w.first(a), last = w.last(a);
       const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
       ok = sleep_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
       for (int c = 0; c < (kQ4 ? kAParts : kChunks) && ok; ++c) {
-        const int q0 = kQ4 ? 2 * c : c, nq = kQ4 && c < kAParts - 1 ? 2 : 1;  // query chunks of this step
+        const int h0 = kQ4 ? 2 * c : c, nh = kQ4 && c < kAParts - 1 ? 2 : 1;  // held chunks of this step
         if (first)
-          for (int i = 0; i < nq; ++i) ok = ok && sleep_wait(&bars[kQFull + q0 + i], qph, abort_s);
+          for (int i = 0; i < nh; ++i) ok = ok && sleep_wait(&bars[kHeldFull + h0 + i], hph, abort_s);
         ok = ok && sleep_wait(&bars[(kQ4 ? kAFull : kFull) + st], ph, abort_s);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t qd = qdesc + q0 * (q_chunk >> 4), kd = kdesc + st * (kStageBytes >> 4);
+        const uint64_t hd = held0 + h0 * held_step, rd = ring0 + st * ring_step;
+        const uint64_t qd = a.keys_held ? rd : hd, kd = a.keys_held ? hd : rd;
         const uint32_t kt = tmem + kACol + 64 * st;
         if (one) {
 #pragma unroll
           for (int k = 0; k < kChunkDims / 16; ++k) {
             if (kQ4)
-              mma_pair_ts(d, kt + 8 * k, qd + 2 * k, idesc, (c | k) != 0);
+              mma_pair_ts(d, kt + 8 * k, hd + 2 * k, idesc, (c | k) != 0);
             else
               mma_pair_ss(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
           }
-          if (kQ4 && nq == 2) {
+          if (kQ4 && nh == 2) {
 #pragma unroll
-            for (int k = 0; k < kChunkDims / 16; ++k) mma_pair_ts(d, kt + 32 + 8 * k, qd + (q_chunk >> 4) + 2 * k, idesc, 1);
+            for (int k = 0; k < kChunkDims / 16; ++k) mma_pair_ts(d, kt + 32 + 8 * k, hd + held_step + 2 * k, idesc, 1);
           }
           commit_pair(&bars[(kQ4 ? kAEmpty : kEmpty) + st]);
           if (last)
-            for (int i = 0; i < nq; ++i) commit_pair(&bars[kQEmpty + q0 + i]);
-          if (q0 == kChunks - 1) commit_pair(&bars[kSFull + buf]);
+            for (int i = 0; i < nh; ++i) commit_pair(&bars[kHeldEmpty + h0 + i]);
+          if (h0 == kChunks - 1) commit_pair(&bars[kSFull + buf]);
         }
         __syncwarp();
         if (++st == slots) {
@@ -560,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         }
       }
       if (!ok) break;
-      if (first) qph ^= 1;
+      if (first) hph ^= 1;
       ++j;
       more = w.next(a, rank);
     }
@@ -584,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       Key k;
       k.ncols = min(a.Rg, a.R - w.g * a.Rg);
       k.i = w.i;
-      k.lse_at = w.first() ? (int64_t)w.b * a.R + w.g * a.Rg : -1;
+      k.lse_at = w.group_begins() ? (int64_t)w.b * a.R + w.g * a.Rg : -1;
       k.add = w.g > 0;
       k.wp = nullptr;
       k.old = 0.f;
@@ -612,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     };
     bool ok = true, more = true;
     uint32_t j = 0;
-    float part[kBlockLast] = {0.f, 0.f, 0.f, 0.f};  // sums over the groups so far, by pair-tile of the block
+    float part = 0.f;  // a tile's sum over the groups so far (4-bit: in acc_s, by tile of the block)
     Key key = look();
     while (more && ok) {
       const Key now = key;
@@ -677,18 +696,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       f2_unpack(f2_add(sum[0], sum[1]), x0, x1);
       float s = __uint_as_float(x0) + __uint_as_float(x1);
       if (a.ngroups > 1) {
-        if (kQ4) {  // this thread's own entry
-          float* acc = acc_s + now.i * kKeys + warp * 32 + lane;
-          if (now.add) s += *acc;
-          *acc = s;
-        } else {
-#pragma unroll
-          for (int k = 0; k < kBlockLast; ++k)
-            if (now.i == k) {
-              if (now.add) s += part[k];
-              part[k] = s;
-            }
-        }
+        float* acc = kQ4 ? acc_s + now.i * kKeys + warp * 32 + lane : &part;  // this thread's own
+        if (now.add) s += *acc;
+        *acc = s;
       }
       if (now.wp && now.page >= 0 && now.page < a.pool_pages) *now.wp = a.decay * now.old + s;
       ++j;
@@ -810,12 +820,14 @@ int32_t weigh(const WeighCall& c) {
   const int groups = (a.R + most - 1) / most;
   a.Rg = ((a.R + groups - 1) / groups + 31) / 32 * 32;
   a.ngroups = (a.R + a.Rg - 1) / a.Rg;
-  const int stage_bytes = kQ4 ? kRawTile : kStageBytes, most_stages = kQ4 ? kMaxRaw : kMaxStages;
-  a.stages = (int32_t)(kSmemBudget - smem_of(a.Rg, 0, 0, kQ4).total) / stage_bytes;
-  a.stages = std::min(a.stages, (int32_t)most_stages);
-  const size_t smem = smem_of(a.Rg, a.stages, stage_bytes, kQ4).total;
-  a.block = kQ4 ? kBlockQ4 : kBlock;
-  a.block_last = kQ4 ? kBlockQ4 : kBlockLast;
+  a.keys_held = !kQ4 && a.ngroups > 1;
+  const int q_chunk = a.Rg / 2 * 128;
+  a.held_bytes = a.keys_held ? kStageBytes : q_chunk;
+  a.ring_bytes = kQ4 ? kRawTile : a.keys_held ? q_chunk : kStageBytes;
+  a.stages = (int32_t)(kSmemBudget - smem_of(a.held_bytes, 0, 0, kQ4).total) / a.ring_bytes;
+  a.stages = std::min(a.stages, kQ4 ? kMaxRaw : kMaxStages);
+  const size_t smem = smem_of(a.held_bytes, a.stages, a.ring_bytes, kQ4).total;
+  a.block = kQ4 ? kBlockQ4 : 1;
   a.box_rows = std::min(c.layout->page_size, kTile);
   a.nbox = kKeys / a.box_rows;
   PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
