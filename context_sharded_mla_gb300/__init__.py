@@ -14,8 +14,8 @@ Functions (same names as the C ABI):
   dcp_lse_merge_packed, dcp_lse_rescale, dcp_kv_append_q4, dcp_kv_relayout_q4,
   dcp_kv_read_q4, dcp_mla_decode_partial_q4, dcp_mla_decode_workspace_size_q4,
   dcp_block_tables, dcp_q_norm_rope, dcp_kv_norm_rope_append, dcp_kv_norm_rope_append_q4,
-  dcp_mla_key_weights, dcp_mla_key_weights_q4, dcp_evict_select, dcp_kv_compact,
-  dcp_kv_compact_q4
+  dcp_mla_key_weights, dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size,
+  dcp_mla_key_weights_workspace_size_q4, dcp_evict_select, dcp_kv_compact, dcp_kv_compact_q4
 """
 
 from __future__ import annotations
@@ -36,7 +36,8 @@ __all__ = [
     "dcp_kv_append_q4", "dcp_kv_relayout_q4", "dcp_kv_read_q4", "dcp_mla_decode_partial_q4",
     "dcp_mla_decode_workspace_size_q4", "dcp_block_tables", "Q4_ROW_BYTES",
     "dcp_q_norm_rope", "dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4", "dcp_mla_key_weights",
-    "dcp_mla_key_weights_q4", "dcp_evict_select", "dcp_kv_compact", "dcp_kv_compact_q4",
+    "dcp_mla_key_weights_q4", "dcp_mla_key_weights_workspace_size", "dcp_mla_key_weights_workspace_size_q4",
+    "dcp_evict_select", "dcp_kv_compact", "dcp_kv_compact_q4",
     "DCP_LSE_BASE_E", "DCP_LSE_BASE_2", "DCP_F32", "DCP_BF16", "DCP_ROPE_PAIRS", "DCP_ROPE_HALVES", "STATUS_BITS",
 ]
 
@@ -109,7 +110,9 @@ for _name in ("dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4"):
                                  _I64, _P, _I64, _P, _P])
 for _name in ("dcp_mla_key_weights", "dcp_mla_key_weights_q4"):
     _SIGNATURES[_name] = (_I32, [_LP, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _P, _I64, _I64, _P, _F, _I32, _P,
-                                 _P, _F, _P, _I64, _P, _P])
+                                 _P, _F, _P, _I64, _P, _SZ, _P, _P])
+for _name in ("dcp_mla_key_weights_workspace_size", "dcp_mla_key_weights_workspace_size_q4"):
+    _SIGNATURES[_name] = (_SZ, [_I32, _I32])
 for _name in ("dcp_kv_compact", "dcp_kv_compact_q4"):
     _SIGNATURES[_name] = (_I32, [_LP, _I32, _I32, _P, _I64, _I32, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P])
 
@@ -688,9 +691,17 @@ dcp_kv_norm_rope_append_q4 = _norm_rope_append(
     """dcp_kv_norm_rope_append into a 4-bit arena [shards, pool_pages*P, 416] uint8.""")
 
 
-def _key_weights(name, width, dtype, doc):
+def dcp_mla_key_weights_workspace_size(q_len, H) -> int:
+    return int(load_library().dcp_mla_key_weights_workspace_size(q_len, H))
+
+
+def dcp_mla_key_weights_workspace_size_q4(q_len, H) -> int:
+    return int(load_library().dcp_mla_key_weights_workspace_size_q4(q_len, H))
+
+
+def _key_weights(name, width, dtype, size, few, doc):
     def call(layout, shard_begin, shard_end, q, arena, pool_pages, block_table, max_pages, seq_lens, scale, lse_base, lse,
-             weights, status, old_lens=None, decay=1.0, stream=None):
+             weights, status, old_lens=None, decay=1.0, workspace=None, stream=None):
         dev = torch.cuda.current_device()
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be [B, q_len, H, 576]")
@@ -699,6 +710,15 @@ def _key_weights(name, width, dtype, doc):
         rows, stride = _table(block_table, "block_table")
         if rows != B:
             raise ValueError("block_table must have one row per request")
+        if workspace is None and q_len * H > few and q.is_cuda:
+            if stream is None:
+                workspace = torch.empty(size(q_len, H), dtype=torch.uint8, device=dev)
+            else:  # of that stream's scratch, which goes back in its order
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(size(q_len, H), dtype=torch.uint8, device=dev)
+        at_ws, ws_bytes = None, 0
+        if workspace is not None:
+            at_ws, ws_bytes = _at(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
         rc = getattr(load_library(), name)(
             layout, shard_begin, shard_end, _at(q, "q", torch.bfloat16, (B, q_len, H, 576), dev), B, q_len, H,
             _at(arena, "arena", dtype, (n, pool_pages * layout.page_size, width), dev), pool_pages,
@@ -707,7 +727,7 @@ def _key_weights(name, width, dtype, doc):
             _at(lse, "lse", torch.float32, (B, q_len, H), dev),
             None if old_lens is None else _at(old_lens, "old_lens", torch.int64, (B,), dev), decay,
             _at(weights, "weights", torch.float32, (n, B, _unit_rows(weights, "weights")), dev), weights.shape[2],
-            _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
+            at_ws, ws_bytes, _at(status, "status", torch.int32, (1,), dev), _raw_stream(stream, dev))
         if rc:
             _check(name, rc)
 
@@ -724,12 +744,13 @@ def _unit_rows(t, name):
 
 
 dcp_mla_key_weights = _key_weights(
-    "dcp_mla_key_weights", 576, torch.bfloat16,
+    "dcp_mla_key_weights", 576, torch.bfloat16, dcp_mla_key_weights_workspace_size, 1024,
     """weights [shards, B, >= max_pages * P] f32: to every cached row the softmax weight that the queries q [B, q_len, H,
     576] give it under their merged lse [B, q_len, H], summed over them, is added; rows at positions below old_lens (int64
-    [B]; None: 0) keep decay times what they had, the others start from 0.""")
+    [B]; None: 0) keep decay times what they had, the others start from 0.  workspace: uint8 of
+    dcp_mla_key_weights_workspace_size(q_len, H) bytes; None: allocated for the call.""")
 dcp_mla_key_weights_q4 = _key_weights(
-    "dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8,
+    "dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8, dcp_mla_key_weights_workspace_size_q4, 512,
     """dcp_mla_key_weights over a 4-bit arena [shards, pool_pages*P, 416] uint8.""")
 
 

@@ -17,20 +17,25 @@
 // through a ring of 16-KB chunks (128 keys x 64 dims); the chunks of a tile are consumed
 // in order, so a product starts when its first chunk is there.
 //
-// More than 256 rows: groups of at most 256, one after the other over a block of pair-tiles
-// that the later groups find in L2, each chunk of the queries replaced as soon as the last
-// product with it is done.  Blocks of two pair-tiles (0.6 MB a pair of SMs, 45 MB over the
-// card), the last up to four of a run as one: 4 requests of 128k tokens with 64 queries of
-// 96 heads take 2091 us, with blocks of four 2309, of eight 2646, of one 2132.  4-bit:
-// blocks of eight (65 MB): 871 us where four take 931 and sixteen 891.
+// More than 256 rows: groups of at most 256, one after the other.  The nine chunks of a
+// tile's keys then stay, each replaced when the last group is done with it, and the queries
+// (which the L2 holds) pass through the ring: 4 requests of 128k tokens with 64 queries of
+// 96 heads take 1950-1985 us.  With the queries held over blocks of tiles that later groups
+// find in the L2 2067 at best (two pair-tiles; 2309 with four, 2132 with one).
 //
 // The 4-bit cache: 416-byte rows land raw, eight warps turn them (a lane a key, 128 dims at
 // a time) into bf16 operands and write them to TMEM, where the product takes its A operand
-// from (lanes are keys there too); no dequantised tile is stored.  Groups of 128 rows.
+// from (lanes are keys there too); no dequantised tile is stored.  Groups of 128 rows; the
+// queries are held, over blocks of eight pair-tiles (65 MB over the card, for the L2): 32
+// requests of 32k tokens with 8 queries of 128 heads take 871 us, with four 931, sixteen 891.
 //
 // Work: the pair-tiles (2 x 128 rows of one request) of all requests in a row, cut into as
 // many equal runs as there are pairs.  A run's start is found from the lengths by every
 // CTA for itself (a block-wide scan, 1 us), so the call is one launch with no workspace.
+// Many query rows over few tiles are cut between row groups as well: the pair that begins
+// a tile writes its weights, the others leave their sums in a workspace and a second
+// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 250 us,
+// 61 of 128 over 8k 113 -> 60, 4-bit 32 of 128 over 4k 101 -> 36.
 #include "dcp_decode.cuh"
 
 namespace {
@@ -71,6 +76,10 @@ struct WeighArgs {
   int32_t box_rows, nbox;       // rows a copy (min(P, 64)), copies a tile
   int32_t npairs;
   int32_t block;                // most pair-tiles of a block
+  // what pairs add to a tile that another pair has begun (null: no tile is shared)
+  int64_t* units;               // units of the call
+  int64_t* part_at;             // [pairs, 256] entry of weights, -1: none
+  float* part;                  // [pairs, 256]
   int64_t pool_rows, pool_pages, max_rows;
   const unsigned char* arena;
   const int32_t* bt;
@@ -233,10 +242,15 @@ struct Shape {
   }
 };
 
+// Where pair p's units (pair-tile, row group) begin.
+__device__ __forceinline__ int64_t run_start(int64_t units, int p, int npairs) { return units * p / npairs; }
+
 // A pair's run, tile by tile: blocks of pair-tiles of one request, and in a block every row
 // group in turn.  Each role of a CTA walks it for itself.
 struct Walk {
   int32_t b, left;           // request; pair-tiles left, this block's included
+  int32_t g0, g1;            // row groups of the block (all but for a tile shared with another pair)
+  int32_t g_last;            // groups of the run's last tile
   int32_t pt, npt;           // block's first pair-tile, pair-tiles of the request
   int32_t nblk, g, i;        // pair-tiles of the block, row group, pair-tile within the block
   int32_t rs, t, rows, nt;   // this CTA's tile: shard (n_held: none), tile of it; the shard's rows and tiles
@@ -256,10 +270,19 @@ struct Walk {
       shard(a, rs + 1);
     }
   }
-  __device__ void block(const WeighArgs& a) {
+  __device__ void block(const WeighArgs& a, int32_t g_first = 0) {
     nblk = min(left, npt - pt);
-    if (a.ngroups > 1) nblk = min(nblk, a.block);
-    g = i = 0;
+    g0 = g_first;
+    g1 = a.ngroups;
+    if (a.ngroups > 1) {
+      nblk = g0 > 0 ? 1 : min(nblk, a.block);
+      if (nblk == left && g_last < a.ngroups) {  // the last tile by itself
+        if (nblk > 1) --nblk;
+        else g1 = g_last;
+      }
+    }
+    g = g0;
+    i = 0;
     rs0 = rs;
     t0 = t;
     rows0 = rows;
@@ -270,15 +293,17 @@ struct Walk {
     npt = sh.pair_tiles(a);
     S_next = b + 1 < a.B ? __ldg(a.seq_lens + b + 1) : 0;
   }
-  __device__ void start(const WeighArgs& a, int32_t b_, int32_t pt_, int32_t n, int rank) {
+  __device__ void start(const WeighArgs& a, int32_t b_, int32_t pt_, int32_t n, int32_t g_first, int32_t g_last_,
+                        int rank) {
     left = n;
+    g_last = g_last_;
     b = b_;
     pt = pt_;
     request(a, __ldg(a.seq_lens + b));
     t = 0;
     shard(a, 0);
     advance(a, 2 * pt + rank);
-    block(a);
+    block(a, g_first);
   }
   __device__ bool next(const WeighArgs& a, int rank) {
     if (++i < nblk) {
@@ -286,7 +311,7 @@ struct Walk {
       return true;
     }
     i = 0;
-    if (++g < a.ngroups) {
+    if (++g < g1) {
       rs = rs0;
       t = t0;
       rows = rows0;
@@ -313,8 +338,8 @@ struct Walk {
   }
   __device__ bool group_begins() const { return i == 0; }
   // the held operand is taken up with this tile and group, is done with after them
-  __device__ bool first(const WeighArgs& a) const { return a.keys_held ? g == 0 : i == 0; }
-  __device__ bool last(const WeighArgs& a) const { return a.keys_held ? g == a.ngroups - 1 : i == nblk - 1; }
+  __device__ bool first(const WeighArgs& a) const { return a.keys_held ? g == g0 : i == 0; }
+  __device__ bool last(const WeighArgs& a) const { return a.keys_held ? g == g1 - 1 : i == nblk - 1; }
 };
 
 // Where copy `box` of the walk's tile starts: its page id, loaded here and looked at later.
@@ -374,7 +399,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   float* acc_s = reinterpret_cast<float*>(smem + sl.acc);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(smem + sl.misc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + sl.misc + 4);
-  int32_t* start_s = reinterpret_cast<int32_t*>(smem + sl.misc + 8);       // request, pair-tile, pair-tiles of the run
+  // request, pair-tile, pair-tiles of the run (met in part too), first group of the first, groups of the last, units
+  int32_t* start_s = reinterpret_cast<int32_t*>(smem + sl.misc + 8);
   int32_t* warp_sums = reinterpret_cast<int32_t*>(smem + sl.misc + 32);
   static_assert(32 + 4 * kWarps <= 128, "room for them");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -441,8 +467,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       if (w < warp) before += warp_sums[w];
       total += warp_sums[w];
     }
-    const int32_t lo = (int32_t)((int64_t)total * pair / a.npairs), hi = (int32_t)((int64_t)total * (pair + 1) / a.npairs);
-    if (lo < hi && before <= lo && lo < before + mine) {
+    // the run in units; its tiles and where in the first and last of them it begins and ends
+    // Tiles are shared where whole ones would leave a pair 1/16 more than its part.  (4-bit: 5/16 of two tiles and more;
+    // the tiles of a shared run are blocks of one, 2.7 us a group where blocks of four take 2.1.)
+    const int32_t G = a.ngroups, most = (total + a.npairs - 1) / a.npairs;
+    const bool share =
+        a.part && 16 * ((int64_t)most * a.npairs - total) > (kQ4 && most > 1 ? 5 : 1) * (int64_t)total;
+    const int32_t per_tile = share ? G : 1;
+    const int64_t u0 = run_start((int64_t)total * per_tile, pair, a.npairs);
+    const int64_t u1 = run_start((int64_t)total * per_tile, pair + 1, a.npairs);
+    if (a.part && blockIdx.x == 0 && tid == 0) *a.units = share ? (int64_t)total * G : 0;
+    const int32_t lo = (int32_t)(per_tile == 1 ? u0 : u0 / G);
+    if (u0 < u1 && before <= lo && lo < before + mine) {
       int32_t b = b0, x = lo - before;
       for (; b < b1; ++b) {
         Shape sh;
@@ -451,9 +487,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         if (x < n) break;
         x -= n;
       }
+      const int32_t hi = (int32_t)(per_tile == 1 ? u1 : (u1 + G - 1) / G);  // tile after the last
       start_s[0] = b;
       start_s[1] = x;
       start_s[2] = hi - lo;
+      start_s[3] = per_tile == 1 ? 0 : (int32_t)(u0 - (int64_t)lo * G);
+      start_s[4] = per_tile == 1 ? G : (int32_t)(u1 - (int64_t)(hi - 1) * G);
+      start_s[5] = per_tile == 1 ? (hi - lo) * G : (int32_t)(u1 - u0);
     }
   }
   tc_fence_before();
@@ -463,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   const uint32_t lead = mapa_shared(smem_u32(bars), 0);  // the leader's barriers
   Walk w;
   const bool any = start_s[2] > 0;
-  if (any && (!kQ4 || warp < kDequantWarp)) w.start(a, start_s[0], start_s[1], start_s[2], rank);
+  if (any && (!kQ4 || warp < kDequantWarp)) w.start(a, start_s[0], start_s[1], start_s[2], start_s[3], start_s[4], rank);
   auto slots_of = [&](bool held) -> Slots {
     return held ? Slots{&bars[kHeldEmpty], lead + 8 * kHeldFull, smem_u32(smem) + sl.held, (uint32_t)a.held_bytes, kChunks}
                 : Slots{&bars[kEmpty], lead + 8 * kFull, smem_u32(smem) + sl.ring, (uint32_t)a.ring_bytes,
@@ -480,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     bool ok = true, more = true;
     while (more && ok) {
       const int32_t y = pool_row(a, w.rs, rho, page);
-      if (a.keys_held) w.g = a.ngroups - 1;  // the groups between meet the same keys
+      if (a.keys_held) w.g = w.g1 - 1;  // the groups between meet the same keys
       more = w.next(a, rank);
       rho = more ? box_row(a, w, lane) : -1;
       page = page_of(a, w, rho);
@@ -589,12 +629,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     const float c = a.scale_log2;
     const uint64_t c2 = f2_pack(__float_as_uint(c), __float_as_uint(c));
     struct Key {
-      float* wp;          // its weight, null: not written
+      int64_t at;         // its entry of weights, -1: not written
       float old;
       int32_t page, col0; // first column of the group that sees it
       int32_t ncols, i;   // columns of the group, pair-tile of the block
       int64_t lse_at;     // the group's first row, -1: as before
       bool add;           // to the groups' sum so far
+      bool joins;         // the tile's last group here, and another pair has begun it
     };
     const bool keeps = a.old_lens && a.decay != 0.f;
     int32_t old_b = -1;
@@ -604,8 +645,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       k.ncols = min(a.Rg, a.R - w.g * a.Rg);
       k.i = w.i;
       k.lse_at = w.group_begins() ? (int64_t)w.b * a.R + w.g * a.Rg : -1;
-      k.add = w.g > 0;
-      k.wp = nullptr;
+      k.add = w.g > w.g0;
+      k.joins = w.g0 > 0 && w.g == w.g1 - 1;
+      k.at = -1;
       k.old = 0.f;
       k.page = k.col0 = 0;
       if (keeps && w.b != old_b) {
@@ -621,10 +663,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
           const int64_t x = hidden * a.H - (int64_t)w.g * a.Rg;
           k.col0 = (int32_t)(x < 0 ? 0 : (x > a.Rg ? a.Rg : x));
         }
-        if (w.g == a.ngroups - 1) {
+        if (w.g == w.g1 - 1) {
           k.page = __ldg(a.bt + (int64_t)w.b * a.bt_stride + row / (int32_t)a.L.P);
-          k.wp = a.weights + ((int64_t)w.rs * a.B + w.b) * a.w_stride + row;
-          if (keeps && p < old_len) k.old = *k.wp;
+          k.at = ((int64_t)w.rs * a.B + w.b) * a.w_stride + row;
+          if (keeps && p < old_len && w.g0 == 0) k.old = a.weights[k.at];
         }
       }
       return k;
@@ -700,7 +742,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         if (now.add) s += *acc;
         *acc = s;
       }
-      if (now.wp && now.page >= 0 && now.page < a.pool_pages) *now.wp = a.decay * now.old + s;
+      const bool there = now.at >= 0 && now.page >= 0 && now.page < a.pool_pages;
+      if (now.joins) {
+        const int32_t k = pair * 2 * kKeys + rank * kKeys + warp * 32 + lane;
+        a.part_at[k] = there ? now.at : -1;
+        a.part[k] = s;
+      } else if (there) {
+        a.weights[now.at] = a.decay * now.old + s;
+      }
       ++j;
     }
   } else if (kQ4 && warp >= kDequantWarp && any) {
@@ -709,7 +758,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     // once a row group; a CTA without a tile in the last of a request turns over what its slot holds, for nobody.
     const int set = (warp - kDequantWarp) >> 2, quarter = warp & 3;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kACol;
-    const uint32_t tiles = (uint32_t)start_s[2] * a.ngroups;
+    const uint32_t tiles = (uint32_t)start_s[5];
     uint32_t rb = 0, rph = 0;  // raw tile and its parity
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
@@ -773,6 +822,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kAllCols) : "memory");
 }
 
+// What the pairs after the first have of a tile that several share, added to what the first has written: a block a
+// boundary between two runs, a thread a key, the pairs in order.
+__global__ void __launch_bounds__(2 * kKeys) join_kernel(WeighArgs a) {
+  const int p = blockIdx.x + 1;
+  const int64_t units = *a.units;  // 0: nothing is shared
+  const int64_t u = run_start(units, p, a.npairs), tile = u - u % a.ngroups;
+  if (u == tile || run_start(units, p - 1, a.npairs) > tile) return;  // not the first boundary within a tile
+  int64_t at = -1, k0 = u;
+  float s = 0.f;
+  for (int k = p; k < a.npairs && k0 < tile + a.ngroups; ++k) {
+    const int64_t k1 = run_start(units, k + 1, a.npairs);
+    if (k1 > k0) {
+      at = a.part_at[k * 2 * kKeys + threadIdx.x];
+      s += a.part[k * 2 * kKeys + threadIdx.x];
+    }
+    k0 = k1;
+  }
+  if (at >= 0 && at < a.w_stride * a.B * a.n_held) a.weights[at] += s;  // (after a timeout it may be anything)
+}
+
+constexpr int kMaxPairs = 128;
+// Tiles are shared from this many row groups on.  A whole tile is then 15 us of a pair's products and more; the second
+// launch and its scratch cost 3 us, 10 on the host.
+constexpr int kShareGroups = 4;
+constexpr size_t kUnitsBytes = 128, kPartAtBytes = (size_t)kMaxPairs * 2 * kKeys * sizeof(int64_t),
+                 kPartBytes = (size_t)kMaxPairs * 2 * kKeys * sizeof(float);
+size_t workspace_size(int64_t R, bool q4) {
+  return R > kShareGroups * (q4 ? 128 : 256) ? kUnitsBytes + kPartAtBytes + kPartBytes : 0;
+}
+
 PairKernel g_bf16(reinterpret_cast<const void*>(&weigh_kernel<false>), kThreads);
 PairKernel g_q4(reinterpret_cast<const void*>(&weigh_kernel<true>), kThreadsQ4);
 
@@ -793,6 +872,8 @@ struct WeighCall {
   float decay;
   float* weights;
   int64_t w_stride;
+  void* workspace;
+  size_t workspace_bytes;
   int32_t* status;
   void* stream;
 };
@@ -807,6 +888,8 @@ int32_t weigh(const WeighCall& c) {
   if (rc != DCP_OK) return rc;
   if (!c.lse || !(c.decay >= 0.f) || !(c.decay < INFINITY) || c.w_stride / c.layout->page_size < c.max_pages)
     return DCP_ERR_INVALID;
+  if ((uintptr_t)c.workspace % 16 != 0) return DCP_ERR_INVALID;
+  if (c.workspace && c.workspace_bytes < workspace_size((int64_t)c.q_len * c.H, kQ4)) return DCP_ERR_WORKSPACE;
   WeighArgs a;
   a.L = to_layout(c.layout);
   a.shard_begin = c.shard_begin;
@@ -831,7 +914,7 @@ int32_t weigh(const WeighCall& c) {
   a.box_rows = std::min(c.layout->page_size, kTile);
   a.nbox = kKeys / a.box_rows;
   PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
-  a.npairs = kernel.max_active_clusters(smem);
+  a.npairs = std::min(kernel.max_active_clusters(smem), kMaxPairs);
   if (a.npairs < 1) return DCP_ERR_CUDA;
   a.pool_pages = c.pool_pages;
   a.pool_rows = c.pool_pages * c.layout->page_size;
@@ -849,6 +932,10 @@ int32_t weigh(const WeighCall& c) {
   a.weights = c.weights;
   a.w_stride = c.w_stride;
   a.status = c.status;
+  unsigned char* ws = workspace_size(a.R, kQ4) > 0 ? static_cast<unsigned char*>(c.workspace) : nullptr;
+  a.units = reinterpret_cast<int64_t*>(ws);
+  a.part_at = reinterpret_cast<int64_t*>(ws ? ws + kUnitsBytes : nullptr);
+  a.part = reinterpret_cast<float*>(ws ? ws + kUnitsBytes + kPartAtBytes : nullptr);
   CUtensorMap tq, tkv;
   if (!make_tmap(&tq, c.q, (uint64_t)c.B * a.R, (uint32_t)a.Rg / 2)) return DCP_ERR_CUDA;
   if (kQ4)
@@ -857,7 +944,9 @@ int32_t weigh(const WeighCall& c) {
     return DCP_ERR_CUDA;
   if (!kernel.ensure_smem(smem)) return DCP_ERR_CUDA;
   weigh_kernel<kQ4><<<2 * a.npairs, kQ4 ? kThreadsQ4 : kThreads, smem, as_stream(c.stream)>>>(tq, tkv, a);
-  return launch_status();
+  if (!ws || a.npairs == 1) return launch_status();
+  join_kernel<<<a.npairs - 1, 2 * kKeys, 0, as_stream(c.stream)>>>(a);
+  return launch_status(2);
 }
 
 }  // namespace
@@ -867,10 +956,10 @@ extern "C" int32_t dcp_mla_key_weights(const dcp_layout_t* layout, int32_t shard
                                        const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
                                        const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
                                        const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
-                                       int32_t* status, void* stream) {
+                                       void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
   return weigh<false>(WeighCall{layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
-                                max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, status,
-                                stream});
+                                max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, workspace,
+                                workspace_bytes, status, stream});
 }
 
 extern "C" int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end,
@@ -878,8 +967,17 @@ extern "C" int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t sh
                                           int64_t pool_pages, const int32_t* block_table, int64_t bt_stride,
                                           int64_t max_pages, const int64_t* seq_lens, float scale, int32_t lse_base,
                                           const float* lse, const int64_t* old_lens, float decay, float* weights,
-                                          int64_t w_stride, int32_t* status, void* stream) {
+                                          int64_t w_stride, void* workspace, size_t workspace_bytes, int32_t* status,
+                                          void* stream) {
   return weigh<true>(WeighCall{layout, shard_begin, shard_end, q, B, q_len, H, arena, pool_pages, block_table, bt_stride,
-                               max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, status,
-                               stream});
+                               max_pages, seq_lens, scale, lse_base, lse, old_lens, decay, weights, w_stride, workspace,
+                               workspace_bytes, status, stream});
+}
+
+extern "C" size_t dcp_mla_key_weights_workspace_size(int32_t q_len, int32_t H) {
+  return q_len > 0 && H > 0 ? workspace_size((int64_t)q_len * H, false) : 0;
+}
+
+extern "C" size_t dcp_mla_key_weights_workspace_size_q4(int32_t q_len, int32_t H) {
+  return q_len > 0 && H > 0 ? workspace_size((int64_t)q_len * H, true) : 0;
 }

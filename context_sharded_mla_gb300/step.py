@@ -33,13 +33,14 @@ from . import (DCP_LSE_BASE_2, DCP_LSE_BASE_E, DCP_ROPE_PAIRS, Q4_ROW_BYTES, Lay
                dcp_kv_append, dcp_kv_append_q4, dcp_kv_compact, dcp_kv_compact_q4, dcp_kv_norm_rope_append,
                dcp_kv_norm_rope_append_q4, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
                dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4, dcp_mla_key_weights,
-               dcp_mla_key_weights_q4)
+               dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size, dcp_mla_key_weights_workspace_size_q4)
 
 _CACHES = {"bf16": (576, torch.bfloat16, dcp_kv_append, dcp_mla_decode_partial, dcp_mla_decode_workspace_size),
            "q4": (Q4_ROW_BYTES, torch.uint8, dcp_kv_append_q4, dcp_mla_decode_partial_q4,
                   dcp_mla_decode_workspace_size_q4)}
 _NORMED = {"bf16": dcp_kv_norm_rope_append, "q4": dcp_kv_norm_rope_append_q4}
-_WEIGH = {"bf16": dcp_mla_key_weights, "q4": dcp_mla_key_weights_q4}
+_WEIGH = {"bf16": (dcp_mla_key_weights, dcp_mla_key_weights_workspace_size),
+          "q4": (dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size_q4)}
 _COMPACT = {"bf16": dcp_kv_compact, "q4": dcp_kv_compact_q4}
 
 
@@ -67,6 +68,9 @@ class ShardedMlaDecoder:
         self.o = torch.empty(B, q_len, H, 512, dtype=out_dtype, device=dev)
         self.lse = torch.empty(B, q_len, H, dtype=torch.float32, device=dev)
         ws = workspace_size(layout, self.shard_begin, self.shard_end, B, q_len, H)
+        self._weigh, weigh_size = _WEIGH[cache]
+        if evict:
+            ws = max(ws, weigh_size(q_len, H))
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         if evict:
@@ -96,9 +100,9 @@ class ShardedMlaDecoder:
 
     def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None):
         """After a decode of q: what weight every cached row got from it is added to decay times what it had."""
-        _WEIGH[self.cache](self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
+        self._weigh(self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
                            self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
-                           old_lens=self.weighed, decay=decay, stream=stream)
+                           old_lens=self.weighed, decay=decay, workspace=self.workspace, stream=stream)
         with torch.cuda.stream(stream):
             self.weighed.copy_(seq_lens)
         return self.weights

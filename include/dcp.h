@@ -784,16 +784,22 @@ int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_beg
  * behind a request's last row does not matter, NaN included.
  * Precision: products bf16 by bf16 added in f32; exponents, weights and sums in f32.  The
  * order of the sums is fixed: equal calls give equal bits.
- * Sizes and errors as dcp_mla_decode_partial (page sizes, H, q_len * H <= 65536), without
- * a workspace; DCP_ERR_INVALID also on w_stride < max_pages * P or a bad decay.  Device
- * status DCP_STATUS_TIMEOUT / INTERNAL: the weights are invalid.
+ *   workspace  device scratch of at least dcp_mla_key_weights_workspace_size(q_len, H)
+ *              bytes, 16-byte aligned, or NULL.  With it the work of many query rows over
+ *              few cached ones is cut finer: by query rows too
+ * Sizes and errors as dcp_mla_decode_partial (page sizes, H, q_len * H <= 65536);
+ * DCP_ERR_INVALID also on w_stride < max_pages * P, a bad decay or a misaligned workspace.
+ * Device status DCP_STATUS_TIMEOUT / INTERNAL: the weights are invalid.
  */
 int32_t dcp_mla_key_weights(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
                             int32_t B, int32_t q_len, int32_t H, const void* arena, int64_t pool_pages,
                             const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
                             const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
                             const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
-                            int32_t* status, void* stream);
+                            void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Workspace bytes dcp_mla_key_weights can use for these sizes (0: it needs none). */
+size_t dcp_mla_key_weights_workspace_size(int32_t q_len, int32_t H);
 
 /* The same over a 4-bit cache (k is the row the cache holds). */
 int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, const void* q,
@@ -801,7 +807,8 @@ int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, 
                                const int32_t* block_table, int64_t bt_stride, int64_t max_pages,
                                const int64_t* seq_lens, float scale, int32_t lse_base, const float* lse,
                                const int64_t* old_lens, float decay, float* weights, int64_t w_stride,
-                               int32_t* status, void* stream);
+                               void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+size_t dcp_mla_key_weights_workspace_size_q4(int32_t q_len, int32_t H);
 
 /*
  * dcp_evict_select — the rows that stay when requests go from seq_lens to new_lens.

@@ -77,12 +77,13 @@ class Case:
         self.seq_lens = torch.tensor(lens, dtype=torch.int64, device="cuda")
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
 
-    def run(self, weights, old_lens=None, decay=1.0, q=None, lse=None, stream=None, arena=None, bt=None):
+    def run(self, weights, old_lens=None, decay=1.0, q=None, lse=None, stream=None, arena=None, bt=None, workspace=None):
         dcp = _dcp()
         fn = dcp.dcp_mla_key_weights_q4 if self.q4 else dcp.dcp_mla_key_weights
         fn(self.layout, self.begin, self.end, (self.q if q is None else q).cuda(), self.arena if arena is None else arena,
            self.pool, self.bt if bt is None else bt, self.bt.shape[1], self.seq_lens, SCALE, self.base,
-           (self.lse if lse is None else lse).cuda(), weights, self.status, old_lens=old_lens, decay=decay, stream=stream)
+           (self.lse if lse is None else lse).cuda(), weights, self.status, old_lens=old_lens, decay=decay, stream=stream,
+           workspace=workspace)
         return weights
 
     def fresh(self, seed=9):
@@ -142,6 +143,71 @@ def test_weights(case, q4):
     again = c.run(before.clone(), old, 0.0)
     assert torch.equal(w, again)                               # equal calls, equal bits
     assert int(c.status.item()) == 0
+
+
+SHARED = [  # few tiles for many query rows: pairs that share a tile, several of them inside one
+    ([130], 33, 64, 1, 1, 16, 0, 1, 0),                        # one tile, more row groups than anything else
+    ([3000, 12, 700], 11, 96, 2, 1, 64, 0, 2, 1),               # a request shorter than a tile between two
+    ([9000], 11, 100, 4, 1, 64, 1, 3, 0),                      # five groups of rows; half of the shards
+    ([16000, 16000], 9, 128, 1, 1, 128, 0, 1, 0),              # a tile and a part of one a run
+    ([9700, 9700], 11, 100, 1, 1, 32, 0, 1, 0),                # a tile a run: none is shared
+    ([64] * 9, 61, 40, 1, 1, 8, 0, 1, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+@pytest.mark.parametrize("q4", [False, True])
+def test_shared_tiles(case, q4):
+    """A workspace, its own and dirty, and none (tiles are not shared then); with weights to add to."""
+    dcp = _dcp()
+    c = Case(*SHARED[case], q4)
+    before = c.fresh()
+    old_lens = [max(0, S - c.q_len - b % 3) for b, S in enumerate(c.lens)]
+    old = torch.tensor(old_lens, dtype=torch.int64, device="cuda")
+    w = c.run(before.clone(), old, 0.5)
+    c.check(w, before, old_lens, 0.5)
+    size = (dcp.dcp_mla_key_weights_workspace_size_q4 if q4 else dcp.dcp_mla_key_weights_workspace_size)(c.q_len, c.H)
+    dirty = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(w, c.run(before.clone(), old, 0.5, workspace=dirty))
+    fn = dcp.load_library().dcp_mla_key_weights_q4 if q4 else dcp.load_library().dcp_mla_key_weights
+    alone, q, lse = before.clone(), c.q.cuda(), c.lse.cuda()
+    assert fn(c.layout, c.begin, c.end, q.data_ptr(), len(c.lens), c.q_len, c.H, c.arena.data_ptr(), c.pool, c.bt.data_ptr(),
+              c.bt.stride(0), c.bt.shape[1], c.seq_lens.data_ptr(), SCALE, c.base, lse.data_ptr(), old.data_ptr(), 0.5,
+              alone.data_ptr(), c.wide, None, 0, c.status.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    c.check(alone, before, old_lens, 0.5)
+    assert int(c.status.item()) == 0
+
+
+def test_shared_tiles_on_two_streams_and_in_graphs():
+    """Scratch that the calls take for themselves: two calls at once on streams of their own, two graphs replayed together."""
+    cases = [Case([2000, 300], 12, 96, 2, 1, 64, seed=s) for s in (1, 2)]
+    qs, lses = [c.q.cuda() for c in cases], [c.lse.cuda() for c in cases]
+    for c, k in zip(cases, range(2)):
+        c.q, c.lse = qs[k], lses[k]
+    want = [c.run(c.fresh()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [c.fresh() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, w, s in zip(cases, got, streams):
+            c.run(w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], [c.fresh() for c in cases]
+    for c, w in zip(cases, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(w)
+        graphs.append(g)
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(int(c.status.item()) == 0 for c in cases)
 
 
 @pytest.mark.parametrize("q4", [False, True])

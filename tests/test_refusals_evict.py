@@ -7,7 +7,7 @@ import torch
 
 import context_sharded_mla_gb300 as dcp
 
-INVALID, UNSUPPORTED = -1, -2
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -4
 P = ctypes.c_void_p
 GOOD, BAD, HUGE = dcp.Layout(4, 1, 16), dcp.Layout(4, 3, 16), 2 ** 62
 NAN, INF = float("nan"), float("inf")
@@ -63,9 +63,20 @@ def test_norm_rope_append(lib, kw):
     (dict(B=2 ** 15, st=2 ** 22, mp=2 ** 22, ws=2 ** 40), UNSUPPORTED)])
 def test_key_weights(lib, kw, rc):
     base = dict(sb=0, se=4, q=P(256), B=1, ql=1, H=16, ar=P(256), pp=1, bt=P(256), st=1, mp=1, sl=P(256), sc=0.1, base=0,
-                lse=P(256), old=None, decay=1.0, w=P(256), ws=16, status=P(256), stream=None)
+                lse=P(256), old=None, decay=1.0, w=P(256), ws=16, work=None, wb=0, status=P(256), stream=None)
     for fn in (lib.dcp_mla_key_weights, lib.dcp_mla_key_weights_q4):
         assert call(fn, base, **kw) == rc
+
+
+def test_key_weights_workspace(lib):
+    sizes = (lib.dcp_mla_key_weights_workspace_size, lib.dcp_mla_key_weights_workspace_size_q4)
+    assert [f(4, 128) for f in sizes] == [f(0, 128) for f in sizes] == [f(2, -1) for f in sizes] == [0, 0]
+    assert sizes[0](8, 128) == 0 < sizes[0](1025, 1) and 0 < sizes[1](513, 1)
+    base = dict(sb=0, se=4, q=P(256), B=1, ql=1025, H=1, ar=P(256), pp=1, bt=P(256), st=1, mp=1, sl=P(256), sc=0.1,
+                base=0, lse=P(256), old=None, decay=1.0, w=P(256), ws=16, work=P(256), wb=0, status=P(256), stream=None)
+    for fn, size in zip((lib.dcp_mla_key_weights, lib.dcp_mla_key_weights_q4), sizes):
+        assert call(fn, base, wb=size(1025, 1) - 1) == WORKSPACE
+        assert call(fn, base, work=P(264), wb=size(1025, 1)) == INVALID
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -112,6 +123,8 @@ def test_tensors_that_cannot_be_used(lib, monkeypatch):
         dcp.dcp_mla_key_weights(GOOD, 0, 4, z(2, 1, 16, 576, d=bf), arena, 1, bt, 1, z(2), 0.1, 0, lse, w, st)
     with pytest.raises(ValueError, match="q must be a CUDA tensor"):
         dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w, st)
+    with pytest.raises(ValueError, match="workspace must"):
+        dcp.dcp_mla_key_weights(GOOD, 0, 4, z(1, 1, 16, 576, d=bf), arena, 1, bt, 1, z(1), 0.1, 0, lse, w, st, workspace=z(4))
     with pytest.raises(ValueError, match="seq_lens must be a CUDA tensor"):
         dcp.dcp_evict_select(GOOD, 0, 4, z(1), z(1), 0, 0, w, z(4, 1, 4, d=i32), st)
     with pytest.raises(ValueError, match="kept must"):
