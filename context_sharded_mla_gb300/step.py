@@ -101,8 +101,8 @@ class ShardedMlaDecoder:
     def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None):
         """After a decode of q: what weight every cached row got from it is added to decay times what it had."""
         self._weigh(self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
-                           self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
-                           old_lens=self.weighed, decay=decay, workspace=self.workspace, stream=stream)
+                    self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
+                    old_lens=self.weighed, decay=decay, workspace=self.workspace, stream=stream)
         with torch.cuda.stream(stream):
             self.weighed.copy_(seq_lens)
         return self.weights
