@@ -914,7 +914,7 @@ int32_t weigh(const WeighCall& c) {
   a.box_rows = std::min(c.layout->page_size, kTile);
   a.nbox = kKeys / a.box_rows;
   PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
-  a.npairs = std::min(kernel.max_active_clusters(smem), kMaxPairs);
+  a.npairs = std::min(kernel.max_active_clusters(kSmemBudget), kMaxPairs);  // one CTA an SM, whatever the sizes are
   if (a.npairs < 1) return DCP_ERR_CUDA;
   a.pool_pages = c.pool_pages;
   a.pool_rows = c.pool_pages * c.layout->page_size;
@@ -942,7 +942,7 @@ int32_t weigh(const WeighCall& c) {
     tkv = tq;  // its rows are copied as they are
   else if (!make_tmap(&tkv, c.arena, (uint64_t)a.n_held * a.pool_rows, (uint32_t)a.box_rows))
     return DCP_ERR_CUDA;
-  if (!kernel.ensure_smem(smem)) return DCP_ERR_CUDA;
+  if (!kernel.ensure_smem(kSmemBudget)) return DCP_ERR_CUDA;
   weigh_kernel<kQ4><<<2 * a.npairs, kQ4 ? kThreadsQ4 : kThreads, smem, as_stream(c.stream)>>>(tq, tkv, a);
   if (!ws || a.npairs == 1) return launch_status();
   join_kernel<<<a.npairs - 1, 2 * kKeys, 0, as_stream(c.stream)>>>(a);
