@@ -31,10 +31,10 @@
 //
 // Work: the pair-tiles (2 x 128 rows of one request) of all requests in a row, cut into as
 // many equal runs as there are pairs.  A run's start is found from the lengths by every
-// CTA for itself (a block-wide scan, 1 us), so the call is one launch with no workspace.
+// CTA for itself (a block-wide scan), so the call is one launch with no workspace.
 // Many query rows over few tiles are cut between row groups as well: the pair that begins
 // a tile writes its weights, the others leave their sums in a workspace and a second
-// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 250 us,
+// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 250-260 us,
 // 61 of 128 over 8k 113 -> 60, 4-bit 32 of 128 over 4k 101 -> 36.
 #include "dcp_decode.cuh"
 
@@ -58,11 +58,11 @@ constexpr int kAParts = 5;                 // slots a tile fills: 4 of codes, on
 constexpr int kACol = 256;
 constexpr uint32_t kAllCols = 512;
 
-// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, (7 idle); 4-bit: 8-15 dequantise, two sets of four that take
+// Warps: 0-3 sums, 4 keys in, 5 products, 6 queries in, 7 idle or keys in too; 4-bit: 8-15 dequantise, two sets of four that take
 // slots in turn.  With three 128 us against 117 (32 requests of 32k tokens, 128 heads), with four 135;
 // both sets on every slot, 64 dims each: 128 (a warp's waits for its slots are then twice as many).
 constexpr int kDequantSets = 2;
-constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kDequantWarp = 8;
+constexpr int kKeyWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kKeyWarp2 = 7, kDequantWarp = 8;
 constexpr int kThreads = 256, kThreadsQ4 = kThreads + 128 * kDequantSets;
 
 struct WeighArgs {
@@ -235,15 +235,19 @@ struct Shape {
     return (int32_t)(n < a.max_rows ? n : a.max_rows);
   }
   __device__ int32_t tiles(const WeighArgs& a, int rs) const { return (rows(a, rs) + kKeys - 1) / kKeys; }
+  // Shards before `cut` have `full` + I rows, those after it `full`.
   __device__ int32_t pair_tiles(const WeighArgs& a) const {
-    int32_t t = 0;
-    for (int rs = 0; rs < a.n_held; ++rs) t += tiles(a, rs);
+    if (S < a.q_len) return 0;
+    const int32_t cut = (int32_t)max((int64_t)0, min(div_tiles(rem, a.L.I) - a.shard_begin, (int64_t)a.n_held));
+    const int32_t most = (int32_t)min(full + a.L.I, a.max_rows), least = (int32_t)min(full, a.max_rows);
+    int32_t t = cut * ((most + kKeys - 1) / kKeys);
+    if (cut < a.n_held) t += tiles(a, cut) + (a.n_held - cut - 1) * ((least + kKeys - 1) / kKeys);
     return (t + 1) / 2;
   }
 };
 
 // Where pair p's units (pair-tile, row group) begin.
-__device__ __forceinline__ int64_t run_start(int64_t units, int p, int npairs) { return units * p / npairs; }
+__device__ __forceinline__ int64_t run_start(int64_t units, int p, int npairs) { return div_tiles(units * p, npairs); }
 
 // A pair's run, tile by tile: blocks of pair-tiles of one request, and in a block every row
 // group in turn.  Each role of a CTA walks it for itself.
@@ -407,44 +411,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   const int rank = (int)cluster_ctarank();
   const int pair = blockIdx.x >> 1;
 
-  if (tid == 0) {
-    *abort_s = 0;
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&bars[kFull + i], 2);
-      mbar_init(&bars[kEmpty + i], 1);
-    }
-    for (int i = 0; i < kChunks; ++i) {
-      mbar_init(&bars[kHeldFull + i], 2);
-      mbar_init(&bars[kHeldEmpty + i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[kSFull + i], 1);
-      mbar_init(&bars[kSFree + i], 8);
-    }
-    for (int i = 0; i < kASlots; ++i) {
-      mbar_init(&bars[kAFull + i], 8);
-      mbar_init(&bars[kAEmpty + i], 1);
-    }
-    for (int i = 0; i < kMaxRaw; ++i) {
-      mbar_init(&bars[kRFull + i], 1);
-      mbar_init(&bars[kRFree + i], 4 * kDequantSets);
-    }
+  const int32_t per = (a.B + kBlockThreads - 1) / kBlockThreads;  // requests a thread of the scan below
+  const int32_t b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const int64_t S_first = b0 < b1 ? __ldg(a.seq_lens + b0) : 0;
+  static_assert(kNumBars <= kBlockThreads, "a thread a barrier");
+  if (tid < kNumBars) {
+    const bool two = tid < kEmpty || (tid >= kHeldFull && tid < kHeldEmpty);        // an arrival of each CTA
+    const bool eight = tid >= kSFree && tid < kAEmpty;                               // of four warps of each
+    mbar_init(&bars[tid], two ? 2 : eight ? 8 : tid >= kRFree ? 4 * kDequantSets : 1);
     fence_barrier_init();
   }
+  if (tid == 0) *abort_s = 0;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_base_s)),
                  "r"(kAllCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  __syncwarp();
+  tc_fence_before();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the barriers are set up
   // ---- this pair's run of pair-tiles: a scan over the requests
   {
-    const int32_t per = (a.B + kBlockThreads - 1) / kBlockThreads;
-    const int32_t b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     int32_t mine = 0;
     for (int32_t b = b0; b < b1; ++b) {
       Shape sh;
-      sh.set(a, __ldg(a.seq_lens + b));
+      sh.set(a, b == b0 ? S_first : __ldg(a.seq_lens + b));
       mine += sh.pair_tiles(a);
       if (blockIdx.x == 0) {
         if (sh.S < a.q_len) flag(a.status, DCP_STATUS_BAD_LENGTH);
@@ -477,17 +469,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     const int64_t u0 = run_start((int64_t)total * per_tile, pair, a.npairs);
     const int64_t u1 = run_start((int64_t)total * per_tile, pair + 1, a.npairs);
     if (a.part && blockIdx.x == 0 && tid == 0) *a.units = share ? (int64_t)total * G : 0;
-    const int32_t lo = (int32_t)(per_tile == 1 ? u0 : u0 / G);
+    const int32_t lo = (int32_t)(per_tile == 1 ? u0 : div_tiles(u0, G));
     if (u0 < u1 && before <= lo && lo < before + mine) {
       int32_t b = b0, x = lo - before;
-      for (; b < b1; ++b) {
+      for (; b + 1 < b1; ++b) {  // (with what is left it is the last)
         Shape sh;
         sh.set(a, __ldg(a.seq_lens + b));
         const int32_t n = sh.pair_tiles(a);
         if (x < n) break;
         x -= n;
       }
-      const int32_t hi = (int32_t)(per_tile == 1 ? u1 : (u1 + G - 1) / G);  // tile after the last
+      const int32_t hi = (int32_t)(per_tile == 1 ? u1 : div_tiles(u1 + G - 1, G));  // tile after the last
       start_s[0] = b;
       start_s[1] = x;
       start_s[2] = hi - lo;
@@ -496,8 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
       start_s[5] = per_tile == 1 ? (hi - lo) * G : (int32_t)(u1 - u0);
     }
   }
-  tc_fence_before();
-  cluster_sync();  // barriers of both CTAs are set up, the start is known
+  __syncthreads();  // the start is known
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   const uint32_t lead = mapa_shared(smem_u32(bars), 0);  // the leader's barriers
@@ -510,9 +502,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
                         (uint32_t)a.stages};
   };
 
-  if (warp == kKeyWarp && any) {
+  const bool two = !kQ4 && a.nbox > 4;  // key warps
+  if ((warp == kKeyWarp || (two && warp == kKeyWarp2)) && any) {
     // ------------------------------------------------------------------ keys in
-    // A lane a copy; the next tile's page ids are on their way while this one's copies go out.
+    // A lane a copy; the next tile's page ids are on their way while this one's copies go out.  A warp issues a copy in
+    // 30 ns: where a chunk is 8 or 16 of them (pages of 16 and 8 rows) two warps share the chunks.  16 requests of 32k
+    // tokens with 96 heads: pages of 8 148.5 us by one warp, 97.6 by two; of 16 99.5 and 95.7; of 64 95.5.
     if (lane == 0) prefetch_tmap(&tmap_kv);
     int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
     Slots slots = slots_of(a.keys_held);
@@ -537,6 +532,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         slots.advance();
       } else {
         for (int c = 0; c < kChunks && ok; ++c) {
+          if (two && (slots.uses & 1) != (warp == kKeyWarp2)) {
+            slots.advance();
+            continue;
+          }
           ok = slots.wait(abort_s);
           if (!ok) break;
           if (lane == 0) expect_tx_cluster(slots.full_bar(), __popc(who) * a.box_rows * 128);
