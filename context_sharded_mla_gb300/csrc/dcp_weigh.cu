@@ -34,8 +34,9 @@
 // CTA for itself (a block-wide scan), so the call is one launch with no workspace.
 // Many query rows over few tiles are cut between row groups as well: the pair that begins
 // a tile writes its weights, the others leave their sums in a workspace and a second
-// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 250-260 us,
-// 61 of 128 over 8k 113 -> 60, 4-bit 32 of 128 over 4k 101 -> 36.
+// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 260 us,
+// 61 of 128 over 8k 113 -> 64, 4-bit 32 of 128 over 4k 101 -> 36 (when masked columns took
+// longer; 237, 46 and 34 now).
 #include "dcp_decode.cuh"
 
 namespace {
@@ -70,7 +71,6 @@ struct WeighArgs {
   int32_t shard_begin, n_held;
   int32_t B, q_len, H, R;       // R = q_len * H
   int32_t Rg, ngroups;          // columns a group, groups
-  bool keys_held;               // the keys of a tile stay and the queries pass through the ring
   int32_t stages;               // ring stages, or raw tiles (4-bit)
   int32_t held_bytes, ring_bytes;  // of a held chunk, of a stage
   int32_t box_rows, nbox;       // rows a copy (min(P, 64)), copies a tile
@@ -342,8 +342,10 @@ struct Walk {
   }
   __device__ bool group_begins() const { return i == 0; }
   // the held operand is taken up with this tile and group, is done with after them
-  __device__ bool first(const WeighArgs& a) const { return a.keys_held ? g == g0 : i == 0; }
-  __device__ bool last(const WeighArgs& a) const { return a.keys_held ? g == g1 - 1 : i == nblk - 1; }
+  template <bool kKeysHeld>
+  __device__ bool first() const { return kKeysHeld ? g == g0 : i == 0; }
+  template <bool kKeysHeld>
+  __device__ bool last() const { return kKeysHeld ? g == g1 - 1 : i == nblk - 1; }
 };
 
 // Where copy `box` of the walk's tile starts: its page id, loaded here and looked at later.
@@ -388,7 +390,8 @@ __device__ __forceinline__ void dequant_chunk(const uint32_t (&w)[8], uint32_t f
   }
 }
 
-template <bool kQ4>
+// kKeysHeld: the keys of a tile stay and the queries pass through the ring.
+template <bool kQ4, bool kKeysHeld>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : kThreads, 1)
     weigh_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv, WeighArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -510,12 +513,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     // tokens with 96 heads: pages of 8 148.5 us by one warp, 97.6 by two; of 16 99.5 and 95.7; of 64 95.5.
     if (lane == 0) prefetch_tmap(&tmap_kv);
     int32_t rho = box_row(a, w, lane), page = page_of(a, w, rho);
-    Slots slots = slots_of(a.keys_held);
+    Slots slots = slots_of(kKeysHeld);
     if (kQ4) slots.empty = &bars[kRFree];
     bool ok = true, more = true;
     while (more && ok) {
       const int32_t y = pool_row(a, w.rs, rho, page);
-      if (a.keys_held) w.g = w.g1 - 1;  // the groups between meet the same keys
+      if (kKeysHeld) w.g = w.g1 - 1;  // the groups between meet the same keys
       more = w.next(a, rank);
       rho = more ? box_row(a, w, lane) : -1;
       page = page_of(a, w, rho);
@@ -550,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
   } else if (warp == kQueryWarp && any) {
     // ------------------------------------------------------------------ queries in
     if (lane == 0) prefetch_tmap(&tmap_q);
-    Slots slots = slots_of(!a.keys_held);
+    Slots slots = slots_of(!kKeysHeld);
     bool ok = true, more = true;
     while (more && ok) {
       if (w.group_begins()) {
@@ -581,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
     uint32_t st = 0, ph = 0, hph = 0, j = 0;
     bool ok = true, more = true;
     while (more && ok) {
-      const bool first = w.first(a), last = w.last(a);
+      const bool first = w.first<kKeysHeld>(), last = w.last<kKeysHeld>();
       const uint32_t buf = j & 1, d = tmem + (kQ4 ? 128 : 256) * buf;
       ok = sleep_wait(&bars[kSFree + buf], ((j >> 1) & 1) ^ 1, abort_s);
       for (int c = 0; c < (kQ4 ? kAParts : kChunks) && ok; ++c) {
@@ -592,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         if (!ok) break;
         tc_fence_after();
         const uint64_t hd = held0 + h0 * held_step, rd = ring0 + st * ring_step;
-        const uint64_t qd = a.keys_held ? rd : hd, kd = a.keys_held ? hd : rd;
+        const uint64_t qd = kKeysHeld ? rd : hd, kd = kKeysHeld ? hd : rd;
         const uint32_t kt = tmem + kACol + 64 * st;
         if (one) {
 #pragma unroll
@@ -697,12 +700,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         __syncwarp();
       }
       const uint32_t s_addr = tmem + ((uint32_t)(warp * 32) << 16) + (kQ4 ? 128 : 256) * buf;
-      const bool masked = __any_sync(0xffffffffu, now.col0 > 0);
+      // Some key of the warp is hidden from some rows: its exponentials are cleared by a bit mask, and blocks that see
+      // none are left out.  (Comparing every column with the key's first took longer than the products of a tile, and with
+      // it the pairs that have a request's last keys: the 64-token window 260 us against 237.)
+      const bool hides = __any_sync(0xffffffffu, now.col0 > 0);
       uint64_t sum[2] = {0, 0};
       for (int k0 = 0; k0 < now.ncols; k0 += 32) {
+        uint32_t vis = ~0u;  // columns [k0, k0 + 32) that count for this key: a bit each
         uint32_t r[32];
-        tmem_ld32_sync(s_addr + k0, r);
-        if (!masked && k0 + 32 <= now.ncols) {
+        auto add = [&](bool masked) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float4 l = *reinterpret_cast<const float4*>(lse_s + k0 + 4 * k);
@@ -712,23 +718,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
                                         f2_pack(__float_as_uint(e ? l.z : l.x), __float_as_uint(e ? l.w : l.y)));
               uint32_t x0, x1;
               f2_unpack(x, x0, x1);
-              sum[e] = f2_add(sum[e], f2_pack(__float_as_uint(fast_exp2(__uint_as_float(x0))),
-                                              __float_as_uint(fast_exp2(__uint_as_float(x1)))));
+              float e0 = fast_exp2(__uint_as_float(x0)), e1 = fast_exp2(__uint_as_float(x1));
+              if (masked) {  // after the exponential: a hidden row's NaN does not count
+                e0 = vis >> (4 * k + 2 * e) & 1 ? e0 : 0.f;
+                e1 = vis >> (4 * k + 2 * e + 1) & 1 ? e1 : 0.f;
+              }
+              sum[e] = f2_add(sum[e], f2_pack(__float_as_uint(e0), __float_as_uint(e1)));
             }
           }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float e[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int col = k0 + k + h;
-              const bool in = col >= now.col0 && col < now.ncols;
-              e[h] = in ? fast_exp2(fmaf(__uint_as_float(r[k + h]), c, lse_s[in ? col : 0])) : 0.f;
-            }
-            sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(__float_as_uint(e[0]), __float_as_uint(e[1])));
-          }
+        };
+        if (!hides && k0 + 32 <= now.ncols) {
+          tmem_ld32_sync(s_addr + k0, r);
+          add(false);
+          continue;
         }
+        vis = now.col0 <= k0 ? ~0u : now.col0 >= k0 + 32 ? 0u : ~0u << (now.col0 - k0);
+        if (now.ncols < k0 + 32) vis &= (1u << (now.ncols - k0)) - 1;
+        if (!__any_sync(0xffffffffu, vis)) continue;
+        tmem_ld32_sync(s_addr + k0, r);
+        add(true);
       }
       tc_fence_before();
       __syncwarp();
@@ -851,8 +859,9 @@ size_t workspace_size(int64_t R, bool q4) {
   return R > kShareGroups * (q4 ? 128 : 256) ? kUnitsBytes + kPartAtBytes + kPartBytes : 0;
 }
 
-PairKernel g_bf16(reinterpret_cast<const void*>(&weigh_kernel<false>), kThreads);
-PairKernel g_q4(reinterpret_cast<const void*>(&weigh_kernel<true>), kThreadsQ4);
+PairKernel g_bf16(reinterpret_cast<const void*>(&weigh_kernel<false, false>), kThreads);
+PairKernel g_bf16_groups(reinterpret_cast<const void*>(&weigh_kernel<false, true>), kThreads);
+PairKernel g_q4(reinterpret_cast<const void*>(&weigh_kernel<true, false>), kThreadsQ4);
 
 struct WeighCall {
   const dcp_layout_t* layout;
@@ -902,17 +911,17 @@ int32_t weigh(const WeighCall& c) {
   const int groups = (a.R + most - 1) / most;
   a.Rg = ((a.R + groups - 1) / groups + 31) / 32 * 32;
   a.ngroups = (a.R + a.Rg - 1) / a.Rg;
-  a.keys_held = !kQ4 && a.ngroups > 1;
+  const bool keys_held = !kQ4 && a.ngroups > 1;
   const int q_chunk = a.Rg / 2 * 128;
-  a.held_bytes = a.keys_held ? kStageBytes : q_chunk;
-  a.ring_bytes = kQ4 ? kRawTile : a.keys_held ? q_chunk : kStageBytes;
+  a.held_bytes = keys_held ? kStageBytes : q_chunk;
+  a.ring_bytes = kQ4 ? kRawTile : keys_held ? q_chunk : kStageBytes;
   a.stages = (int32_t)(kSmemBudget - smem_of(a.held_bytes, 0, 0, kQ4).total) / a.ring_bytes;
   a.stages = std::min(a.stages, kQ4 ? kMaxRaw : kMaxStages);
   const size_t smem = smem_of(a.held_bytes, a.stages, a.ring_bytes, kQ4).total;
   a.block = kQ4 ? kBlockQ4 : 1;
   a.box_rows = std::min(c.layout->page_size, kTile);
   a.nbox = kKeys / a.box_rows;
-  PairKernel& kernel = kQ4 ? g_q4 : g_bf16;
+  PairKernel& kernel = kQ4 ? g_q4 : keys_held ? g_bf16_groups : g_bf16;
   a.npairs = std::min(kernel.max_active_clusters(kSmemBudget), kMaxPairs);  // one CTA an SM, whatever the sizes are
   if (a.npairs < 1) return DCP_ERR_CUDA;
   a.pool_pages = c.pool_pages;
@@ -942,7 +951,8 @@ int32_t weigh(const WeighCall& c) {
   else if (!make_tmap(&tkv, c.arena, (uint64_t)a.n_held * a.pool_rows, (uint32_t)a.box_rows))
     return DCP_ERR_CUDA;
   if (!kernel.ensure_smem(kSmemBudget)) return DCP_ERR_CUDA;
-  weigh_kernel<kQ4><<<2 * a.npairs, kQ4 ? kThreadsQ4 : kThreads, smem, as_stream(c.stream)>>>(tq, tkv, a);
+  const auto run = kQ4 ? weigh_kernel<true, false> : keys_held ? weigh_kernel<false, true> : weigh_kernel<false, false>;
+  run<<<2 * a.npairs, kQ4 ? kThreadsQ4 : kThreads, smem, as_stream(c.stream)>>>(tq, tkv, a);
   if (!ws || a.npairs == 1) return launch_status();
   join_kernel<<<a.npairs - 1, 2 * kKeys, 0, as_stream(c.stream)>>>(a);
   return launch_status(2);
