@@ -15,7 +15,8 @@ Functions (same names as the C ABI):
   dcp_kv_read_q4, dcp_mla_decode_partial_q4, dcp_mla_decode_workspace_size_q4,
   dcp_block_tables, dcp_q_norm_rope, dcp_kv_norm_rope_append, dcp_kv_norm_rope_append_q4,
   dcp_mla_key_weights, dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size,
-  dcp_mla_key_weights_workspace_size_q4, dcp_evict_select, dcp_kv_compact, dcp_kv_compact_q4
+  dcp_mla_key_weights_workspace_size_q4, dcp_key_weights_mark, dcp_evict_select, dcp_kv_compact,
+  dcp_kv_compact_q4
 """
 
 from __future__ import annotations
@@ -37,7 +38,7 @@ __all__ = [
     "dcp_mla_decode_workspace_size_q4", "dcp_block_tables", "Q4_ROW_BYTES",
     "dcp_q_norm_rope", "dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4", "dcp_mla_key_weights",
     "dcp_mla_key_weights_q4", "dcp_mla_key_weights_workspace_size", "dcp_mla_key_weights_workspace_size_q4",
-    "dcp_evict_select", "dcp_kv_compact", "dcp_kv_compact_q4",
+    "dcp_key_weights_mark", "dcp_evict_select", "dcp_kv_compact", "dcp_kv_compact_q4",
     "DCP_LSE_BASE_E", "DCP_LSE_BASE_2", "DCP_F32", "DCP_BF16", "DCP_ROPE_PAIRS", "DCP_ROPE_HALVES", "STATUS_BITS",
 ]
 
@@ -103,6 +104,7 @@ _SIGNATURES = {
     "dcp_mla_decode_workspace_size_q4": (_SZ, [_LP, _I32, _I32, _I32, _I32, _I32]),
     "dcp_block_tables": (_I32, [_LP, _I32, _P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dcp_q_norm_rope": (_I32, [_I64, _I32, _P, _I64, _P, _P, _I32, _F, _P, _I32, _P, _P, _P]),
+    "dcp_key_weights_mark": (_I32, [_LP, _I32, _I32, _I32, _P, _P, _P, _I64, _P]),
     "dcp_evict_select": (_I32, [_LP, _I32, _I32, _I32, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P]),
 }
 for _name in ("dcp_kv_norm_rope_append", "dcp_kv_norm_rope_append_q4"):
@@ -747,18 +749,31 @@ dcp_mla_key_weights = _key_weights(
     "dcp_mla_key_weights", 576, torch.bfloat16, dcp_mla_key_weights_workspace_size, 1024,
     """weights [shards, B, >= max_pages * P] f32: to every cached row the softmax weight that the queries q [B, q_len, H,
     576] give it under their merged lse [B, q_len, H], summed over them, is added; rows at positions below old_lens (int64
-    [B]; None: 0) keep decay times what they had, the others start from 0.  workspace: uint8 of
+    [B]; None: 0) keep decay times what they had, the others, and those at +inf, start from 0.  workspace: uint8 of
     dcp_mla_key_weights_workspace_size(q_len, H) bytes; None: allocated for the call.""")
 dcp_mla_key_weights_q4 = _key_weights(
     "dcp_mla_key_weights_q4", Q4_ROW_BYTES, torch.uint8, dcp_mla_key_weights_workspace_size_q4, 512,
     """dcp_mla_key_weights over a 4-bit arena [shards, pool_pages*P, 416] uint8.""")
 
 
+def dcp_key_weights_mark(layout, shard_begin, shard_end, from_lens, seq_lens, weights, stream=None):
+    """Rows at positions [from_lens[b], seq_lens[b]) (int64 [B]) have no weight yet: theirs in weights [shards, B, rows] f32
+    becomes +inf, which dcp_evict_select keeps before any other number and dcp_mla_key_weights takes for none."""
+    dev = torch.cuda.current_device()
+    B = seq_lens.numel()
+    rc = load_library().dcp_key_weights_mark(
+        layout, shard_begin, shard_end, B, _at(from_lens, "from_lens", torch.int64, (B,), dev),
+        _at(seq_lens, "seq_lens", torch.int64, (B,), dev),
+        _at(weights, "weights", torch.float32, (shard_end - shard_begin, B, _unit_rows(weights, "weights")), dev),
+        weights.shape[2], _raw_stream(stream, dev))
+    _check("dcp_key_weights_mark", rc)
+
+
 def dcp_evict_select(layout, shard_begin, shard_end, seq_lens, new_lens, sinks, recent, weights, kept, status,
                      stream=None):
     """kept [shards, B, rows] int32: the local rows (ascending) that each shard keeps when requests go from seq_lens to
     new_lens (int64 [B]): those below position `sinks`, of the last `recent` positions, and the heaviest of weights
-    [shards, B, rows] f32."""
+    [shards, B, rows] f32.  Rows that have none yet are marked first (dcp_key_weights_mark)."""
     dev = torch.cuda.current_device()
     B = seq_lens.numel()
     n = shard_end - shard_begin

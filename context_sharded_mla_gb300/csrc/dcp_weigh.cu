@@ -755,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQ4 ? kThreadsQ4 : k
         a.part_at[k] = there ? now.at : -1;
         a.part[k] = s;
       } else if (there) {
-        a.weights[now.at] = a.decay * now.old + s;
+        a.weights[now.at] = (now.old == INFINITY ? 0.f : a.decay * now.old) + s;  // +inf: marked as having none
       }
       ++j;
     }

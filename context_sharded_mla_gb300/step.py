@@ -31,7 +31,7 @@ import torch
 
 from . import (DCP_LSE_BASE_2, DCP_LSE_BASE_E, DCP_ROPE_PAIRS, Q4_ROW_BYTES, Layout, dcp_block_tables, dcp_evict_select,
                dcp_kv_append, dcp_kv_append_q4, dcp_kv_compact, dcp_kv_compact_q4, dcp_kv_norm_rope_append,
-               dcp_kv_norm_rope_append_q4, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
+               dcp_kv_norm_rope_append_q4, dcp_key_weights_mark, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
                dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4, dcp_mla_key_weights,
                dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size, dcp_mla_key_weights_workspace_size_q4)
 
@@ -77,8 +77,10 @@ class ShardedMlaDecoder:
             rows = max_pages * layout.page_size
             self.weights = torch.zeros(n, B, rows, dtype=torch.float32, device=dev)
             self.kept = torch.full((n, B, rows), -1, dtype=torch.int32, device=dev)
-            # requests' positions below it have a weight (set an entry to 0 when its slot gets another request)
+            # requests' positions below it have a weight, or the mark of none (lower an entry when its request loses
+            # tokens from the end, to 0 when its slot gets another request)
             self.weighed = torch.zeros(B, dtype=torch.int64, device=dev)
+            self._where = torch.zeros(B, dtype=torch.bool, device=dev)
 
     def append(self, kv_new, pos, req, block_table, stream=None):
         """Place T new latent rows (kv_new [T, 576] bf16 at positions pos of requests req):
@@ -99,25 +101,35 @@ class ShardedMlaDecoder:
                             rope_style=rope_style, rope_pos=rope_pos, stream=stream)
 
     def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None):
-        """After a decode of q: what weight every cached row got from it is added to decay times what it had."""
+        """After a decode of q: what weight every cached row got from it is added to decay times what it had.  A request
+        with fewer tokens than q has gets none (DCP_STATUS_BAD_LENGTH)."""
         self._weigh(self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
                     self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
                     old_lens=self.weighed, decay=decay, workspace=self.workspace, stream=stream)
         with torch.cuda.stream(stream):
-            self.weighed.copy_(seq_lens)
+            if self.q_len == 1:
+                self.weighed.copy_(seq_lens)
+            else:
+                torch.ge(seq_lens, self.q_len, out=self._where)
+                torch.minimum(self.weighed, seq_lens, out=self.weighed)
+                torch.where(self._where, seq_lens, self.weighed, out=self.weighed)
         return self.weights
 
     def evict(self, block_table, seq_lens, new_lens, sinks=0, recent=0, stream=None):
         """Every shard keeps its share of new_lens positions of each request: the first `sinks`, the last `recent` and
-        the heaviest, moved to the front.  The tables, which still hold the old lengths, shrink afterwards
-        (BlockTables.update(new_lens)).  Returns kept: the rows that stayed."""
+        the heaviest, moved to the front.  Rows that no weigh has seen stay before those that have a weight.  The tables,
+        which still hold the old lengths, shrink afterwards (BlockTables.update(new_lens)).  Returns kept: the rows that
+        stayed."""
+        dcp_key_weights_mark(self.layout, self.shard_begin, self.shard_end, self.weighed, seq_lens, self.weights, stream)
         dcp_evict_select(self.layout, self.shard_begin, self.shard_end, seq_lens, new_lens, sinks, recent, self.weights,
                          self.kept, self.status, stream)
         _COMPACT[self.cache](self.layout, self.shard_begin, self.shard_end, self.kept, new_lens, block_table,
                              self.max_pages, self.arena, self.pool_pages, self.status, weights=self.weights,
                              stream=stream)
-        with torch.cuda.stream(stream):
-            torch.minimum(self.weighed, new_lens, out=self.weighed)
+        with torch.cuda.stream(stream):  # every row that is left has a weight or the mark; a refused request keeps its length
+            torch.lt(new_lens, 0, out=self._where)
+            torch.minimum(seq_lens, new_lens, out=self.weighed)
+            torch.where(self._where, seq_lens, self.weighed, out=self.weighed)
         return self.kept
 
     def partial(self, q, block_table, seq_lens, stream=None):

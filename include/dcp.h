@@ -33,6 +33,7 @@
  *      dcp_kv_norm_rope_append (_q4)  the same for the latent rows, into the shards' pools
  * and, to shorten a cache by what its rows weigh,
  *  14. dcp_mla_key_weights (_q4)  the attention weight of every cached row, accumulated
+ *      dcp_key_weights_mark    rows that have no weight yet, before a selection
  *  15. dcp_evict_select        the rows each shard keeps of each request
  *  16. dcp_kv_compact (_q4)    kept rows moved to the front of their shard, in place
  *
@@ -772,7 +773,8 @@ int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_beg
  *              -inf (it saw nothing) adds nothing
  *   old_lens   int64[B] or NULL: rows at positions below it have a weight to add to, those
  *              from it on (new since the last call) start from 0.  NULL: every row starts
- *              from 0
+ *              from 0.  A weight of +infinity below old_lens (dcp_key_weights_mark) is
+ *              none: that row starts from 0 too
  *   decay      factor on the weights there are, finite and not negative; with 0 they are
  *              not read
  *   weights    f32[shard_end - shard_begin, B, w_stride], w_stride >= max_pages * P; entries
@@ -811,6 +813,22 @@ int32_t dcp_mla_key_weights_q4(const dcp_layout_t* layout, int32_t shard_begin, 
 size_t dcp_mla_key_weights_workspace_size_q4(int32_t q_len, int32_t H);
 
 /*
+ * dcp_key_weights_mark — rows that have no weight yet, before dcp_evict_select: the weight
+ * of every held row at a position in [from_lens[b], seq_lens[b]) becomes +infinity, so that
+ * no row is dropped for what an earlier one left there.  Those rows stay before any row with
+ * a finite weight; dcp_kv_compact moves the mark with the row; dcp_mla_key_weights lets such
+ * a row start from 0.
+ *   from_lens, seq_lens  int64[B] (device); a negative one counts as 0
+ *   weights              f32[shard_end - shard_begin, B, w_stride]; rows past w_stride are
+ *                        left out
+ * Errors: DCP_ERR_INVALID for a bad layout or shard range, B < 1, w_stride < 1 or a null
+ * pointer.
+ */
+int32_t dcp_key_weights_mark(const dcp_layout_t* layout, int32_t shard_begin, int32_t shard_end, int32_t B,
+                             const int64_t* from_lens, const int64_t* seq_lens, float* weights, int64_t w_stride,
+                             void* stream);
+
+/*
  * dcp_evict_select — the rows that stay when requests go from seq_lens to new_lens.
  *
  * For held shard r and request b, n = count_r(seq_lens[b]) rows become
@@ -820,7 +838,9 @@ size_t dcp_mla_key_weights_workspace_size_q4(int32_t q_len, int32_t H);
  * m of that sequence stay.
  *   seq_lens, new_lens  int64[B] (device), 0 <= new_lens[b] <= seq_lens[b]
  *   sinks, recent       positions, >= 0
- *   weights             f32[shard_end - shard_begin, B, w_stride] (dcp_mla_key_weights)
+ *   weights             f32[shard_end - shard_begin, B, w_stride] (dcp_mla_key_weights); every
+ *                       row below seq_lens is ranked by what lies there, so rows since the
+ *                       last weights are marked first (dcp_key_weights_mark)
  *   kept  (out)         int32[shard_end - shard_begin, B, kept_stride]: the rows that
  *                       stay, ascending, in entries [0, m); the others are left as they are
  * A request with new_lens outside [0, seq_lens], or a unit with n > w_stride or
