@@ -334,11 +334,18 @@ def _rows(t, name, width):
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape[-1] != width or t.stride(-1) != 1:
         raise ValueError(f"{name} must be [..., {width}] with a contiguous last dim")
-    row = t.stride(-2) if t.dim() >= 2 else width
-    for i in range(t.dim() - 2):
-        if t.shape[i + 1] > 1 and t.stride(i) != t.stride(i + 1) * t.shape[i + 1]:
+    if t.numel() == 0:
+        return width
+    row = span = None   # of the dimensions so far, from the last; the stride of one of extent 1 says nothing
+    for n, step in zip(t.shape[-2::-1], t.stride()[-2::-1]):
+        if n == 1:
+            continue
+        if row is None:
+            row = step
+        elif step != span:
             raise ValueError(f"{name}'s rows must be equally strided")
-    return row
+        span = step * n
+    return width if row is None else row
 
 
 def dcp_absorb_q(q_nope, q_pe, w_kc, q, status=None, stream=None):
