@@ -67,10 +67,14 @@ class ShardedMlaDecoder:
         self.lse_part = torch.empty(n, B, q_len, H, dtype=torch.float32, device=dev)
         self.o = torch.empty(B, q_len, H, 512, dtype=out_dtype, device=dev)
         self.lse = torch.empty(B, q_len, H, dtype=torch.float32, device=dev)
+        self._whole = n == layout.n_shards
+        self._merged_part = False   # self.lse is of the held shards alone
+        if not self._whole:
+            self.lse.fill_(float("nan"))    # until merged, or filled by the caller
         ws = workspace_size(layout, self.shard_begin, self.shard_end, B, q_len, H)
-        self._weigh, weigh_size = _WEIGH[cache]
+        self._weigh, self._weigh_size = _WEIGH[cache]
         if evict:
-            ws = max(ws, weigh_size(q_len, H))
+            ws = max(ws, self._weigh_size(q_len, H))
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         if evict:
@@ -100,17 +104,27 @@ class ShardedMlaDecoder:
                             self.arena, self.pool_pages, self.status, gamma=gamma, eps=eps, inv_freq=inv_freq,
                             rope_style=rope_style, rope_pos=rope_pos, stream=stream)
 
-    def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None):
+    def weigh(self, q, block_table, seq_lens, decay=1.0, stream=None, lse=None):
         """After a decode of q: what weight every cached row got from it is added to decay times what it had.  A request
-        with fewer tokens than q has gets none (DCP_STATUS_BAD_LENGTH)."""
+        with fewer tokens than q has gets none (DCP_STATUS_BAD_LENGTH).
+
+        lse [B, q_len, H] is the merged one of q over all shards, in the decoder's base; None: self.lse, as decode leaves
+        it where all shards are held.  With lse, q may have any number of tokens (a prompt's last ones, say)."""
+        if lse is None:
+            if self._merged_part:
+                raise ValueError(f"self.lse is merged over shards [{self.shard_begin}, {self.shard_end}) of "
+                                 f"{self.layout.n_shards} alone; pass lse, the one merged over all of them")
+            lse = self.lse
+        q_len = q.shape[1]
+        fits = q_len <= self.q_len or self._weigh_size(q_len, self.H) <= self.workspace.numel()
         self._weigh(self.layout, self.shard_begin, self.shard_end, q, self.arena, self.pool_pages, block_table,
-                    self.max_pages, seq_lens, self.scale, self.lse_base, self.lse, self.weights, self.status,
-                    old_lens=self.weighed, decay=decay, workspace=self.workspace, stream=stream)
+                    self.max_pages, seq_lens, self.scale, self.lse_base, lse, self.weights, self.status,
+                    old_lens=self.weighed, decay=decay, workspace=self.workspace if fits else None, stream=stream)
         with torch.cuda.stream(stream):
-            if self.q_len == 1:
+            if q_len == 1:
                 self.weighed.copy_(seq_lens)
             else:
-                torch.ge(seq_lens, self.q_len, out=self._where)
+                torch.ge(seq_lens, q_len, out=self._where)
                 torch.minimum(self.weighed, seq_lens, out=self.weighed)
                 torch.where(self._where, seq_lens, self.weighed, out=self.weighed)
         return self.weights
@@ -140,6 +154,7 @@ class ShardedMlaDecoder:
 
     def merge(self, stream=None):
         n = self.shard_end - self.shard_begin
+        self._merged_part = not self._whole
         dcp_lse_merge(self.o_part.view(n, -1, 512), self.lse_part.view(n, -1), self.lse_base,
                       self.o.view(-1, 512), self.lse.view(-1), stream)
 

@@ -751,8 +751,10 @@ int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_beg
  * steps, dcp_evict_select picks the rows that stay, dcp_kv_compact moves them to the front
  * and dcp_block_tables (from the old lengths to the new ones) gives the freed pages back.
  * Every shard keeps count_r(new length) of its OWN rows ("PCP / DCP：计算、KV 布局与块
- * 轮转", section 6, local_len): no row changes shard, so a group of GPUs needs no exchange,
- * and what is left is laid out as any request of that length.  Afterwards a position is a
+ * 轮转", section 6, local_len): no row changes shard, so that a group of GPUs needs no exchange
+ * to select and move, and what is left is laid out as any request of that length.  (To weigh, each
+ * of them needs the queries of all heads and their lse merged over all shards; after an exchange
+ * by head slice a GPU has that of its own heads only, and the caller gathers the others'.)  Afterwards a position is a
  * place in the shortened cache; the rows keep the rotation of their place in the text.
  */
 
