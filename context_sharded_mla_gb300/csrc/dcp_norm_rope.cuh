@@ -22,8 +22,7 @@ struct Turn {
 __device__ __forceinline__ Turn turn_of(uint64_t step, int64_t pos) {
   const uint64_t f = step * (uint64_t)pos;  // modulo a turn
   Turn t;
-  // [-pi, pi], where the hardware's sine and cosine are within 2^-21: their rounding to bf16 is 2^-8
-  __sincosf((float)(int32_t)(f >> 32) * 1.4629180792671596e-9f, &t.s, &t.c);  // pi 2^-31
+  sincospif((float)(int32_t)(f >> 32) * 0x1p-31f, &t.s, &t.c);  // half turns in [-1, 1], rounded once: 2^-23 rad
   return t;
 }
 

@@ -689,8 +689,8 @@ int32_t dcp_block_tables(const dcp_layout_t* layout, int32_t B, int64_t* seq_len
  *             or (i, i + 32) with DCP_ROPE_HALVES, turns by position * inv_freq[i]:
  *             (a, b) -> (a cos - b sin, a sin + b cos).  inv_freq f32[32], finite, in
  *             radians a position; NULL: no rotation.  The angle is taken modulo a turn
- *             in 64 bits: off by at most 2^-52 of itself + 2^-22, whatever the position;
- *             its sine and cosine are within 2^-21
+ *             in 64 bits: off by at most 2^-52 of itself + 2^-62 a position + 2^-23; its
+ *             sine and cosine are within a last place of f32
  * Both are computed in f32 and rounded to bf16 once, at the end (the 4-bit append
  * quantises that bf16 row).
  */
