@@ -48,9 +48,13 @@ constexpr int kMaxStages = 12;
 constexpr int kBlockQ4 = 8;                // 4-bit: pair-tiles of a block when there is more than one row group
 constexpr int kRawTile = kKeys * kQ4RowBytes;
 constexpr int kMaxRaw = 3;
-// The tensor core cuts its running sum off toward zero at each of the 36 steps of a score instead of rounding it: half
-// a last place of the sum so far, a relative loss between 0 and 36 * 2^-24 that averages 16 * 2^-25 over the scores that
-// carry the weights (measured: weights 1.5e-6 low without this, 1e-7 off with it).
+// The tensor core cuts its running sum off toward zero at each of the 36 steps of a score instead of rounding it.  Of a
+// bf16 score that loses, in 2^-24 of it: 9 to 10 where queries and rows are dense, 20 where all products have one sign, under
+// 1 with few terms (measured against fp64).  8 are made good: a dense query row's weights then sum to one within 2 against fp64
+// and within 5 under the decode's own lse (the decode adds two sums of 18 steps and loses half as much); without that 10 and
+// 5, with the difference to the decode alone (5) 5 and 1.  At worst, one sign or few terms: 12 and 8; without 20 and 11.
+// 4-bit values have few bits, of which the sums cut fewer: dense 4, within 2 of the decode's.  Left as it is (made good
+// like the bf16 ones they summed to 4 to 5 too much against fp64 and 7 under the decode's lse).
 constexpr double kTruncation = 0x1p-21;
 // 4-bit: operand slots of 128 dims (64 columns) in TMEM.  A slot of 64 dims costs its wait, its commit and its
 // products' issue more than the products take at 128 rows.
@@ -932,7 +936,7 @@ int32_t weigh(const WeighCall& c) {
   a.bt_stride = c.bt_stride;
   a.max_pages = c.max_pages;
   a.seq_lens = c.seq_lens;
-  a.scale_log2 = (float)((double)c.scale * 1.4426950408889634 * (1.0 + kTruncation));
+  a.scale_log2 = kQ4 ? c.scale * kLog2e : (float)((double)c.scale * 1.4426950408889634 * (1.0 + kTruncation));
   a.base2 = c.lse_base == DCP_LSE_BASE_2;
   a.lse = c.lse;
   a.old_lens = c.old_lens;

@@ -786,8 +786,10 @@ int32_t dcp_kv_norm_rope_append_q4(const dcp_layout_t* layout, int32_t shard_beg
  * flagged (BAD_PAGE_ID) and worked on as far as the table goes.  A NaN in a cached row
  * makes that row's weight NaN; a NaN in a query row or its lse that of every row it sees.  What lies
  * behind a request's last row does not matter, NaN included.
- * Precision: products bf16 by bf16 added in f32; exponents, weights and sums in f32.  The
- * order of the sums is fixed: equal calls give equal bits.
+ * Precision: products bf16 by bf16 added in f32; exponents, weights and sums in f32.  Under the
+ * lse of this library's decode and merge a query row's weights sum to one but for the roundings
+ * and some 2^-21 of its score, which the tensor core's sums cut off or a correction for that
+ * adds (bf16 cache).  The order of the sums is fixed: equal calls give equal bits.
  *   workspace  device scratch of at least dcp_mla_key_weights_workspace_size(q_len, H)
  *              bytes, 16-byte aligned, or NULL.  With it the work of many query rows over
  *              few cached ones is cut finer: by query rows too
