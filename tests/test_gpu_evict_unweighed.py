@@ -154,3 +154,21 @@ def test_marked_rows_start_from_nothing(q4, lens, q_len, H):
     for decay in (1.0, 0.5, 0.0):
         w = c.run(marked.clone(), old, decay)
         assert torch.equal(w, c.run(zeroed.clone(), old, decay)) and not torch.isinf(w).any()
+
+
+def test_refused_requests_keep_their_rows_and_weights():
+    r = Tracked("bf16", seed=8)
+    r.append([90, 40, 61])
+    r.weigh()
+    r.append([91, 42, 63])
+    before, w = [r.rows(b, S) for b, S in enumerate(r.lens)], r.dec.weights.clone()
+    r.dec.evict(r.tables.block_table, r.tables.seq_lens, torch.tensor([-1, 43, 63], device="cuda"), 2, 3)
+    assert r.dec.status_bits() == 16 and r.dec.weighed.tolist() == [91, 42, 63]
+    for b, (S, had) in enumerate(zip(r.lens, [90, 40, 61])):
+        assert np.array_equal(r.rows(b, S), before[b])
+        own, row = (torch.from_numpy(x).cuda() for x in r.at(S))
+        assert torch.equal(r.dec.weights[own[:had], b, row[:had]], w[own[:had], b, row[:had]])
+        assert torch.isinf(r.dec.weights[own[had:], b, row[had:]]).all()
+    r.dec.status.zero_()
+    r.weigh()                                   # and go on from there
+    assert r.dec.status_bits() == 0
