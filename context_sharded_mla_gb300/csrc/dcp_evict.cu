@@ -10,9 +10,10 @@
 // that compete is found digit by digit: 12 bits first (one histogram a CTA; weights of one
 // magnitude share their first bits, but few lanes of a warp the first 12), the others among
 // the keys of that bin alone.  Rows are then written in order: ballots, and a sum over the
-// warps.  Only whole numbers are added, so the result depends on no order.  Bound by its
-// instructions and block barriers: 512 units of 16384 rows (33 MB) take 28 us, 1.2 TB/s; a
-// unit of a few rows 5 us.
+// warps.  Only whole numbers are added, so the result depends on no order.  Bound by
+// latency: two CTAs an SM go from load to histogram to scan to list to write, a block
+// barrier between each, with no load of a next unit under way (53 % of the issue slots, 13 %
+// of DRAM).  512 units of 16384 rows (33 MB) take 28 us, 1.2 TB/s; a unit of a few rows 5 us.
 //
 // mark_kernel: rows that no query has weighed get the weight +infinity, which the
 // selection keeps before any other number and the next weights take for none.  A launch and

@@ -72,9 +72,9 @@ struct RowArgs {
   const int64_t* rope_pos;
 };
 
-// Tokens whose loads are in flight before their stores, 32768 tokens in a captured graph: 13.5 us with 2 and four blocks
-// an SM; when that took 14.9 it was 16.1 with 4 and two blocks, 18.4 with 3 and three, 16.0 with 1 and five.  Eight rows a
-// warp copied asynchronously into shared memory: 16.6.
+// Tokens whose loads are in flight before their stores, 32768 tokens in a captured graph: 14.4 us with 2 and four blocks
+// an SM (4-bit 20); when that took 14.9 it was 16.1 with 4 and two blocks, 18.4 with 3 and three, 16.0 with 1 and five.
+// Eight rows a warp copied asynchronously into shared memory: 16.6.
 constexpr int kRowAhead = 2;
 
 // A bf16 row's first 512 dims: lane l has dims [8 l, 8 l + 8) and [256 + 8 l, 256 + 8 l + 8).

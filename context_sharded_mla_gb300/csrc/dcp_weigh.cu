@@ -34,9 +34,8 @@
 // CTA for itself (a block-wide scan), so the call is one launch with no workspace.
 // Many query rows over few tiles are cut between row groups as well: the pair that begins
 // a tile writes its weights, the others leave their sums in a workspace and a second
-// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 278 -> 260 us,
-// 61 of 128 over 8k 113 -> 64, 4-bit 32 of 128 over 4k 101 -> 36 (when masked columns took
-// longer; 237, 46 and 34 now).
+// launch adds them, in order.  64 queries of 96 heads over 2 x 32k tokens 249 -> 218 us,
+// 61 of 128 over 8k 81 -> 47, 4-bit 32 of 128 over 4k 99 -> 34.
 #include "dcp_decode.cuh"
 
 namespace {
