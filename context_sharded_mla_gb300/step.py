@@ -31,8 +31,8 @@ import torch
 
 from . import (DCP_LSE_BASE_2, DCP_LSE_BASE_E, DCP_ROPE_PAIRS, Q4_ROW_BYTES, Layout, dcp_block_tables, dcp_evict_select,
                dcp_kv_append, dcp_kv_append_q4, dcp_kv_compact, dcp_kv_compact_q4, dcp_kv_norm_rope_append,
-               dcp_kv_norm_rope_append_q4, dcp_key_weights_mark, dcp_lse_merge, dcp_mla_decode_partial, dcp_mla_decode_partial_q4,
-               dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4, dcp_mla_key_weights,
+               dcp_kv_norm_rope_append_q4, dcp_key_weights_mark, dcp_lse_merge, dcp_mla_decode_partial,
+               dcp_mla_decode_partial_q4, dcp_mla_decode_workspace_size, dcp_mla_decode_workspace_size_q4, dcp_mla_key_weights,
                dcp_mla_key_weights_q4, dcp_mla_key_weights_workspace_size, dcp_mla_key_weights_workspace_size_q4)
 
 _CACHES = {"bf16": (576, torch.bfloat16, dcp_kv_append, dcp_mla_decode_partial, dcp_mla_decode_workspace_size),
@@ -131,9 +131,9 @@ class ShardedMlaDecoder:
 
     def evict(self, block_table, seq_lens, new_lens, sinks=0, recent=0, stream=None):
         """Every shard keeps its share of new_lens positions of each request: the first `sinks`, the last `recent` and
-        the heaviest, moved to the front.  Rows that no weigh has seen stay before those that have a weight.  The tables,
-        which still hold the old lengths, shrink afterwards (BlockTables.update(new_lens)).  Returns kept: the rows that
-        stayed."""
+        the heaviest, moved to the front.  Rows that no weigh has seen stay before those that have a weight (theirs is +inf
+        until the next weigh).  The tables, which still hold the old lengths, shrink afterwards
+        (BlockTables.update(new_lens)).  Returns kept: the rows that stayed."""
         dcp_key_weights_mark(self.layout, self.shard_begin, self.shard_end, self.weighed, seq_lens, self.weights, stream)
         dcp_evict_select(self.layout, self.shard_begin, self.shard_end, seq_lens, new_lens, sinks, recent, self.weights,
                          self.kept, self.status, stream)
